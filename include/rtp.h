@@ -464,9 +464,156 @@ int rtp_tp_mlp_sp(int P, int64_t M, int64_t K, int64_t F, int64_t N, const void*
 int rtp_tp_mlp_noalloc(int P, int64_t M, int64_t K, int64_t F, int64_t N, const void* X, const void* const* A_shards,
                        const void* const* B_shards, float* Z, rtp_stream stream);
 
+/* Activations of rtp_tp_linear and rtp_tp_glu: identity; x Phi(x) (erf); its tanh
+ * form x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2; x / (1 + e^-x); max(x, 0). */
+typedef enum {
+    RTP_ACT_NONE = 0,
+    RTP_ACT_GELU = 1,
+    RTP_ACT_GELU_TANH = 2,
+    RTP_ACT_SILU = 3,
+    RTP_ACT_RELU = 4
+} rtp_act;
+
+/* How a linear layer's weight [K, N] is split over the ranks (ColossalAI "1D
+ * tensor parallelism" page, sections 2 and 2.1). */
+enum { RTP_SPLIT_COLUMN = 0, RTP_SPLIT_ROW = 1 };
+
+/*
+ * Tensor-parallel linear layer on P virtual ranks with bias, activation and
+ * residual in the product's epilogue (ColossalAI "1D tensor parallelism" page,
+ * sections 2 and 2.1: column-parallel and row-parallel layers; the bias and the
+ * residual are added where the page's layer ends, once, after the ranks are
+ * summed).
+ *   RTP_SPLIT_COLUMN  out_i = act(X W_i + b_i) + R_i     W_i [K, N/P]
+ *       X: 1 pointer [M, K]; bias, residual, H, out: P pointers [N/P], [M, N/P]
+ *   RTP_SPLIT_ROW     out = act(sum_i X_i W_i + b) + R   W_i [K/P, N]
+ *       X: P pointers [M, K/P]; bias, residual, H, out: 1 pointer [N], [M, N]
+ *   X, W_shards, bias, residual  bf16 device pointers; bias and residual may be
+ *             NULL (none)
+ *   act       an rtp_act
+ *   H         NULL, or bf16 buffers that receive the pre-activation (product
+ *             plus bias, rounded once) for rtp_tp_linear_backward; the
+ *             activation itself is of the float32 value
+ *   out       bf16 or float32 by out_dtype, rounded once; float32 accumulation,
+ *             the ranks' products summed in the accumulator
+ * Requirements: the split extent is a multiple of P, the two extents of W_i are
+ * multiples of 8 (RTP_ESHAPE); P <= 8 (RTP_EUNSUPPORTED); pointers 16-byte
+ * aligned, no overlap of outputs with anything (RTP_EINVAL for the alignment; an
+ * overlap is not detected). M == 0 launches nothing, and buffers of M rows may then
+ * be NULL. Errors leave nothing launched; nothing is allocated; results do not
+ * change from run to run. Up to 256 rows run in a kernel of their own, which cuts
+ * K over a cluster, so a row's bits may depend on how many rows go with it.
+ * Like the GEMMs of rtp_tp_mlp, the products are launched as programmatic
+ * dependents and wait for the previous kernel of the stream.
+ */
+int rtp_tp_linear(int split, int P, int64_t M, int64_t K, int64_t N, const void* const* X, const void* const* W_shards,
+                  const void* const* bias, const void* const* residual, int act, rtp_dtype out_dtype, void* const* H,
+                  void* const* out, rtp_stream stream);
+
+/*
+ * Gradients of rtp_tp_linear (ColossalAI page, section 2.2):
+ *   dH = dOut * act'(H)   db = column sums of dH   dW_i = X^T dH_i (row: X_i^T dH)
+ *   dX = sum_i dH_i W_i^T (column, in one accumulator)   dX_i = dH W_i^T (row)
+ * and the residual's gradient is dOut itself.
+ *   H         the kept pre-activation; NULL with RTP_ACT_NONE
+ *   dOut      bf16, laid out as out
+ *   dH        bf16 scratch laid out as out (receives dH); NULL with RTP_ACT_NONE
+ *   dX, dW    bf16 or float32 by dx_dtype, dw_dtype, laid out as X and W_shards
+ *   db        float32, laid out as bias
+ * dX, dW and db may each be NULL (not wanted); X is read for dW only, W_shards for
+ * dX only. dW and dX are products of the bf16 dH, db is summed from the float32 dH.
+ * M == 0 zeroes dW and db. Requirements and errors as in rtp_tp_linear.
+ */
+int rtp_tp_linear_backward(int split, int P, int64_t M, int64_t K, int64_t N, const void* const* X,
+                           const void* const* W_shards, const void* const* H, const void* const* dOut, int act,
+                           void* const* dH, rtp_dtype dx_dtype, void* const* dX, rtp_dtype dw_dtype, void* const* dW,
+                           float* const* db, rtp_stream stream);
+
+/*
+ * Gated feed-forward block on P virtual ranks: the tensor-parallel MLP (ColossalAI
+ * "1D tensor parallelism" page, sections 2 and 2.1) with a gate beside its first
+ * projection:
+ *   Hg_i = X Ag_i   Hu_i = X Au_i   Y_i = act(Hg_i) * Hu_i   Z = sum_i Y_i B_i + R
+ *   X         bf16 [M, K];  Ag_shards, Au_shards: P bf16 [K, F/P];  B_shards: P bf16 [F/P, N]
+ *   residual  bf16 [M, N] or NULL
+ *   Y         P bf16 [M, F/P], scratch that receives Y_i (of the float32 Hg_i and
+ *             Hu_i, rounded once)
+ *   Z         bf16 or float32 [M, N] by out_dtype
+ * Both projections, the activation and the product are one kernel, the second
+ * product with the sum over ranks and the residual another. Requirements
+ * (RTP_ESHAPE): F % P == 0; K, F/P and N multiples of 8. The rest as in rtp_tp_linear.
+ */
+int rtp_tp_glu(int P, int64_t M, int64_t K, int64_t F, int64_t N, const void* X, const void* const* Ag_shards,
+               const void* const* Au_shards, const void* const* B_shards, const void* residual, int act, void* const* Y,
+               rtp_dtype out_dtype, void* Z, rtp_stream stream);
+
+/*
+ * rtp_tp_glu that also keeps what its backward pass needs: Hg, Hu (P bf16 [M, F/P]
+ * each, the pre-activations rounded once) beside Y. Z and Y are those of rtp_tp_glu.
+ */
+int rtp_tp_glu_train_forward(int P, int64_t M, int64_t K, int64_t F, int64_t N, const void* X,
+                             const void* const* Ag_shards, const void* const* Au_shards, const void* const* B_shards,
+                             const void* residual, int act, void* const* Y, void* const* Hg, void* const* Hu,
+                             rtp_dtype out_dtype, void* Z, rtp_stream stream);
+
+/*
+ * Gradients of the gated block (ColossalAI page, section 2.2), with dY_i = dZ B_i^T
+ * (never stored):
+ *   dHg_i = dY_i * Hu_i * act'(Hg_i)   dHu_i = dY_i * act(Hg_i)
+ *   dX = sum_i dHg_i Ag_i^T + dHu_i Au_i^T (one accumulator)
+ *   dAg_i = X^T dHg_i   dAu_i = X^T dHu_i   dB_i = Y_i^T dZ
+ * and the residual's gradient is dZ itself.
+ *   Hg, Hu, Y  what rtp_tp_glu_train_forward kept;  dZ bf16 [M, N]
+ *   dHg, dHu   P bf16 [M, F/P] scratch each
+ *   dX         [M, K] bf16 or float32 by dx_dtype, or NULL
+ *   dAg, dAu   P [K, F/P] by dw_dtype, or both NULL;  dB: P [F/P, N] by dw_dtype, or NULL
+ * M == 0 zeroes the weight gradients. Requirements and errors as in rtp_tp_glu.
+ */
+int rtp_tp_glu_backward(int P, int64_t M, int64_t K, int64_t F, int64_t N, const void* X, const void* const* Ag_shards,
+                        const void* const* Au_shards, const void* const* B_shards, const void* const* Hg,
+                        const void* const* Hu, const void* const* Y, const void* dZ, int act, void* const* dHg,
+                        void* const* dHu, rtp_dtype dx_dtype, void* dX, rtp_dtype dw_dtype, void* const* dAg,
+                        void* const* dAu, void* const* dB, rtp_stream stream);
+
+/*
+ * Global norm of the gradients of many tensors (the rank pieces that the backward
+ * calls write), no page counterpart:
+ *   norm = sqrt(sum over counted tensors of the sum of g^2)
+ *   dtypes[n]   RTP_F32 or RTP_BF16 per tensor;  numels[n] element counts (0 allowed)
+ *   grads[n]    device pointers, aligned to their elements (16-byte aligned ones
+ *               are read in vectors)
+ *   counted[n]  0: the tensor does not count (a replica of a piece that does: under
+ *               a broadcast mesh dim only coordinate 0 counts); NULL: all count
+ *   workspace   rtp_grad_workspace_bytes(n) bytes of device memory, 8-byte aligned,
+ *               need not be initialised; not shared by calls that may overlap
+ *   norm        device pointer, receives the float32 norm
+ * Sums are finished in float64 in a fixed order: results do not change from run to
+ * run, and squares that overflow or underflow float32 do not spoil a norm that is a
+ * float32 number. A NaN gradient gives NaN, an infinite one infinity. n == 0: 0.
+ */
+int rtp_grad_norm(int n, const int32_t* dtypes, const int64_t* numels, const void* const* grads, const uint8_t* counted,
+                  void* workspace, float* norm, rtp_stream stream);
+
+/*
+ * The norm, and every tensor (counted or not) times c = min(1, max_norm / (norm +
+ * 1e-6)), rounded once to its type; c is computed on the device, nothing waits for
+ * the host. With c == 1 and out NULL nothing is written; a NaN norm makes everything
+ * NaN, an infinite one scales by 0, as the formula says.
+ *   out  NULL (in place), or n device pointers of the tensors' types and sizes; an
+ *        output may be its own input and shares bytes with nothing else (RTP_EINVAL,
+ *        as for a tensor listed twice in place)
+ *   max_norm >= 0 (RTP_EINVAL)
+ */
+int rtp_clip_grad_norm(int n, const int32_t* dtypes, const int64_t* numels, const void* const* grads,
+                       const uint8_t* counted, float max_norm, void* const* out, void* workspace, float* norm,
+                       rtp_stream stream);
+
+/* Bytes of workspace for n tensors (0 for n < 0). Host only. */
+int64_t rtp_grad_workspace_bytes(int n);
+
 /*
  * Reads and clears the device words in which the tensor-core kernels of
- * rtp_tp_mlp record a wait that gave up (no progress for about 4 seconds; the
+ * rtp_tp_mlp, rtp_tp_linear and rtp_tp_glu record a wait that gave up (no progress for about 4 seconds; the
  * kernel then stops, frees its tensor memory and returns instead of hanging),
  * and in which the resharding kernel records a bulk copy that never completed.
  * Synchronises `stream`. *code == 0: no such event since the last check;

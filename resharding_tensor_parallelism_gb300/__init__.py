@@ -8,7 +8,8 @@ the compiled library is missing; there is no fallback.
 Names mirror the C ABI in ``include/rtp.h``:
   spec_from_dims_mapping, spec_from_onnx, spec_nd_sbp (the ND-SBP form filled
   directly), shard_shape, shard_box, shard, reshard, reshard_cost,
-  infer_spmd, infer_reshape, tp_mlp, last_error.
+  infer_spmd, infer_reshape, tp_mlp, last_error; tp_linear, tp_glu and their
+  backward calls, grad_norm, clip_grad_norm (GradGroup keeps their tables).
 """
 from __future__ import annotations
 
@@ -80,7 +81,7 @@ def _load():
     P = ctypes.POINTER
     i64p, i32p, u32p, vp = P(ctypes.c_int64), P(ctypes.c_int32), P(ctypes.c_uint32), ctypes.c_void_p
     vpp = P(ctypes.c_void_p)
-    c_int = ctypes.c_int
+    c_int, i64 = ctypes.c_int, ctypes.c_int64
     sig = {
         "rtp_spec_from_dims_mapping": [c_int, i32p, c_int, i64p, i32p, ctypes.c_uint32, P(Spec)],
         "rtp_spec_from_onnx": [c_int, c_int, i64p, c_int, i64p, i32p, i64p, c_int, i64p, i64p, P(Spec)],
@@ -96,6 +97,16 @@ def _load():
         "rtp_infer_sbp_signature": [c_int, c_int, i64p, c_int, c_int, i32p, i32p, i32p, i32p, i32p, i32p,
                                     P(ctypes.c_double), i32p],
         "rtp_infer_broadcast": [c_int, i32p, P(i64p), P(Spec), P(c_int), i64p, P(Spec)],
+        "rtp_tp_linear": [c_int, c_int, i64, i64, i64, vpp, vpp, vpp, vpp, c_int, c_int, vpp, vpp, vp],
+        "rtp_tp_linear_backward": [c_int, c_int, i64, i64, i64, vpp, vpp, vpp, vpp, c_int, vpp, c_int, vpp, c_int, vpp,
+                                   vpp, vp],
+        "rtp_tp_glu": [c_int, i64, i64, i64, i64, vp, vpp, vpp, vpp, vp, c_int, vpp, c_int, vp, vp],
+        "rtp_tp_glu_train_forward": [c_int, i64, i64, i64, i64, vp, vpp, vpp, vpp, vp, c_int, vpp, vpp, vpp, c_int, vp,
+                                     vp],
+        "rtp_tp_glu_backward": [c_int, i64, i64, i64, i64, vp, vpp, vpp, vpp, vpp, vpp, vpp, vp, c_int, vpp, vpp, c_int,
+                                vp, c_int, vpp, vpp, vpp, vp],
+        "rtp_grad_norm": [c_int, i32p, i64p, vpp, vp, vp, vp, vp],
+        "rtp_clip_grad_norm": [c_int, i32p, i64p, vpp, vp, ctypes.c_float, vpp, vp, vp, vp],
         "rtp_device_error": [vp, u32p],
         "rtp_wait_selftest": [c_int, ctypes.c_ulonglong, vp, vp],
         "rtp_test_hook": [c_int, ctypes.c_int64],
@@ -119,6 +130,8 @@ def _load():
     lib.rtp_last_error.argtypes = []
     lib.rtp_version.restype = ctypes.c_char_p
     lib.rtp_version.argtypes = []
+    lib.rtp_grad_workspace_bytes.restype = ctypes.c_int64
+    lib.rtp_grad_workspace_bytes.argtypes = [c_int]
     _lib = lib
     return lib
 
@@ -596,6 +609,317 @@ def tp_mlp_noalloc(X, A_shards, B_shards, Z=None, stream=None):
     _check(_load().rtp_tp_mlp_noalloc(P, M, K, Fp * P, N, X.data_ptr(), _ptrs([a.data_ptr() for a in A_shards]),
                                       _ptrs([b.data_ptr() for b in B_shards]), Z.data_ptr(), _stream_ptr(stream)))
     return Z
+
+
+# ---- linear layers and the gated feed-forward block -------------------------------------
+
+ACTS = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3, "relu": 4}
+
+
+def _act_code(act: str) -> int:
+    try:
+        return ACTS[act]
+    except (KeyError, TypeError):
+        raise RtpError(-1, "unknown activation %r (one of %s)" % (act, ", ".join(ACTS))) from None
+
+
+def _listed(t) -> list:
+    """A list of rank buffers; one tensor stands for a list of one."""
+    return list(t) if isinstance(t, (list, tuple)) else [t]
+
+
+def _tensor_ptrs(ts) -> ctypes.Array:
+    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+
+
+def _matrix(fn: str, name: str, t):
+    if t.dim() != 2:
+        raise RtpError(-2, "%s: %s is %s, expected a matrix" % (fn, name, tuple(t.shape)))
+    return t.shape
+
+
+def _new(n: int, shape, dtype, dev, stream=None) -> list:
+    """n fresh buffers of one shape, owned by the stream the call runs on: memory that torch hands out again is ordered
+    on its owning stream only, and scratch is dropped when the call returns."""
+    torch = _torch()
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):
+            return [torch.empty(shape, dtype=dtype, device=dev) for _ in range(n)]
+    return [torch.empty(shape, dtype=dtype, device=dev) for _ in range(n)]
+
+
+def _linear_shapes(fn: str, X, W_shards, split: str):
+    """(row?, X list, W list, P, M, K, N, Kp, Np) of a linear layer's arguments."""
+    if split not in ("column", "row"):
+        raise RtpError(-1, "%s: split %r is not 'column' or 'row'" % (fn, split))
+    X, W = _listed(X), _listed(W_shards)
+    if not W or not X:
+        raise RtpError(-1, "%s: no weight shards or no X" % fn)
+    row, P = split == "row", len(W)
+    M, _ = _matrix(fn, "X", X[0])
+    Kp, Np = _matrix(fn, "W_shards[0]", W[0])
+    return row, X, W, P, M, Kp * P if row else Kp, Np if row else Np * P, Kp, Np
+
+
+def tp_linear(X, W_shards, split: str = "column", bias=None, act: str = "none", residual=None, H=None, out=None,
+              out_dtype=None, keep_h: bool = False, stream=None):
+    """Linear layer on P = len(W_shards) virtual ranks, bias, activation and residual in the product's epilogue.
+
+    column: out_i = act(X W_i + b_i) + R_i, X one tensor [M, K], W_i [K, N/P];
+    row:    out = act(sum_i X_i W_i + b) + R, X a list of P tensors [M, K/P], W_i [K/P, N].
+    bias, residual, H and out are lists with one entry per output buffer (P for column, 1 for row; a
+    single tensor stands for a list of one). All bf16; out may be float32 (out_dtype, or by `out`).
+    Returns the list of outputs, or (outputs, H) with keep_h (or H given): the bf16 pre-activations that
+    tp_linear_backward reads."""
+    torch = _torch()
+    fn = "tp_linear"
+    bf16 = torch.bfloat16
+    row, X, W, P, M, K, N, Kp, Np = _linear_shapes(fn, X, W_shards, split)
+    outs, code = 1 if row else P, _act_code(act)
+    device = _device_of(X[0])
+    if out is None:
+        out = _new(outs, (M, Np), out_dtype or bf16, X[0].device, stream)
+    else:
+        out = _listed(out)
+        if not out:
+            raise RtpError(-1, "%s: no out buffers" % fn)
+        out_dtype = out_dtype or out[0].dtype
+    if keep_h and H is None:
+        H = _new(outs, (M, Np), bf16, X[0].device, stream)
+    groups = [("X", X, [(M, Kp)] * (P if row else 1), bf16), ("W_shards", W, (Kp, Np), bf16),
+              ("out", out, [(M, Np)] * outs, out_dtype or bf16)]
+    ptrs = {}
+    for name, ts, shape in (("bias", bias, (Np,)), ("residual", residual, (M, Np)), ("H", H, (M, Np))):
+        if ts is not None:
+            ts = _listed(ts)
+            groups.append((name, ts, [shape] * outs, bf16))
+            ptrs[name] = ts
+    _check_buffers(fn, device, groups)
+    opt = {k: _tensor_ptrs(v) for k, v in ptrs.items()}
+    _check(_load().rtp_tp_linear(1 if row else 0, P, M, K, N, _tensor_ptrs(X), _tensor_ptrs(W), opt.get("bias"),
+                                 opt.get("residual"), code, _dtype_code(out[0]), opt.get("H"), _tensor_ptrs(out),
+                                 _stream_ptr(stream)))
+    return (out, ptrs["H"]) if "H" in ptrs else out
+
+
+def tp_linear_backward(X, W_shards, dOut, split: str = "column", H=None, act: str = "none", dH=None, dX=None, dW=None,
+                       db=None, bias_grad: bool = True, dx_dtype=None, dw_dtype=None, stream=None):
+    """Gradients of tp_linear given dOut (bf16, laid out as its outputs) and, with an activation, the kept H.
+    Returns lists (dX, dW, db): dX like X, dW like W_shards (bf16, or float32 by dx_dtype / dw_dtype or by the
+    buffers given), db float32 like bias (None without bias_grad). The residual's gradient is dOut."""
+    torch = _torch()
+    fn = "tp_linear_backward"
+    bf16, f32 = torch.bfloat16, torch.float32
+    row, X, W, P, M, K, N, Kp, Np = _linear_shapes(fn, X, W_shards, split)
+    outs, ins, code = 1 if row else P, P if row else 1, _act_code(act)
+    dev, device = X[0].device, _device_of(X[0])
+    dOut = _listed(dOut)
+    if code and H is None:
+        raise RtpError(-1, "%s: the kept pre-activation H is needed with act=%r" % (fn, act))
+    groups = [("X", X, [(M, Kp)] * ins, bf16), ("W_shards", W, (Kp, Np), bf16), ("dOut", dOut, [(M, Np)] * outs, bf16)]
+    hp = dhp = None
+    if code:
+        H = _listed(H)
+        dH = _new(outs, (M, Np), bf16, dev, stream) if dH is None else _listed(dH)
+        groups += [("H", H, [(M, Np)] * outs, bf16), ("dH", dH, [(M, Np)] * outs, bf16)]
+    dX = _new(ins, (M, Kp), dx_dtype or bf16, dev, stream) if dX is None else _listed(dX)
+    dW = _new(P, (Kp, Np), dw_dtype or bf16, dev, stream) if dW is None else _listed(dW)
+    dx_dtype, dw_dtype = dx_dtype or dX[0].dtype, dw_dtype or dW[0].dtype
+    groups += [("dX", dX, [(M, Kp)] * ins, dx_dtype), ("dW", dW, [(Kp, Np)] * P, dw_dtype)]
+    if db is not None or bias_grad:
+        db = _new(outs, (Np,), f32, dev, stream) if db is None else _listed(db)
+        groups.append(("db", db, [(Np,)] * outs, f32))
+    _check_buffers(fn, device, groups)
+    if code:
+        hp, dhp = _tensor_ptrs(H), _tensor_ptrs(dH)
+    _check(_load().rtp_tp_linear_backward(1 if row else 0, P, M, K, N, _tensor_ptrs(X), _tensor_ptrs(W), hp,
+                                          _tensor_ptrs(dOut), code, dhp, _dtype_code(dX[0]), _tensor_ptrs(dX),
+                                          _dtype_code(dW[0]), _tensor_ptrs(dW),
+                                          _tensor_ptrs(db) if db is not None else None, _stream_ptr(stream)))
+    return dX, dW, db
+
+
+def _glu_shapes(fn: str, X, Ag, Au, B):
+    for name, w in (("Ag_shards", Ag), ("Au_shards", Au), ("B_shards", B)):
+        if len(w) != len(Ag) or not w:
+            raise RtpError(-1, "%s: %d %s for %d ranks" % (fn, len(w), name, len(Ag)))
+    M, K = _matrix(fn, "X", X)
+    _, Fp = _matrix(fn, "Ag_shards[0]", Ag[0])
+    _, N = _matrix(fn, "B_shards[0]", B[0])
+    bf16 = _torch().bfloat16
+    return M, K, Fp, N, [("X", [X], (M, K), bf16), ("Ag_shards", Ag, (K, Fp), bf16), ("Au_shards", Au, (K, Fp), bf16),
+                         ("B_shards", B, (Fp, N), bf16)]
+
+
+def _glu_forward(fn, X, Ag, Au, B, act, residual, kept, Z, out_dtype, stream):
+    """kept: [Y] or [Y, Hg, Hu], each a list of P buffers or None. Returns (Z, kept)."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    P = len(Ag)
+    M, K, Fp, N, groups = _glu_shapes(fn, X, Ag, Au, B)
+    code, device = _act_code(act), _device_of(X)
+    if Z is None:
+        Z, = _new(1, (M, N), out_dtype or bf16, X.device, stream)
+    kept = [_new(P, (M, Fp), bf16, X.device, stream) if k is None else _listed(k) for k in kept]
+    groups.append(("Z", [Z], (M, N), out_dtype or Z.dtype))
+    if residual is not None:
+        groups.append(("residual", [residual], (M, N), bf16))
+    for name, k in zip(("Y", "Hg", "Hu"), kept):
+        groups.append((name, k, [(M, Fp)] * P, bf16))
+    _check_buffers(fn, device, groups)
+    call = _load().rtp_tp_glu if len(kept) == 1 else _load().rtp_tp_glu_train_forward
+    _check(call(P, M, K, Fp * P, N, X.data_ptr(), _tensor_ptrs(Ag), _tensor_ptrs(Au), _tensor_ptrs(B),
+                residual.data_ptr() if residual is not None else None, code, *[_tensor_ptrs(k) for k in kept],
+                _dtype_code(Z), Z.data_ptr(), _stream_ptr(stream)))
+    return Z, kept
+
+
+def tp_glu(X, Ag_shards, Au_shards, B_shards, act: str = "silu", residual=None, Y=None, Z=None, out_dtype=None,
+           stream=None):
+    """Gated feed-forward block on P = len(Ag_shards) virtual ranks:
+    Z = sum_i (act(X Ag_i) * (X Au_i)) B_i + residual, bf16 [M, N] (or float32: out_dtype, or by `Z`).
+    Y: P bf16 [M, F/P] scratch buffers, allocated when not given. Returns Z."""
+    return _glu_forward("tp_glu", X, _listed(Ag_shards), _listed(Au_shards), _listed(B_shards), act, residual, [Y], Z,
+                        out_dtype, stream)[0]
+
+
+def tp_glu_train_forward(X, Ag_shards, Au_shards, B_shards, act: str = "silu", residual=None, Y=None, Hg=None, Hu=None,
+                         Z=None, out_dtype=None, stream=None):
+    """tp_glu that keeps the bf16 pre-activations Hg_i = X Ag_i and Hu_i = X Au_i beside Y_i = act(Hg_i) * Hu_i for
+    tp_glu_backward. Returns (Z, Y, Hg, Hu)."""
+    Z, kept = _glu_forward("tp_glu_train_forward", X, _listed(Ag_shards), _listed(Au_shards), _listed(B_shards), act,
+                           residual, [Y, Hg, Hu], Z, out_dtype, stream)
+    return (Z, *kept)
+
+
+def tp_glu_backward(X, Ag_shards, Au_shards, B_shards, Hg, Hu, Y, dZ, act: str = "silu", dHg=None, dHu=None, dX=None,
+                    dAg=None, dAu=None, dB=None, dx_dtype=None, dw_dtype=None, stream=None):
+    """Gradients of the gated block given dZ (bf16 [M, N]) and what tp_glu_train_forward kept. Returns (dX, dAg, dAu,
+    dB): dX [M, K] and lists of P weight gradients, bf16 or float32 (dx_dtype, dw_dtype, or by the buffers given). The
+    residual's gradient is dZ. dHg, dHu: P bf16 [M, F/P] scratch buffers each."""
+    torch = _torch()
+    fn = "tp_glu_backward"
+    bf16 = torch.bfloat16
+    Ag, Au, B = _listed(Ag_shards), _listed(Au_shards), _listed(B_shards)
+    P, dev = len(Ag), X.device
+    M, K, Fp, N, groups = _glu_shapes(fn, X, Ag, Au, B)
+    code, device = _act_code(act), _device_of(X)
+    mid = [(n, _new(P, (M, Fp), bf16, dev, stream) if t is None else _listed(t))
+           for n, t in (("Hg", Hg), ("Hu", Hu), ("Y", Y), ("dHg", dHg), ("dHu", dHu))]
+    if Hg is None or Hu is None or Y is None:
+        raise RtpError(-1, "%s: Hg, Hu and Y of the training forward are needed" % fn)
+    if dX is None:
+        dX, = _new(1, (M, K), dx_dtype or bf16, dev, stream)
+    dw = [_new(P, s, dw_dtype or bf16, dev, stream) if t is None else _listed(t)
+          for t, s in ((dAg, (K, Fp)), (dAu, (K, Fp)), (dB, (Fp, N)))]
+    dw_dtype = dw_dtype or dw[0][0].dtype
+    groups += [(n, t, [(M, Fp)] * P, bf16) for n, t in mid]
+    groups += [("dZ", [dZ], (M, N), bf16), ("dX", [dX], (M, K), dx_dtype or dX.dtype),
+               ("dAg", dw[0], [(K, Fp)] * P, dw_dtype), ("dAu", dw[1], [(K, Fp)] * P, dw_dtype),
+               ("dB", dw[2], [(Fp, N)] * P, dw_dtype)]
+    _check_buffers(fn, device, groups)
+    hg, hu, y, dhg, dhu = (_tensor_ptrs(t) for _, t in mid)
+    _check(_load().rtp_tp_glu_backward(P, M, K, Fp * P, N, X.data_ptr(), _tensor_ptrs(Ag), _tensor_ptrs(Au),
+                                       _tensor_ptrs(B), hg, hu, y, dZ.data_ptr(), code, dhg, dhu, _dtype_code(dX),
+                                       dX.data_ptr(), _dtype_code(dw[0][0]), *[_tensor_ptrs(t) for t in dw],
+                                       _stream_ptr(stream)))
+    return (dX, *dw)
+
+
+# ---- global gradient norm and clipping -----------------------------------------------------
+
+def counted_pieces(spec: Spec) -> List[bool]:
+    """Which rank pieces of a gradient laid out by `spec` count towards the global norm: under broadcast mesh dims only
+    the ranks at coordinate 0 (the others hold replicas). A partial layout has no per-rank norm: reshard it first."""
+    md = spec.mesh_ndim
+    if any(spec.sbp_kind[d] not in (SPLIT, BROADCAST) for d in range(md)):
+        raise RtpError(-3, "counted_pieces: a partial layout must be reshard before its norm is taken")
+    flags = [True] * spec.num_ranks
+    for p in range(spec.num_ranks):
+        rest = p
+        for d in reversed(range(md)):
+            c, rest = rest % spec.mesh_shape[d], rest // spec.mesh_shape[d]
+            if c and spec.sbp_kind[d] == BROADCAST:
+                flags[spec.rank_ids[p]] = False
+    return flags
+
+
+class GradGroup:
+    """The gradients of a program's tensors (rank pieces, float32 and bf16 mixed), for their global norm and clipping.
+    Keeps the tensors, their tables and the workspace, as a training loop keeps its gradient buffers; the values are
+    read at each call. counted[i] False: tensor i is a replica (counted_pieces) that is clipped but not counted. Calls
+    on one group that may overlap on the GPU share its workspace and must be ordered by the caller."""
+
+    def __init__(self, grads, counted=None):
+        torch = _torch()
+        self.grads = list(grads)
+        n = len(self.grads)
+        if n and not self.grads[0].is_cuda:
+            raise RtpError(-1, "GradGroup: tensors must live on the GPU")
+        self.device = self.grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+        self._numels = self._table("grads", self.grads)
+        self._dtypes = _i32([_dtype_code(g) for g in self.grads])
+        self._ptrs = _ptrs([g.data_ptr() for g in self.grads])
+        self._counted = None
+        if counted is not None:
+            counted = [bool(c) for c in counted]
+            if len(counted) != n:
+                raise RtpError(-1, "GradGroup: %d counted flags for %d tensors" % (len(counted), n))
+            self._counted = (ctypes.c_uint8 * max(1, n))(*counted)
+        self._ws = torch.empty((_load().rtp_grad_workspace_bytes(n) // 8,), dtype=torch.float64, device=self.device)
+
+    def _table(self, name, ts):
+        for i, t in enumerate(ts):
+            _dtype_code(t)
+            if not t.is_contiguous():
+                raise RtpError(-1, "GradGroup: %s[%d] must be contiguous (row-major)" % (name, i))
+            if t.device != self.device:
+                raise RtpError(-1, "GradGroup: %s[%d] is on %s, the group on %s" % (name, i, t.device, self.device))
+        return _i64([t.numel() for t in ts])
+
+    def _begin(self, stream):
+        torch = _torch()
+        if torch.cuda.current_device() != self.device.index:
+            raise RtpError(-1, "GradGroup: tensors are on %s but the current CUDA device is %d" % (
+                self.device, torch.cuda.current_device()))
+        return _new(1, (), torch.float32, self.device, stream)[0]
+
+    def norm(self, stream=None):
+        """The global norm, a float32 scalar tensor on the GPU."""
+        norm = self._begin(stream)
+        _check(_load().rtp_grad_norm(len(self.grads), self._dtypes, self._numels, self._ptrs, self._counted,
+                                     self._ws.data_ptr(), norm.data_ptr(), _stream_ptr(stream)))
+        return norm
+
+    def clip(self, max_norm: float, out=None, stream=None):
+        """Scales every tensor by min(1, max_norm / (norm + 1e-6)), in place or into the tensors of `out` (same types
+        and sizes). Returns (norm, tensors)."""
+        norm = self._begin(stream)
+        optr = None
+        if out is not None:
+            if len(out) != len(self.grads):
+                raise RtpError(-1, "GradGroup: %d out tensors for %d gradients" % (len(out), len(self.grads)))
+            for i, (o, g) in enumerate(zip(out, self.grads)):
+                if o.dtype is not g.dtype or o.shape != g.shape or not o.is_contiguous() or o.device != self.device:
+                    raise RtpError(-2, "GradGroup: out[%d] is %s %s on %s, expected contiguous %s %s on %s" % (
+                        i, o.dtype, tuple(o.shape), o.device, g.dtype, tuple(g.shape), self.device))
+            optr = _ptrs([o.data_ptr() for o in out])
+        _check(_load().rtp_clip_grad_norm(len(self.grads), self._dtypes, self._numels, self._ptrs, self._counted,
+                                          float(max_norm), optr, self._ws.data_ptr(), norm.data_ptr(),
+                                          _stream_ptr(stream)))
+        return norm, (self.grads if out is None else out)
+
+
+def grad_norm(grads, counted=None, stream=None):
+    """Global norm of a list of gradients (GradGroup.norm without keeping a group)."""
+    return GradGroup(grads, counted).norm(stream)
+
+
+def clip_grad_norm(grads, max_norm: float, counted=None, out=None, stream=None):
+    """Clips a list of gradients by their global norm (GradGroup.clip without keeping a group)."""
+    return GradGroup(grads, counted).clip(max_norm, out, stream)
 
 
 def device_error(stream=None) -> int:

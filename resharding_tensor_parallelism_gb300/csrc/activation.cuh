@@ -1,0 +1,78 @@
+// The activations of rtp_tp_linear and rtp_tp_glu (rtp_act) and their
+// derivatives, in float32 on the float32 accumulator.
+//   GELU       x Phi(x), Phi(x) = (1 + erf(x / sqrt 2)) / 2;  d = Phi(x) + x phi(x)
+//   GELU_TANH  x s(2z), z = sqrt(2 / pi) (x + 0.044715 x^3), since (1 + tanh z) / 2 = s(2z),
+//              s(v) = 1 / (1 + e^-v); this form keeps its relative accuracy where tanh z is near -1
+//   SILU       x s(x);  d = s(x) (1 + x (1 - s(x)))
+//   RELU       max(x, 0), a NaN passes;  d = 1 for x > 0
+#pragma once
+
+#include "rtp.h"
+
+namespace rtp {
+
+namespace {
+
+__device__ __forceinline__ float logistic(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
+
+constexpr float kTanhScale = 1.5957691216057307f;  // 2 sqrt(2 / pi)
+constexpr float kTanhCubic = 0.044715f;
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float x)
+{
+    if constexpr (ACT == RTP_ACT_GELU) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752440f));
+    if constexpr (ACT == RTP_ACT_GELU_TANH) return x * logistic(kTanhScale * (x + kTanhCubic * x * x * x));
+    if constexpr (ACT == RTP_ACT_SILU) return x * logistic(x);
+    if constexpr (ACT == RTP_ACT_RELU) return x > 0.0f || x != x ? x : 0.0f;
+    return x;
+}
+
+// a = act(x), d = act'(x)
+template <int ACT>
+__device__ __forceinline__ void act_both(float x, float& a, float& d)
+{
+    if constexpr (ACT == RTP_ACT_GELU) {
+        const float cdf = 0.5f * (1.0f + erff(x * 0.70710678118654752440f));
+        a = x * cdf;
+        d = cdf + x * (0.39894228040143267794f * expf(-0.5f * x * x));
+    } else if constexpr (ACT == RTP_ACT_GELU_TANH) {
+        const float s = logistic(kTanhScale * (x + kTanhCubic * x * x * x));
+        const float w = s * (1.0f - s);
+        a = x * s;
+        // w is zero once the sigmoid has saturated, where x^2 may overflow
+        d = s + (w != 0.0f ? x * w * kTanhScale * (1.0f + 3.0f * kTanhCubic * x * x) : 0.0f);
+    } else if constexpr (ACT == RTP_ACT_SILU) {
+        const float s = logistic(x);
+        a = x * s;
+        d = s * (1.0f + x * (1.0f - s));
+    } else if constexpr (ACT == RTP_ACT_RELU) {
+        a = x > 0.0f || x != x ? x : 0.0f;
+        d = x > 0.0f ? 1.0f : 0.0f;
+    } else {
+        a = x;
+        d = 1.0f;
+    }
+}
+
+// Calls body(std::integral_constant-like tag<ACT>) for the runtime `act`: the
+// branch is uniform and stands outside the loops over a chunk's elements.
+template <int ACT>
+struct ActTag {
+    static constexpr int value = ACT;
+};
+template <class Body>
+__device__ __forceinline__ void with_act(int act, Body&& body)
+{
+    switch (act) {
+    case RTP_ACT_GELU: body(ActTag<RTP_ACT_GELU>()); break;
+    case RTP_ACT_GELU_TANH: body(ActTag<RTP_ACT_GELU_TANH>()); break;
+    case RTP_ACT_SILU: body(ActTag<RTP_ACT_SILU>()); break;
+    case RTP_ACT_RELU: body(ActTag<RTP_ACT_RELU>()); break;
+    default: body(ActTag<RTP_ACT_NONE>()); break;
+    }
+}
+
+}  // namespace
+
+}  // namespace rtp

@@ -1,0 +1,407 @@
+// The same products for few rows (a token or a small batch being decoded, short
+// prompts): out^T = W^T X^T with the weights as the M operand and the rows
+// ("tokens") as the N operand of the MMA.
+//
+// With few tokens every weight is used a handful of times, so the bytes of the
+// weights over the HBM rate bound the time, and the tile of the pair kernel
+// would leave most of its rows, and with few columns most SMs, idle. Here a CTA
+// multiplies 128 weight columns (64 gate and the same 64 up columns for LIN_GLU)
+// with a tile of up to 256 tokens: tcgen05.mma M = 128, N = tokens rounded up to
+// 16, K = 16 a step. The weight tile is used straight from its row-major form (an
+// M-major A operand), so no weight is laid out anew. The K range (all ranks' K
+// ranges when the ranks are summed) is cut over a cluster of up to 8 CTAs: each
+// holds a float32 partial of the tile in its shared memory, and the CTAs then add
+// up slices of it over distributed shared memory in cluster-rank order, so the
+// result does not depend on timing and no workspace is needed. Two CTAs fit on
+// an SM for up to 128 tokens, so that about 190 KB of loads are in flight per SM.
+#include <atomic>
+#include <cstring>
+
+#include "activation.cuh"
+#include "linear.h"
+#include "tcgen05.cuh"
+
+namespace rtp {
+
+namespace {
+
+constexpr int FEAT = 128;                      // weight columns (MMA rows) of a tile
+constexpr uint32_t SUB = 64 * BK * 2;          // one 64 x 64 box, 8 KB
+constexpr uint32_t W_BYTES = FEAT * BK * 2;    // 16 KB
+constexpr int THREADS = 128;
+constexpr int MAX_STAGES = 8;
+constexpr int MAX_SPLIT = 8;                   // portable cluster size
+constexpr size_t SMEM_TWO = 113 * 1024;        // per CTA, two on an SM (228 KB, 1 KB reserved per CTA)
+constexpr size_t SMEM_ONE = 227 * 1024;
+constexpr size_t SMEM_EXTRA = 1024 + 256;      // alignment; barriers
+
+struct Args {
+    CUtensorMap tw[LIN_MAX_GROUPS];  // weights; LIN_GLU: [g] gate, [LIN_MAX_RANKS + g] up
+    CUtensorMap tx[LIN_MAX_RANKS];
+    void* out[LIN_MAX_RANKS];
+    __nv_bfloat16* out2[LIN_MAX_RANKS];
+    __nv_bfloat16* out3[LIN_MAX_RANKS];
+    const __nv_bfloat16* bias[LIN_MAX_RANKS];
+    const __nv_bfloat16* residual[LIN_MAX_RANKS];
+    int32_t groups, fused, kb_per_group, kbs;
+    int32_t tiles;  // feature tiles of a group
+    int32_t rows, cols, ntok, tmem_cols;
+    int32_t split, stages;
+    int32_t act, keep, weights_ready;
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 bf16x4(const __nv_bfloat16* p)
+{
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+__device__ __forceinline__ void store_bf16x4(__nv_bfloat16* p, float4 v)
+{
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
+template <int EPI, bool F32>
+__global__ void __launch_bounds__(THREADS) linear_few_kernel(const __grid_constant__ Args a)
+{
+    constexpr int TILE_COLS = EPI == LIN_GLU ? FEAT / 2 : FEAT;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t x_bytes = (uint32_t)a.ntok * (BK * 2), stage_bytes = W_BYTES + x_bytes;
+    const uint32_t bar0 = smem + (uint32_t)a.stages * stage_bytes;
+    auto full_bar = [&](int s) { return bar0 + 8u * (uint32_t)s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (uint32_t)(MAX_STAGES + s); };
+    const uint32_t acc_bar = bar0 + 8u * (uint32_t)(2 * MAX_STAGES), drain_bar = acc_bar + 8u;
+    const uint32_t word0 = bar0 - smem_u32(smem_raw) + 8u * (2 * MAX_STAGES + 2);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem_raw + word0);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cr = (int)cluster_rank();
+    const int tile = (int)blockIdx.x / a.split;
+    const int g = tile / a.tiles, f0 = (tile - g * a.tiles) * TILE_COLS;
+    const int t0 = (int)blockIdx.y * a.ntok;
+    const int kb0 = (int)((int64_t)a.kbs * cr / a.split), kb1 = (int)((int64_t)a.kbs * (cr + 1) / a.split);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(acc_bar, 1);
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32((const void*)tmem_slot)),
+                     "r"(a.tmem_cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const int n = kb1 - kb0;
+            auto load_w = [&](int i, int s) {
+                const int kb = kb0 + i, kg = a.fused ? kb / a.kb_per_group : 0;
+                const int k = (kb - kg * a.kb_per_group) * BK, wg = a.fused ? kg : g;
+                const uint32_t dst = smem + (uint32_t)s * stage_bytes;
+                if constexpr (EPI == LIN_GLU) {
+                    tma_load_2d(dst, &a.tw[wg], full_bar(s), f0, k);
+                    tma_load_2d(dst + SUB, &a.tw[LIN_MAX_RANKS + wg], full_bar(s), f0, k);
+                } else {
+                    tma_load_2d(dst, &a.tw[wg], full_bar(s), f0, k);
+                    tma_load_2d(dst + SUB, &a.tw[wg], full_bar(s), f0 + 64, k);
+                }
+            };
+            auto load_x = [&](int i, int s) {
+                const int kb = kb0 + i, kg = a.fused ? kb / a.kb_per_group : 0;
+                tma_load_2d(smem + (uint32_t)s * stage_bytes + W_BYTES, &a.tx[a.fused ? kg : g], full_bar(s),
+                            (kb - kg * a.kb_per_group) * BK, t0);
+            };
+            // Weights that nothing on the stream can still be writing are fetched
+            // while the previous kernel finishes.
+            const int early = a.weights_ready ? min(n, a.stages) : 0;
+            for (int i = 0; i < early; ++i) {
+                mbar_expect_tx(full_bar(i), stage_bytes);
+                load_w(i, i);
+            }
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            // This kernel's own dependents may be set up from here on: whatever
+            // ran before this kernel is complete.
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+            for (int i = 0; i < early; ++i) load_x(i, i);
+            int s = early == a.stages ? 0 : early;
+            uint32_t phase = early == a.stages ? 1u : 0u;
+            int issued = early;
+            for (int i = early; i < n; ++i) {
+                if (!wait_bar(empty_bar(s), phase ^ 1u, abort_flag, ERR_PRODUCER)) break;
+                mbar_expect_tx(full_bar(s), stage_bytes);
+                load_w(i, s);
+                load_x(i, s);
+                ++issued;
+                if (++s == a.stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (issued < n)  // gave up: the loads in flight land before the CTA leaves
+                for (int i = max(0, issued - a.stages); i < issued; ++i)
+                    drain_wait(full_bar(i % a.stages), (uint32_t)((i / a.stages) & 1));
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | ((uint32_t)(a.ntok >> 3) << 17) |
+                                   ((uint32_t)(FEAT >> 4) << 24);
+            const uint64_t desc_w = smem_desc(smem, SUB, 1024u), desc_x = smem_desc(smem + W_BYTES, 16u, 1024u);
+            int s = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int i = 0; i < kb1 - kb0; ++i) {
+                if (!wait_bar(full_bar(s), phase, abort_flag, ERR_MMA_STAGE)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t off = (uint64_t)((uint32_t)s * stage_bytes >> 4);
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k)
+                    mma_bf16(tmem_base, desc_w + off + (uint64_t)(2048u * k >> 4), desc_x + off + (uint64_t)(32u * k >> 4),
+                             idesc, (i > 0 || k > 0) ? 1u : 0u);
+                mma_commit(empty_bar(s));
+                if (++s == a.stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (ok) {
+                mma_commit(acc_bar);
+            } else {
+                mma_commit(drain_bar);
+                drain_wait(drain_bar, 0);
+            }
+        }
+        __syncwarp();
+    }
+
+    // ---------------- the partial tile to shared memory, then the sum ----------------
+    // Every load has landed and every MMA is done when acc_bar completes, so the
+    // ring's memory is free: token t, feature f at float t * 128 + f.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int ok = 1;
+    if (lane == 0) ok = wait_bar(acc_bar, 0, abort_flag, ERR_EPILOGUE) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    const int mtok = min(a.ntok, a.rows - t0);
+    if (ok) {
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + ((uint32_t)(warp * 32) << 16);
+        for (int c = 0; c < mtok; c += 16) {
+            uint32_t r[16];
+            tmem_ld_16cols(taddr + (uint32_t)c, r);
+            const uint32_t dst = smem + 4u * (uint32_t)(c * FEAT + warp * 32 + lane);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 4u * FEAT * j), "r"(r[j]) : "memory");
+        }
+    }
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(a.tmem_cols) : "memory");
+
+    // A thread takes 4 neighbouring output columns of one token.
+    constexpr int QUADS = TILE_COLS / 4;
+    auto sum4 = [&](int t, int f) {
+        const uint32_t addr = smem + 4u * (uint32_t)(t * FEAT + f);
+        float4 v = ld_cluster_f4(map_to_rank(addr, 0));
+        for (int r = 1; r < a.split; ++r) v = add4(v, ld_cluster_f4(map_to_rank(addr, (uint32_t)r)));
+        return v;
+    };
+    for (int i = cr * THREADS + (int)threadIdx.x; i < mtok * QUADS; i += a.split * THREADS) {
+        const int t = i / QUADS, f = (i - t * QUADS) * 4, col = f0 + f;
+        if (col >= a.cols) continue;
+        const int64_t at = (int64_t)(t0 + t) * a.cols + col;
+        float4 v = sum4(t, f);
+        if constexpr (EPI == LIN_GLU) {
+            const float4 u = sum4(t, 64 + f);
+            if (a.keep) {
+                store_bf16x4(a.out2[g] + at, v);
+                store_bf16x4(a.out3[g] + at, u);
+            }
+            with_act(a.act, [&](auto tag) {
+                constexpr int ACT = decltype(tag)::value;
+                v = make_float4(act_value<ACT>(v.x) * u.x, act_value<ACT>(v.y) * u.y, act_value<ACT>(v.z) * u.z,
+                                act_value<ACT>(v.w) * u.w);
+            });
+        } else {
+            if (a.bias[g]) v = add4(v, bf16x4(a.bias[g] + col));
+            if (a.keep) store_bf16x4(a.out2[g] + at, v);
+            with_act(a.act, [&](auto tag) {
+                constexpr int ACT = decltype(tag)::value;
+                v = make_float4(act_value<ACT>(v.x), act_value<ACT>(v.y), act_value<ACT>(v.z), act_value<ACT>(v.w));
+            });
+            if (a.residual[g]) v = add4(v, bf16x4(a.residual[g] + at));
+        }
+        if constexpr (F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out[g]) + at) = v;
+        else store_bf16x4(static_cast<__nv_bfloat16*>(a.out[g]) + at, v);
+    }
+    cluster_sync();  // no CTA leaves while a peer may still read its partial
+}
+
+// ---- host side --------------------------------------------------------------------
+
+int sm_count(int* n)
+{
+    static std::atomic<int> sms[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return RTP_ECUDA;
+    int v = sms[dev].load(std::memory_order_acquire);
+    if (!v) {
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) return RTP_ECUDA;
+        sms[dev].store(v, std::memory_order_release);
+    }
+    *n = v;
+    return RTP_OK;
+}
+
+template <int EPI, bool F32>
+int launch_t(const char* fn, const Args& args, dim3 grid, size_t smem, cudaStream_t stream)
+{
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<EPI, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_ONE);
+        if (e != cudaSuccess) return fail(RTP_ECUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
+        ready[dev].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)args.split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, linear_few_kernel<EPI, F32>, args);
+    if (e != cudaSuccess) return fail(RTP_ECUDA, "%s: few-row launch failed: %s", fn, cudaGetErrorString(e));
+    return RTP_OK;
+}
+
+}  // namespace
+
+int launch_linear_few(const char* fn, const LinGemm& p, bool weights_ready, cudaStream_t stream)
+{
+    int sms = 0, st;
+    if (sm_count(&sms)) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
+    static thread_local Args a;
+    std::memset(&a, 0, sizeof a);
+    const int tile_cols = p.epi == LIN_GLU ? FEAT / 2 : FEAT;
+    // equal token tiles of at most 256, rounded up to the MMA's step of 16
+    const int ttiles = (int)((p.rows + 255) / 256);
+    a.ntok = (int)(((p.rows + ttiles - 1) / ttiles + 15) / 16 * 16);
+    for (a.tmem_cols = 32; a.tmem_cols < a.ntok;) a.tmem_cols *= 2;
+    const size_t stage = W_BYTES + (size_t)a.ntok * (BK * 2);
+    const bool two = a.ntok <= 128;
+    a.stages = (int)(((two ? SMEM_TWO : SMEM_ONE) - SMEM_EXTRA) / stage);
+    if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
+    for (int g = 0; g < p.groups; ++g) {
+        if ((st = make_map(&a.tw[g], p.B[g], p.kdim, p.cols, BK))) return st;
+        if (p.epi == LIN_GLU && (st = make_map(&a.tw[LIN_MAX_RANKS + g], p.B2[g], p.kdim, p.cols, BK))) return st;
+        if (g > 0 && p.A[g] == p.A[g - 1]) a.tx[g] = a.tx[g - 1];
+        else if ((st = make_map(&a.tx[g], p.A[g], p.rows, p.kdim, a.ntok))) return st;
+    }
+    const int outs = p.fused ? 1 : p.groups;
+    for (int g = 0; g < outs; ++g) {
+        a.out[g] = p.out[g];
+        a.out2[g] = static_cast<__nv_bfloat16*>(p.out2[g]);
+        a.out3[g] = static_cast<__nv_bfloat16*>(p.out3[g]);
+        a.bias[g] = static_cast<const __nv_bfloat16*>(p.bias[g]);
+        a.residual[g] = static_cast<const __nv_bfloat16*>(p.residual[g]);
+    }
+    a.keep = p.out2[0] != nullptr;
+    a.groups = p.groups;
+    a.fused = p.fused;
+    a.kb_per_group = (int)((p.kdim + BK - 1) / BK);
+    a.kbs = (p.fused ? p.groups : 1) * a.kb_per_group;
+    a.tiles = (int)((p.cols + tile_cols - 1) / tile_cols);
+    a.rows = (int)p.rows;
+    a.cols = (int)p.cols;
+    a.act = p.act;
+    a.weights_ready = weights_ready;
+    // K split: as many CTAs as fit at once, at least 4 K blocks each
+    const int64_t tiles = (int64_t)outs * a.tiles * ttiles, fit = (int64_t)sms * (two ? 2 : 1);
+    for (a.split = 1; a.split < MAX_SPLIT && tiles * a.split * 2 <= fit && a.kbs >= a.split * 2 * 4;) a.split *= 2;
+    if (tiles * a.split >= ((int64_t)1 << 31) || ttiles > 65535) return fail(RTP_ESHAPE, "%s: too many tiles", fn);
+    const dim3 grid((unsigned)(outs * a.tiles * a.split), (unsigned)ttiles, 1);
+    const size_t smem = (size_t)a.stages * stage + SMEM_EXTRA;
+    if (p.epi == LIN_GLU) return launch_t<LIN_GLU, false>(fn, a, grid, smem, stream);
+    if (p.out_f32) return launch_t<LIN_OUT, true>(fn, a, grid, smem, stream);
+    return launch_t<LIN_OUT, false>(fn, a, grid, smem, stream);
+}
+
+int take_linear_few_error(void* stream, uint32_t* code)
+{
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    unsigned int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&v, g_tp_error, sizeof v, 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_tp_error, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return fail(RTP_ECUDA, "rtp_device_error: %s", cudaGetErrorString(cudaGetLastError()));
+    *code = v;
+    return RTP_OK;
+}
+
+}  // namespace rtp
