@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import List, Optional, Sequence, Tuple, Union
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -97,16 +98,15 @@ def _load():
         "rtp_infer_sbp_signature": [c_int, c_int, i64p, c_int, c_int, i32p, i32p, i32p, i32p, i32p, i32p,
                                     P(ctypes.c_double), i32p],
         "rtp_infer_broadcast": [c_int, i32p, P(i64p), P(Spec), P(c_int), i64p, P(Spec)],
-        "rtp_tp_linear": [c_int, c_int, i64, i64, i64, vpp, vpp, vpp, vpp, c_int, c_int, vpp, vpp, vp],
-        "rtp_tp_linear_backward": [c_int, c_int, i64, i64, i64, vpp, vpp, vpp, vpp, c_int, vpp, c_int, vpp, c_int, vpp,
-                                   vpp, vp],
-        "rtp_tp_glu": [c_int, i64, i64, i64, i64, vp, vpp, vpp, vpp, vp, c_int, vpp, c_int, vp, vp],
-        "rtp_tp_glu_train_forward": [c_int, i64, i64, i64, i64, vp, vpp, vpp, vpp, vp, c_int, vpp, vpp, vpp, c_int, vp,
-                                     vp],
-        "rtp_tp_glu_backward": [c_int, i64, i64, i64, i64, vp, vpp, vpp, vpp, vpp, vpp, vpp, vp, c_int, vpp, vpp, c_int,
-                                vp, c_int, vpp, vpp, vpp, vp],
-        "rtp_grad_norm": [c_int, i32p, i64p, vpp, vp, vp, vp, vp],
-        "rtp_clip_grad_norm": [c_int, i32p, i64p, vpp, vp, ctypes.c_float, vpp, vp, vp, vp],
+        # tables of pointers are passed as void*: ctypes arrays or bytes
+        "rtp_tp_linear": [c_int, c_int, i64, i64, i64, vp, vp, vp, vp, c_int, c_int, vp, vp, vp],
+        "rtp_tp_linear_backward": [c_int, c_int, i64, i64, i64, vp, vp, vp, vp, c_int, vp, c_int, vp, c_int, vp, vp, vp],
+        "rtp_tp_glu": [c_int, i64, i64, i64, i64, vp, vp, vp, vp, vp, c_int, vp, c_int, vp, vp],
+        "rtp_tp_glu_train_forward": [c_int, i64, i64, i64, i64, vp, vp, vp, vp, vp, c_int, vp, vp, vp, c_int, vp, vp],
+        "rtp_tp_glu_backward": [c_int, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, c_int, vp, vp, c_int, vp,
+                                c_int, vp, vp, vp, vp],
+        "rtp_grad_norm": [c_int, i32p, i64p, vp, vp, vp, vp, vp],
+        "rtp_clip_grad_norm": [c_int, i32p, i64p, vp, vp, ctypes.c_float, vp, vp, vp, vp],
         "rtp_device_error": [vp, u32p],
         "rtp_wait_selftest": [c_int, ctypes.c_ulonglong, vp, vp],
         "rtp_test_hook": [c_int, ctypes.c_int64],
@@ -252,8 +252,8 @@ def _dtype_code(t) -> int:
 
 def _stream_ptr(stream) -> Optional[int]:
     torch = _torch()
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without building a Stream object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
@@ -614,6 +614,38 @@ def tp_mlp_noalloc(X, A_shards, B_shards, Z=None, stream=None):
 # ---- linear layers and the gated feed-forward block -------------------------------------
 
 ACTS = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3, "relu": 4}
+_ext = None
+
+
+def _tables():
+    """The Python extension that checks lists of tensors and tabulates their addresses."""
+    global _ext
+    if _ext is None:
+        _load()
+        _torch()  # the extension's libraries are torch's
+        try:
+            from . import _table
+        except ImportError as e:
+            raise ImportError("_table.so is not built (%s); run `python -c \"import __graft_entry__ as g; g.build()\"`"
+                              % e) from e
+        _ext = _table
+    return _ext
+
+
+def _table_of(fn: str, name: str, ts, n: int, shape, dtype, device: int) -> bytes:
+    """Addresses of the n tensors of a list as one table, each checked against the shape, type and device that the call
+    will touch (the library sees addresses only)."""
+    if len(ts) != n:
+        raise RtpError(-1, "%s: %d %s buffers given, %d expected" % (fn, len(ts), name, n))
+    code = F32 if dtype is _torch().float32 else BF16
+    got = (_ext or _tables()).table(ts, shape, code, device)
+    if type(got) is int:
+        t = ts[got]
+        if not isinstance(t, _torch().Tensor):
+            raise RtpError(-1, "%s: %s[%d] is no tensor" % (fn, name, got))
+        _buffer_error(fn, name, got, t, shape, dtype, device)
+        raise RtpError(-1, "%s: %s[%d] does not fit" % (fn, name, got))
+    return got
 
 
 def _act_code(act: str) -> int:
@@ -623,13 +655,19 @@ def _act_code(act: str) -> int:
         raise RtpError(-1, "unknown activation %r (one of %s)" % (act, ", ".join(ACTS))) from None
 
 
+def _out_dtype(given, buffer, default):
+    """The type of an output: as asked for, else as the buffer given, else the default."""
+    dtype = given or (default if buffer is None else buffer.dtype)
+    if dtype is not _torch().float32 and dtype is not _torch().bfloat16:
+        raise TypeError("rtp tensors are float32 or bfloat16, got %s" % dtype)
+    return dtype
+
+
 def _listed(t) -> list:
     """A list of rank buffers; one tensor stands for a list of one."""
-    return list(t) if isinstance(t, (list, tuple)) else [t]
-
-
-def _tensor_ptrs(ts) -> ctypes.Array:
-    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+    if type(t) is list:
+        return t
+    return list(t) if isinstance(t, tuple) else [t]
 
 
 def _matrix(fn: str, name: str, t):
@@ -638,29 +676,35 @@ def _matrix(fn: str, name: str, t):
     return t.shape
 
 
-def _new(n: int, shape, dtype, dev, stream=None) -> list:
+def _new(n: int, shape, dtype, device: int, stream=None) -> list:
     """n fresh buffers of one shape, owned by the stream the call runs on: memory that torch hands out again is ordered
     on its owning stream only, and scratch is dropped when the call returns."""
     torch = _torch()
-    if stream is not None:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
-        with torch.cuda.stream(stream):
-            return [torch.empty(shape, dtype=dtype, device=dev) for _ in range(n)]
-    return [torch.empty(shape, dtype=dtype, device=dev) for _ in range(n)]
+    code = F32 if dtype is torch.float32 else BF16
+    if stream is None:
+        return (_ext or _tables()).buffers(n, shape, code, device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(stream):
+        return _tables().buffers(n, shape, code, device)
 
 
-def _linear_shapes(fn: str, X, W_shards, split: str):
-    """(row?, X list, W list, P, M, K, N, Kp, Np) of a linear layer's arguments."""
-    if split not in ("column", "row"):
+def _slices(whole, n: int, nbytes: int) -> bytes:
+    """Addresses of n equal slices of nbytes each of one allocation (scratch that the caller does not see)."""
+    p = whole.data_ptr()
+    return struct.pack("%dQ" % n, *[p + i * nbytes for i in range(n)])
+
+
+def _linear_shapes(fn: str, X, W, split: str):
+    """(row?, P, M, K, N, Kp, Np) of a linear layer's arguments (lists)."""
+    if split != "column" and split != "row":
         raise RtpError(-1, "%s: split %r is not 'column' or 'row'" % (fn, split))
-    X, W = _listed(X), _listed(W_shards)
     if not W or not X:
         raise RtpError(-1, "%s: no weight shards or no X" % fn)
     row, P = split == "row", len(W)
     M, _ = _matrix(fn, "X", X[0])
     Kp, Np = _matrix(fn, "W_shards[0]", W[0])
-    return row, X, W, P, M, Kp * P if row else Kp, Np if row else Np * P, Kp, Np
+    return row, P, M, Kp * P if row else Kp, Np if row else Np * P, Kp, Np
 
 
 def tp_linear(X, W_shards, split: str = "column", bias=None, act: str = "none", residual=None, H=None, out=None,
@@ -673,35 +717,31 @@ def tp_linear(X, W_shards, split: str = "column", bias=None, act: str = "none", 
     single tensor stands for a list of one). All bf16; out may be float32 (out_dtype, or by `out`).
     Returns the list of outputs, or (outputs, H) with keep_h (or H given): the bf16 pre-activations that
     tp_linear_backward reads."""
-    torch = _torch()
     fn = "tp_linear"
-    bf16 = torch.bfloat16
-    row, X, W, P, M, K, N, Kp, Np = _linear_shapes(fn, X, W_shards, split)
-    outs, code = 1 if row else P, _act_code(act)
+    bf16 = _torch().bfloat16
+    X, W = _listed(X), _listed(W_shards)
+    row, P, M, K, N, Kp, Np = _linear_shapes(fn, X, W, split)
+    outs, code, shape = 1 if row else P, _act_code(act), (M, Np)
     device = _device_of(X[0])
-    if out is None:
-        out = _new(outs, (M, Np), out_dtype or bf16, X[0].device, stream)
-    else:
+    xp = _table_of(fn, "X", X, P if row else 1, (M, Kp), bf16, device)
+    wp = _table_of(fn, "W_shards", W, P, (Kp, Np), bf16, device)
+    bp = rp = hp = None
+    if bias is not None:
+        bp = _table_of(fn, "bias", _listed(bias), outs, (Np,), bf16, device)
+    if residual is not None:
+        rp = _table_of(fn, "residual", _listed(residual), outs, shape, bf16, device)
+    if out is not None:
         out = _listed(out)
-        if not out:
-            raise RtpError(-1, "%s: no out buffers" % fn)
-        out_dtype = out_dtype or out[0].dtype
-    if keep_h and H is None:
-        H = _new(outs, (M, Np), bf16, X[0].device, stream)
-    groups = [("X", X, [(M, Kp)] * (P if row else 1), bf16), ("W_shards", W, (Kp, Np), bf16),
-              ("out", out, [(M, Np)] * outs, out_dtype or bf16)]
-    ptrs = {}
-    for name, ts, shape in (("bias", bias, (Np,)), ("residual", residual, (M, Np)), ("H", H, (M, Np))):
-        if ts is not None:
-            ts = _listed(ts)
-            groups.append((name, ts, [shape] * outs, bf16))
-            ptrs[name] = ts
-    _check_buffers(fn, device, groups)
-    opt = {k: _tensor_ptrs(v) for k, v in ptrs.items()}
-    _check(_load().rtp_tp_linear(1 if row else 0, P, M, K, N, _tensor_ptrs(X), _tensor_ptrs(W), opt.get("bias"),
-                                 opt.get("residual"), code, _dtype_code(out[0]), opt.get("H"), _tensor_ptrs(out),
-                                 _stream_ptr(stream)))
-    return (out, ptrs["H"]) if "H" in ptrs else out
+    out_dtype = _out_dtype(out_dtype, out[0] if out else None, bf16)
+    if out is None:
+        out = _new(outs, shape, out_dtype, device, stream)
+    op = _table_of(fn, "out", out, outs, shape, out_dtype, device)
+    if keep_h or H is not None:
+        H = _new(outs, shape, bf16, device, stream) if H is None else _listed(H)
+        hp = _table_of(fn, "H", H, outs, shape, bf16, device)
+    _check(_lib.rtp_tp_linear(1 if row else 0, P, M, K, N, xp, wp, bp, rp, code, _dtype_code(out[0]), hp, op,
+                              _stream_ptr(stream)))
+    return (out, H) if hp is not None else out
 
 
 def tp_linear_backward(X, W_shards, dOut, split: str = "column", H=None, act: str = "none", dH=None, dX=None, dW=None,
@@ -709,70 +749,74 @@ def tp_linear_backward(X, W_shards, dOut, split: str = "column", H=None, act: st
     """Gradients of tp_linear given dOut (bf16, laid out as its outputs) and, with an activation, the kept H.
     Returns lists (dX, dW, db): dX like X, dW like W_shards (bf16, or float32 by dx_dtype / dw_dtype or by the
     buffers given), db float32 like bias (None without bias_grad). The residual's gradient is dOut."""
-    torch = _torch()
     fn = "tp_linear_backward"
-    bf16, f32 = torch.bfloat16, torch.float32
-    row, X, W, P, M, K, N, Kp, Np = _linear_shapes(fn, X, W_shards, split)
-    outs, ins, code = 1 if row else P, P if row else 1, _act_code(act)
-    dev, device = X[0].device, _device_of(X[0])
-    dOut = _listed(dOut)
-    if code and H is None:
-        raise RtpError(-1, "%s: the kept pre-activation H is needed with act=%r" % (fn, act))
-    groups = [("X", X, [(M, Kp)] * ins, bf16), ("W_shards", W, (Kp, Np), bf16), ("dOut", dOut, [(M, Np)] * outs, bf16)]
-    hp = dhp = None
+    bf16, f32 = _torch().bfloat16, _torch().float32
+    X, W = _listed(X), _listed(W_shards)
+    row, P, M, K, N, Kp, Np = _linear_shapes(fn, X, W, split)
+    outs, ins, code, shape = 1 if row else P, P if row else 1, _act_code(act), (M, Np)
+    device = _device_of(X[0])
+    xp = _table_of(fn, "X", X, ins, (M, Kp), bf16, device)
+    wp = _table_of(fn, "W_shards", W, P, (Kp, Np), bf16, device)
+    dop = _table_of(fn, "dOut", _listed(dOut), outs, shape, bf16, device)
+    hp = dhp = dbp = None
     if code:
-        H = _listed(H)
-        dH = _new(outs, (M, Np), bf16, dev, stream) if dH is None else _listed(dH)
-        groups += [("H", H, [(M, Np)] * outs, bf16), ("dH", dH, [(M, Np)] * outs, bf16)]
-    dX = _new(ins, (M, Kp), dx_dtype or bf16, dev, stream) if dX is None else _listed(dX)
-    dW = _new(P, (Kp, Np), dw_dtype or bf16, dev, stream) if dW is None else _listed(dW)
-    dx_dtype, dw_dtype = dx_dtype or dX[0].dtype, dw_dtype or dW[0].dtype
-    groups += [("dX", dX, [(M, Kp)] * ins, dx_dtype), ("dW", dW, [(Kp, Np)] * P, dw_dtype)]
+        if H is None:
+            raise RtpError(-1, "%s: the kept pre-activation H is needed with act=%r" % (fn, act))
+        hp = _table_of(fn, "H", _listed(H), outs, shape, bf16, device)
+        dH = _new(outs, shape, bf16, device, stream) if dH is None else _listed(dH)
+        dhp = _table_of(fn, "dH", dH, outs, shape, bf16, device)
+    dx_dtype = _out_dtype(dx_dtype, None if dX is None else _listed(dX)[0], bf16)
+    dw_dtype = _out_dtype(dw_dtype, None if dW is None else _listed(dW)[0], bf16)
+    dX = _new(ins, (M, Kp), dx_dtype, device, stream) if dX is None else _listed(dX)
+    dW = _new(P, (Kp, Np), dw_dtype, device, stream) if dW is None else _listed(dW)
+    dxp = _table_of(fn, "dX", dX, ins, (M, Kp), dx_dtype, device)
+    dwp = _table_of(fn, "dW", dW, P, (Kp, Np), dw_dtype, device)
     if db is not None or bias_grad:
-        db = _new(outs, (Np,), f32, dev, stream) if db is None else _listed(db)
-        groups.append(("db", db, [(Np,)] * outs, f32))
-    _check_buffers(fn, device, groups)
-    if code:
-        hp, dhp = _tensor_ptrs(H), _tensor_ptrs(dH)
-    _check(_load().rtp_tp_linear_backward(1 if row else 0, P, M, K, N, _tensor_ptrs(X), _tensor_ptrs(W), hp,
-                                          _tensor_ptrs(dOut), code, dhp, _dtype_code(dX[0]), _tensor_ptrs(dX),
-                                          _dtype_code(dW[0]), _tensor_ptrs(dW),
-                                          _tensor_ptrs(db) if db is not None else None, _stream_ptr(stream)))
+        db = _new(outs, (Np,), f32, device, stream) if db is None else _listed(db)
+        dbp = _table_of(fn, "db", db, outs, (Np,), f32, device)
+    _check(_lib.rtp_tp_linear_backward(1 if row else 0, P, M, K, N, xp, wp, hp, dop, code, dhp, _dtype_code(dX[0]), dxp,
+                                       _dtype_code(dW[0]), dwp, dbp, _stream_ptr(stream)))
     return dX, dW, db
 
 
-def _glu_shapes(fn: str, X, Ag, Au, B):
-    for name, w in (("Ag_shards", Ag), ("Au_shards", Au), ("B_shards", B)):
-        if len(w) != len(Ag) or not w:
-            raise RtpError(-1, "%s: %d %s for %d ranks" % (fn, len(w), name, len(Ag)))
+def _glu_weights(fn: str, X, Ag, Au, B):
+    """(P, M, K, Fp, N, device, tables of X, Ag, Au, B) of the gated block's arguments."""
+    bf16 = _torch().bfloat16
+    P = len(Ag)
+    if not P or not B:
+        raise RtpError(-1, "%s: no weight shards" % fn)
     M, K = _matrix(fn, "X", X)
     _, Fp = _matrix(fn, "Ag_shards[0]", Ag[0])
     _, N = _matrix(fn, "B_shards[0]", B[0])
-    bf16 = _torch().bfloat16
-    return M, K, Fp, N, [("X", [X], (M, K), bf16), ("Ag_shards", Ag, (K, Fp), bf16), ("Au_shards", Au, (K, Fp), bf16),
-                         ("B_shards", B, (Fp, N), bf16)]
+    device = _device_of(X)
+    _table_of(fn, "X", [X], 1, (M, K), bf16, device)
+    return (P, M, K, Fp, N, device, _table_of(fn, "Ag_shards", Ag, P, (K, Fp), bf16, device),
+            _table_of(fn, "Au_shards", Au, P, (K, Fp), bf16, device),
+            _table_of(fn, "B_shards", B, P, (Fp, N), bf16, device))
 
 
 def _glu_forward(fn, X, Ag, Au, B, act, residual, kept, Z, out_dtype, stream):
     """kept: [Y] or [Y, Hg, Hu], each a list of P buffers or None. Returns (Z, kept)."""
-    torch = _torch()
-    bf16 = torch.bfloat16
-    P = len(Ag)
-    M, K, Fp, N, groups = _glu_shapes(fn, X, Ag, Au, B)
-    code, device = _act_code(act), _device_of(X)
+    bf16 = _torch().bfloat16
+    code = _act_code(act)
+    P, M, K, Fp, N, device, agp, aup, bp = _glu_weights(fn, X, Ag, Au, B)
+    out_dtype = _out_dtype(out_dtype, Z, bf16)
     if Z is None:
-        Z, = _new(1, (M, N), out_dtype or bf16, X.device, stream)
-    kept = [_new(P, (M, Fp), bf16, X.device, stream) if k is None else _listed(k) for k in kept]
-    groups.append(("Z", [Z], (M, N), out_dtype or Z.dtype))
+        Z, = _new(1, (M, N), out_dtype, device, stream)
+    _table_of(fn, "Z", [Z], 1, (M, N), out_dtype, device)
+    rp = None
     if residual is not None:
-        groups.append(("residual", [residual], (M, N), bf16))
-    for name, k in zip(("Y", "Hg", "Hu"), kept):
-        groups.append((name, k, [(M, Fp)] * P, bf16))
-    _check_buffers(fn, device, groups)
-    call = _load().rtp_tp_glu if len(kept) == 1 else _load().rtp_tp_glu_train_forward
-    _check(call(P, M, K, Fp * P, N, X.data_ptr(), _tensor_ptrs(Ag), _tensor_ptrs(Au), _tensor_ptrs(B),
-                residual.data_ptr() if residual is not None else None, code, *[_tensor_ptrs(k) for k in kept],
-                _dtype_code(Z), Z.data_ptr(), _stream_ptr(stream)))
+        _table_of(fn, "residual", [residual], 1, (M, N), bf16, device)
+        rp = residual.data_ptr()
+    if len(kept) == 1 and kept[0] is None:  # Y as scratch
+        scratch, = _new(1, (P, M, Fp), bf16, device, stream)
+        kp = [_slices(scratch, P, 2 * M * Fp)]
+    else:
+        kept = [_new(P, (M, Fp), bf16, device, stream) if k is None else _listed(k) for k in kept]
+        kp = [_table_of(fn, name, k, P, (M, Fp), bf16, device) for name, k in zip(("Y", "Hg", "Hu"), kept)]
+    call = _lib.rtp_tp_glu if len(kp) == 1 else _lib.rtp_tp_glu_train_forward
+    _check(call(P, M, K, Fp * P, N, X.data_ptr(), agp, aup, bp, rp, code, *kp, _dtype_code(Z), Z.data_ptr(),
+                _stream_ptr(stream)))
     return Z, kept
 
 
@@ -799,32 +843,29 @@ def tp_glu_backward(X, Ag_shards, Au_shards, B_shards, Hg, Hu, Y, dZ, act: str =
     """Gradients of the gated block given dZ (bf16 [M, N]) and what tp_glu_train_forward kept. Returns (dX, dAg, dAu,
     dB): dX [M, K] and lists of P weight gradients, bf16 or float32 (dx_dtype, dw_dtype, or by the buffers given). The
     residual's gradient is dZ. dHg, dHu: P bf16 [M, F/P] scratch buffers each."""
-    torch = _torch()
     fn = "tp_glu_backward"
-    bf16 = torch.bfloat16
-    Ag, Au, B = _listed(Ag_shards), _listed(Au_shards), _listed(B_shards)
-    P, dev = len(Ag), X.device
-    M, K, Fp, N, groups = _glu_shapes(fn, X, Ag, Au, B)
-    code, device = _act_code(act), _device_of(X)
-    mid = [(n, _new(P, (M, Fp), bf16, dev, stream) if t is None else _listed(t))
-           for n, t in (("Hg", Hg), ("Hu", Hu), ("Y", Y), ("dHg", dHg), ("dHu", dHu))]
+    bf16 = _torch().bfloat16
+    code = _act_code(act)
+    P, M, K, Fp, N, device, agp, aup, bp = _glu_weights(fn, X, _listed(Ag_shards), _listed(Au_shards), _listed(B_shards))
     if Hg is None or Hu is None or Y is None:
         raise RtpError(-1, "%s: Hg, Hu and Y of the training forward are needed" % fn)
+    mid = [(name, _new(P, (M, Fp), bf16, device, stream) if t is None else _listed(t))
+           for name, t in (("Hg", Hg), ("Hu", Hu), ("Y", Y), ("dHg", dHg), ("dHu", dHu))]
+    hg, hu, y, dhg, dhu = (_table_of(fn, name, t, P, (M, Fp), bf16, device) for name, t in mid)
+    _table_of(fn, "dZ", [dZ], 1, (M, N), bf16, device)
+    dx_dtype = _out_dtype(dx_dtype, dX, bf16)
     if dX is None:
-        dX, = _new(1, (M, K), dx_dtype or bf16, dev, stream)
-    dw = [_new(P, s, dw_dtype or bf16, dev, stream) if t is None else _listed(t)
+        dX, = _new(1, (M, K), dx_dtype, device, stream)
+    _table_of(fn, "dX", [dX], 1, (M, K), dx_dtype, device)
+    given = [t for t in (dAg, dAu, dB) if t is not None]
+    dw_dtype = _out_dtype(dw_dtype, _listed(given[0])[0] if given else None, bf16)
+    dw = [_new(P, s, dw_dtype, device, stream) if t is None else _listed(t)
           for t, s in ((dAg, (K, Fp)), (dAu, (K, Fp)), (dB, (Fp, N)))]
-    dw_dtype = dw_dtype or dw[0][0].dtype
-    groups += [(n, t, [(M, Fp)] * P, bf16) for n, t in mid]
-    groups += [("dZ", [dZ], (M, N), bf16), ("dX", [dX], (M, K), dx_dtype or dX.dtype),
-               ("dAg", dw[0], [(K, Fp)] * P, dw_dtype), ("dAu", dw[1], [(K, Fp)] * P, dw_dtype),
-               ("dB", dw[2], [(Fp, N)] * P, dw_dtype)]
-    _check_buffers(fn, device, groups)
-    hg, hu, y, dhg, dhu = (_tensor_ptrs(t) for _, t in mid)
-    _check(_load().rtp_tp_glu_backward(P, M, K, Fp * P, N, X.data_ptr(), _tensor_ptrs(Ag), _tensor_ptrs(Au),
-                                       _tensor_ptrs(B), hg, hu, y, dZ.data_ptr(), code, dhg, dhu, _dtype_code(dX),
-                                       dX.data_ptr(), _dtype_code(dw[0][0]), *[_tensor_ptrs(t) for t in dw],
-                                       _stream_ptr(stream)))
+    dwp = [_table_of(fn, name, t, P, s, dw_dtype, device)
+           for name, t, s in (("dAg", dw[0], (K, Fp)), ("dAu", dw[1], (K, Fp)), ("dB", dw[2], (Fp, N)))]
+    _check(_lib.rtp_tp_glu_backward(P, M, K, Fp * P, N, X.data_ptr(), agp, aup, bp, hg, hu, y, dZ.data_ptr(), code, dhg,
+                                    dhu, _dtype_code(dX), dX.data_ptr(), _dtype_code(dw[0][0]), *dwp,
+                                    _stream_ptr(stream)))
     return (dX, *dw)
 
 
@@ -884,7 +925,7 @@ class GradGroup:
         if torch.cuda.current_device() != self.device.index:
             raise RtpError(-1, "GradGroup: tensors are on %s but the current CUDA device is %d" % (
                 self.device, torch.cuda.current_device()))
-        return _new(1, (), torch.float32, self.device, stream)[0]
+        return _new(1, (), torch.float32, self.device.index, stream)[0]
 
     def norm(self, stream=None):
         """The global norm, a float32 scalar tensor on the GPU."""
@@ -899,13 +940,16 @@ class GradGroup:
         norm = self._begin(stream)
         optr = None
         if out is not None:
+            out = _listed(out)
             if len(out) != len(self.grads):
                 raise RtpError(-1, "GradGroup: %d out tensors for %d gradients" % (len(out), len(self.grads)))
-            for i, (o, g) in enumerate(zip(out, self.grads)):
-                if o.dtype is not g.dtype or o.shape != g.shape or not o.is_contiguous() or o.device != self.device:
-                    raise RtpError(-2, "GradGroup: out[%d] is %s %s on %s, expected contiguous %s %s on %s" % (
-                        i, o.dtype, tuple(o.shape), o.device, g.dtype, tuple(g.shape), self.device))
-            optr = _ptrs([o.data_ptr() for o in out])
+            optr = _tables().like(out, self.grads, self.device.index)
+            if type(optr) is int:
+                o, g = out[optr], self.grads[optr]
+                if not isinstance(o, _torch().Tensor):
+                    raise RtpError(-1, "GradGroup: out[%d] is no tensor" % optr)
+                raise RtpError(-2, "GradGroup: out[%d] is %s %s on %s, expected contiguous %s %s on %s" % (
+                    optr, o.dtype, tuple(o.shape), o.device, g.dtype, tuple(g.shape), self.device))
         _check(_load().rtp_clip_grad_norm(len(self.grads), self._dtypes, self._numels, self._ptrs, self._counted,
                                           float(max_norm), optr, self._ws.data_ptr(), norm.data_ptr(),
                                           _stream_ptr(stream)))

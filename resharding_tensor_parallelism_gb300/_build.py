@@ -1,7 +1,7 @@
 """Builds librtp.so in-tree: host C++ with g++, CUDA with nvcc for sm_103a only.
 
 Translation units compile in parallel; the result links the CUDA runtime
-statically. Object files go to ``_build/`` next to this file.
+statically. A small Python extension (_table.so) is built beside it. Object files go to ``_build/`` next to this file.
 """
 from __future__ import annotations
 
@@ -16,6 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librtp.so")
+TABLE = os.path.join(HERE, "_table.so")  # Python extension: pointer tables of checked tensors
 
 HOST_SOURCES = ["spec.cpp", "plan.cpp", "infer.cpp"]
 CUDA_SOURCES = ["boxing.cu", "tp_mlp.cu", "tp_mlp_static.cu", "linear.cu", "linear_gemm.cu", "linear_few.cu", "grad_norm.cu"]
@@ -41,9 +42,21 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _table_command(target: str) -> list:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+
+    inc = [a for p in ext.include_paths() + [sysconfig.get_paths()["include"]] for a in ("-isystem", p)]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared", *inc,
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, os.path.join(CSRC, "table.cpp"), "-o", target,
+            "-L", ext.library_paths()[0], "-lc10", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     deps = _deps() + [os.path.abspath(__file__)]
-    if not force and not _stale(LIB, deps):
+    if not force and not _stale(LIB, deps) and not _stale(TABLE, deps):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -61,6 +74,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             cmd.insert(1, "-Xptxas=-v")
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         objs.append(obj)
+    table_tmp = TABLE + ".tmp%d" % os.getpid()
+    cmd = _table_command(table_tmp)
+    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for cmd, p in procs:
         out, _ = p.communicate()
@@ -75,6 +91,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     tmp = LIB + ".tmp%d" % os.getpid()
     subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    os.replace(table_tmp, TABLE)
     return LIB
 
 
