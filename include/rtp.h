@@ -501,8 +501,9 @@ enum { RTP_SPLIT_COLUMN = 0, RTP_SPLIT_ROW = 1 };
  * aligned, no overlap of outputs with anything (RTP_EINVAL for the alignment; an
  * overlap is not detected). M == 0 launches nothing, and buffers of M rows may then
  * be NULL. Errors leave nothing launched; nothing is allocated; results do not
- * change from run to run. Up to 256 rows run in a kernel of their own, which cuts
- * K over a cluster, so a row's bits may depend on how many rows go with it.
+ * change from run to run.
+ * A product with few rows or few tiles cuts its K range over a cluster of SMs, so a
+ * row's bits may depend on how many rows go with it.
  * Like the GEMMs of rtp_tp_mlp, the products are launched as programmatic
  * dependents and wait for the previous kernel of the stream.
  */

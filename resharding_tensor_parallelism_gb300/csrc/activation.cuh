@@ -13,7 +13,9 @@ namespace rtp {
 
 namespace {
 
-__device__ __forceinline__ float logistic(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
+// 1 / (1 + e^-v) with the fast exponential and quotient: 2 + 1.2 |v| and 2 ulp, which
+// is below 2^-19 relative where the result is above 2^-24, far below bf16's 2^-9
+__device__ __forceinline__ float logistic(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
 constexpr float kTanhScale = 1.5957691216057307f;  // 2 sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;

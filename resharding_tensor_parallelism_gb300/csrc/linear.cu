@@ -109,10 +109,12 @@ int launch_act_grad(const char* fn, const SumArgs& a, int groups, cudaStream_t s
     return RTP_OK;
 }
 
-// Which kernel runs a forward product: the few-row kernel up to 256 rows.
+// A forward product: the few-row kernel up to LIN_FEW_ROWS rows (measured on
+// products of 2048 x 2048 to 8192 x 28672: at 128 rows it takes 0.35 to 0.9 of the
+// pair kernel's time), the pair kernel beyond.
 int forward(const char* fn, const LinGemm& p, bool weights_ready, cudaStream_t stream)
 {
-    if (p.rows <= 256) return launch_linear_few(fn, p, weights_ready, stream);
+    if (p.rows <= LIN_FEW_ROWS) return launch_linear_few(fn, p, weights_ready, stream);
     return launch_linear_gemm(fn, p, stream);
 }
 
@@ -351,7 +353,7 @@ int glu_impl(const char* fn, int P, int64_t M, int64_t K, int64_t F, int64_t N, 
     g2.residual[0] = residual;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     TRY(forward(fn, g1, false, stream));
-    // g1's kernel waits for its predecessors and does not write B, so B is ready
+    // g1's kernels wait for their predecessors and do not write B, so B is ready
     return forward(fn, g2, true, stream);
 }
 

@@ -43,13 +43,15 @@ struct LinGemm {
 
 // The 2-SM pair kernel (linear_gemm.cu): any LinGemm.
 int launch_linear_gemm(const char* fn, const LinGemm& g, cudaStream_t stream);
-// The few-row kernel (linear_few.cu): LIN_OUT and LIN_GLU without transposed
-// operands. weights_ready: nothing queued on the stream since a kernel that
-// waited for its own predecessor writes B, so B may be read before the previous
-// kernel has finished.
+// The few-row kernel (linear_few.cu): LIN_OUT and LIN_GLU, at most
+// LIN_FEW_ROWS rows, no transposed operands. weights_ready: nothing queued on the
+// stream since a kernel that waited for its own predecessor writes B, so B may be
+// read before the previous kernel has finished.
+constexpr int LIN_FEW_ROWS = 128;
 int launch_linear_few(const char* fn, const LinGemm& g, bool weights_ready, cudaStream_t stream);
 
 int take_linear_gemm_error(void* stream, uint32_t* code);
+int take_linear_split_error(void* stream, uint32_t* code);
 int take_linear_few_error(void* stream, uint32_t* code);
 
 }  // namespace rtp

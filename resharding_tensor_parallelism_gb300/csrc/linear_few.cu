@@ -1,19 +1,17 @@
-// The same products for few rows (a token or a small batch being decoded, short
-// prompts): out^T = W^T X^T with the weights as the M operand and the rows
-// ("tokens") as the N operand of the MMA.
+// The same products for few rows (a token or a small batch being decoded), computed
+// transposed, out^T = B^T A^T: 128 output columns ("features") of a CTA are the M
+// operand of the MMA, the rows ("tokens"), up to 128 in steps of 16, its N operand.
+// For LIN_GLU a CTA's 128 features are 64 gate and the same 64 up columns.
 //
-// With few tokens every weight is used a handful of times, so the bytes of the
-// weights over the HBM rate bound the time, and the tile of the pair kernel
-// would leave most of its rows, and with few columns most SMs, idle. Here a CTA
-// multiplies 128 weight columns (64 gate and the same 64 up columns for LIN_GLU)
-// with a tile of up to 256 tokens: tcgen05.mma M = 128, N = tokens rounded up to
-// 16, K = 16 a step. The weight tile is used straight from its row-major form (an
-// M-major A operand), so no weight is laid out anew. The K range (all ranks' K
-// ranges when the ranks are summed) is cut over a cluster of up to 8 CTAs: each
-// holds a float32 partial of the tile in its shared memory, and the CTAs then add
-// up slices of it over distributed shared memory in cluster-rank order, so the
-// result does not depend on timing and no workspace is needed. Two CTAs fit on
-// an SM for up to 128 tokens, so that about 190 KB of loads are in flight per SM.
+// With few tokens every weight is used a handful of times, so the weights' bytes
+// over the HBM rate bound the time, and the tiles of the pair kernel would leave
+// most of their rows, and with few columns most SMs, idle. Weights are used straight
+// from their row-major form (an M-major operand). The K range (all ranks' K ranges
+// when the ranks are summed) is cut into `split` parts over a cluster of CTAs: each
+// part's float32 partial tile goes to its CTA's shared memory, and the CTAs then add
+// up slices of it over distributed shared memory in the order of the parts, so the
+// result does not depend on timing and no workspace is needed. Two CTAs fit on an
+// SM, so that about 190 KB of loads are in flight on it.
 #include <atomic>
 #include <cstring>
 
@@ -25,25 +23,24 @@ namespace rtp {
 
 namespace {
 
-constexpr int FEAT = 128;                      // weight columns (MMA rows) of a tile
+constexpr int FEAT = 128;                      // features of a CTA's tile
 constexpr uint32_t SUB = 64 * BK * 2;          // one 64 x 64 box, 8 KB
 constexpr uint32_t W_BYTES = FEAT * BK * 2;    // 16 KB
-constexpr int THREADS = 128;
+constexpr int THREADS = 256;                   // warps w and w + 4 read the same quarter of the tensor memory's lanes
 constexpr int MAX_STAGES = 8;
 constexpr int MAX_SPLIT = 8;                   // portable cluster size
-constexpr size_t SMEM_TWO = 113 * 1024;        // per CTA, two on an SM (228 KB, 1 KB reserved per CTA)
-constexpr size_t SMEM_ONE = 227 * 1024;
+constexpr size_t SMEM_LIMIT = 113 * 1024;      // per CTA, two on an SM (228 KB, 1 KB reserved per CTA)
 constexpr size_t SMEM_EXTRA = 1024 + 256;      // alignment; barriers
 
 struct Args {
-    CUtensorMap tw[LIN_MAX_GROUPS];  // weights; LIN_GLU: [g] gate, [LIN_MAX_RANKS + g] up
-    CUtensorMap tx[LIN_MAX_RANKS];
+    CUtensorMap tw[LIN_MAX_GROUPS];  // B operands; LIN_GLU: [g] gate, [LIN_MAX_RANKS + g] up
+    CUtensorMap tx[LIN_MAX_RANKS];   // A operands
     void* out[LIN_MAX_RANKS];
     __nv_bfloat16* out2[LIN_MAX_RANKS];
     __nv_bfloat16* out3[LIN_MAX_RANKS];
     const __nv_bfloat16* bias[LIN_MAX_RANKS];
     const __nv_bfloat16* residual[LIN_MAX_RANKS];
-    int32_t groups, fused, kb_per_group, kbs;
+    int32_t fused, kb_per_group, kbs;
     int32_t tiles;  // feature tiles of a group
     int32_t rows, cols, ntok, tmem_cols;
     int32_t split, stages;
@@ -87,8 +84,13 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr)
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(cluster_addr)
-                 : "memory");
+                 : "r"(cluster_addr));
+    return v;
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
 }
 __device__ __forceinline__ float4 bf16x4(const __nv_bfloat16* p)
@@ -101,28 +103,28 @@ __device__ __forceinline__ void store_bf16x4(__nv_bfloat16* p, float4 v)
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 __device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+__device__ __forceinline__ float4 mul4(float4 a, float4 b) { return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w); }
 
 template <int EPI, bool F32>
-__global__ void __launch_bounds__(THREADS) linear_few_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_constant__ Args a)
 {
-    constexpr int TILE_COLS = EPI == LIN_GLU ? FEAT / 2 : FEAT;
+    constexpr int CTA_COLS = EPI == LIN_GLU ? FEAT / 2 : FEAT;  // output columns of a CTA
     extern __shared__ uint8_t smem_raw[];
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t x_bytes = (uint32_t)a.ntok * (BK * 2), stage_bytes = W_BYTES + x_bytes;
+    const uint32_t stage_bytes = W_BYTES + (uint32_t)a.ntok * (BK * 2);
     const uint32_t bar0 = smem + (uint32_t)a.stages * stage_bytes;
     auto full_bar = [&](int s) { return bar0 + 8u * (uint32_t)s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (uint32_t)(MAX_STAGES + s); };
     const uint32_t acc_bar = bar0 + 8u * (uint32_t)(2 * MAX_STAGES), drain_bar = acc_bar + 8u;
-    const uint32_t word0 = bar0 - smem_u32(smem_raw) + 8u * (2 * MAX_STAGES + 2);
-    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem_raw + word0);
+    volatile uint32_t* tmem_slot =
+        reinterpret_cast<volatile uint32_t*>(smem_raw + (bar0 - smem_u32(smem_raw)) + 8u * (2 * MAX_STAGES + 2));
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cr = (int)cluster_rank();
-    const int tile = (int)blockIdx.x / a.split;
-    const int g = tile / a.tiles, f0 = (tile - g * a.tiles) * TILE_COLS;
-    const int t0 = (int)blockIdx.y * a.ntok;
-    const int kb0 = (int)((int64_t)a.kbs * cr / a.split), kb1 = (int)((int64_t)a.kbs * (cr + 1) / a.split);
+    const int part = (int)cluster_rank();  // K part
+    const int tile = (int)blockIdx.x / a.split, g = tile / a.tiles, f0 = (tile - g * a.tiles) * CTA_COLS;
+    const int kb0 = (int)((int64_t)a.kbs * part / a.split), kb1 = (int)((int64_t)a.kbs * (part + 1) / a.split);
+    const int n = kb1 - kb0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(full_bar(s), 1);
@@ -146,7 +148,6 @@ __global__ void __launch_bounds__(THREADS) linear_few_kernel(const __grid_consta
 
     if (warp == 0) {
         if (lane == 0) {
-            const int n = kb1 - kb0;
             auto load_w = [&](int i, int s) {
                 const int kb = kb0 + i, kg = a.fused ? kb / a.kb_per_group : 0;
                 const int k = (kb - kg * a.kb_per_group) * BK, wg = a.fused ? kg : g;
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(THREADS) linear_few_kernel(const __grid_consta
             auto load_x = [&](int i, int s) {
                 const int kb = kb0 + i, kg = a.fused ? kb / a.kb_per_group : 0;
                 tma_load_2d(smem + (uint32_t)s * stage_bytes + W_BYTES, &a.tx[a.fused ? kg : g], full_bar(s),
-                            (kb - kg * a.kb_per_group) * BK, t0);
+                            (kb - kg * a.kb_per_group) * BK, 0);
             };
             // Weights that nothing on the stream can still be writing are fetched
             // while the previous kernel finishes.
@@ -199,11 +200,14 @@ __global__ void __launch_bounds__(THREADS) linear_few_kernel(const __grid_consta
         if (lane == 0) {
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | ((uint32_t)(a.ntok >> 3) << 17) |
                                    ((uint32_t)(FEAT >> 4) << 24);
+            // weights M-major: 2048-byte steps (16 K rows), the two 64-wide boxes SUB
+            // bytes apart; tokens K-major: 32-byte steps (16 bf16) in the 128-byte
+            // swizzle row, 8-row groups 1024 bytes apart
             const uint64_t desc_w = smem_desc(smem, SUB, 1024u), desc_x = smem_desc(smem + W_BYTES, 16u, 1024u);
             int s = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int i = 0; i < kb1 - kb0; ++i) {
+            for (int i = 0; i < n; ++i) {
                 if (!wait_bar(full_bar(s), phase, abort_flag, ERR_MMA_STAGE)) {
                     ok = false;
                     break;
@@ -237,61 +241,78 @@ __global__ void __launch_bounds__(THREADS) linear_few_kernel(const __grid_consta
     int ok = 1;
     if (lane == 0) ok = wait_bar(acc_bar, 0, abort_flag, ERR_EPILOGUE) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
-    const int mtok = min(a.ntok, a.rows - t0);
+    tc_fence_after();
     if (ok) {
-        tc_fence_after();
-        const uint32_t taddr = tmem_base + ((uint32_t)(warp * 32) << 16);
-        for (int c = 0; c < mtok; c += 16) {
+        const int quarter = warp & 3;
+        const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16);
+        for (int c = 16 * (warp >> 2); c < a.rows; c += 16 * (THREADS / 128)) {
             uint32_t r[16];
             tmem_ld_16cols(taddr + (uint32_t)c, r);
-            const uint32_t dst = smem + 4u * (uint32_t)(c * FEAT + warp * 32 + lane);
+            const uint32_t dst = smem + 4u * (uint32_t)(c * FEAT + quarter * 32 + lane);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 4u * FEAT * j), "r"(r[j]) : "memory");
         }
     }
     tc_fence_before();
-    cluster_sync();
+    if (a.split > 1) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(a.tmem_cols) : "memory");
-
-    // A thread takes 4 neighbouring output columns of one token.
-    constexpr int QUADS = TILE_COLS / 4;
+    // A thread takes 4 neighbouring output columns of one token, UNROLL such quads
+    // at a time: the loads of the other operands, then of the partials, of all of
+    // them are in flight together (one by one, each cost its full latency: the
+    // epilogue of 256 tokens took 50 us).
+    constexpr int QUADS = CTA_COLS / 4, UNROLL = 4;
+    const int step = a.split * THREADS, items = a.rows * QUADS;
     auto sum4 = [&](int t, int f) {
         const uint32_t addr = smem + 4u * (uint32_t)(t * FEAT + f);
+        if (a.split == 1) return ld_shared_f4(addr);
         float4 v = ld_cluster_f4(map_to_rank(addr, 0));
         for (int r = 1; r < a.split; ++r) v = add4(v, ld_cluster_f4(map_to_rank(addr, (uint32_t)r)));
         return v;
     };
-    for (int i = cr * THREADS + (int)threadIdx.x; i < mtok * QUADS; i += a.split * THREADS) {
-        const int t = i / QUADS, f = (i - t * QUADS) * 4, col = f0 + f;
-        if (col >= a.cols) continue;
-        const int64_t at = (int64_t)(t0 + t) * a.cols + col;
-        float4 v = sum4(t, f);
-        if constexpr (EPI == LIN_GLU) {
-            const float4 u = sum4(t, 64 + f);
-            if (a.keep) {
-                store_bf16x4(a.out2[g] + at, v);
-                store_bf16x4(a.out3[g] + at, u);
+    for (int i0 = part * THREADS + (int)threadIdx.x; i0 < items; i0 += UNROLL * step) {
+        float4 v[UNROLL], u[UNROLL], x[UNROLL];
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j) {
+            const int i = i0 + j * step, t = i / QUADS, f = (i - t * QUADS) * 4;
+            v[j] = u[j] = x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i >= items || f0 + f >= a.cols) continue;
+            if constexpr (EPI == LIN_OUT) {
+                if (a.bias[g]) u[j] = bf16x4(a.bias[g] + f0 + f);
+                if (a.residual[g]) x[j] = bf16x4(a.residual[g] + (int64_t)t * a.cols + f0 + f);
+            }
+            v[j] = sum4(t, f);
+            if constexpr (EPI == LIN_GLU) u[j] = sum4(t, 64 + f);
+        }
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j) {
+            const int i = i0 + j * step, t = i / QUADS, f = (i - t * QUADS) * 4;
+            if (i >= items || f0 + f >= a.cols) continue;
+            const int64_t at = (int64_t)t * a.cols + f0 + f;
+            if constexpr (EPI == LIN_GLU) {
+                if (a.keep) {
+                    store_bf16x4(a.out2[g] + at, v[j]);
+                    store_bf16x4(a.out3[g] + at, u[j]);
+                }
+            } else {
+                v[j] = add4(v[j], u[j]);
+                if (a.keep) store_bf16x4(a.out2[g] + at, v[j]);
             }
             with_act(a.act, [&](auto tag) {
                 constexpr int ACT = decltype(tag)::value;
-                v = make_float4(act_value<ACT>(v.x) * u.x, act_value<ACT>(v.y) * u.y, act_value<ACT>(v.z) * u.z,
-                                act_value<ACT>(v.w) * u.w);
+                v[j] = make_float4(act_value<ACT>(v[j].x), act_value<ACT>(v[j].y), act_value<ACT>(v[j].z),
+                                   act_value<ACT>(v[j].w));
             });
-        } else {
-            if (a.bias[g]) v = add4(v, bf16x4(a.bias[g] + col));
-            if (a.keep) store_bf16x4(a.out2[g] + at, v);
-            with_act(a.act, [&](auto tag) {
-                constexpr int ACT = decltype(tag)::value;
-                v = make_float4(act_value<ACT>(v.x), act_value<ACT>(v.y), act_value<ACT>(v.z), act_value<ACT>(v.w));
-            });
-            if (a.residual[g]) v = add4(v, bf16x4(a.residual[g] + at));
+            v[j] = EPI == LIN_GLU ? mul4(v[j], u[j]) : add4(v[j], x[j]);
+            if constexpr (F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out[g]) + at) = v[j];
+            else store_bf16x4(static_cast<__nv_bfloat16*>(a.out[g]) + at, v[j]);
         }
-        if constexpr (F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out[g]) + at) = v;
-        else store_bf16x4(static_cast<__nv_bfloat16*>(a.out[g]) + at, v);
     }
-    cluster_sync();  // no CTA leaves while a peer may still read its partial
+    // No CTA leaves while a peer may still read its partial.
+    if (a.split > 1) cluster_sync();
 }
 
 // ---- host side --------------------------------------------------------------------
@@ -311,13 +332,14 @@ int sm_count(int* n)
 }
 
 template <int EPI, bool F32>
-int launch_t(const char* fn, const Args& args, dim3 grid, size_t smem, cudaStream_t stream)
+int launch_t(const char* fn, const Args& args, unsigned tiles, size_t smem, cudaStream_t stream)
 {
     static std::atomic<bool> ready[64];
+    auto kernel = linear_few_kernel<EPI, F32>;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
     if (!ready[dev].load(std::memory_order_acquire)) {
-        cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<EPI, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_ONE);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_LIMIT);
         if (e != cudaSuccess) return fail(RTP_ECUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
         ready[dev].store(true, std::memory_order_release);
     }
@@ -329,13 +351,13 @@ int launch_t(const char* fn, const Args& args, dim3 grid, size_t smem, cudaStrea
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(tiles * (unsigned)args.split);
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, linear_few_kernel<EPI, F32>, args);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
     if (e != cudaSuccess) return fail(RTP_ECUDA, "%s: few-row launch failed: %s", fn, cudaGetErrorString(e));
     return RTP_OK;
 }
@@ -344,18 +366,16 @@ int launch_t(const char* fn, const Args& args, dim3 grid, size_t smem, cudaStrea
 
 int launch_linear_few(const char* fn, const LinGemm& p, bool weights_ready, cudaStream_t stream)
 {
-    int sms = 0, st;
+    int st, sms = 0;
     if (sm_count(&sms)) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
     static thread_local Args a;
     std::memset(&a, 0, sizeof a);
-    const int tile_cols = p.epi == LIN_GLU ? FEAT / 2 : FEAT;
-    // equal token tiles of at most 256, rounded up to the MMA's step of 16
-    const int ttiles = (int)((p.rows + 255) / 256);
-    a.ntok = (int)(((p.rows + ttiles - 1) / ttiles + 15) / 16 * 16);
+    const int cta_cols = p.epi == LIN_GLU ? FEAT / 2 : FEAT;
+    a.ntok = (int)((p.rows + 15) / 16 * 16);
     for (a.tmem_cols = 32; a.tmem_cols < a.ntok;) a.tmem_cols *= 2;
+    // the ring also has to hold a partial tile (512 bytes a token): 64 KB of at least 96
     const size_t stage = W_BYTES + (size_t)a.ntok * (BK * 2);
-    const bool two = a.ntok <= 128;
-    a.stages = (int)(((two ? SMEM_TWO : SMEM_ONE) - SMEM_EXTRA) / stage);
+    a.stages = (int)((SMEM_LIMIT - SMEM_EXTRA) / stage);
     if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
     for (int g = 0; g < p.groups; ++g) {
         if ((st = make_map(&a.tw[g], p.B[g], p.kdim, p.cols, BK))) return st;
@@ -372,24 +392,22 @@ int launch_linear_few(const char* fn, const LinGemm& p, bool weights_ready, cuda
         a.residual[g] = static_cast<const __nv_bfloat16*>(p.residual[g]);
     }
     a.keep = p.out2[0] != nullptr;
-    a.groups = p.groups;
     a.fused = p.fused;
     a.kb_per_group = (int)((p.kdim + BK - 1) / BK);
     a.kbs = (p.fused ? p.groups : 1) * a.kb_per_group;
-    a.tiles = (int)((p.cols + tile_cols - 1) / tile_cols);
+    a.tiles = (int)((p.cols + cta_cols - 1) / cta_cols);
     a.rows = (int)p.rows;
     a.cols = (int)p.cols;
     a.act = p.act;
     a.weights_ready = weights_ready;
-    // K split: as many CTAs as fit at once, at least 4 K blocks each
-    const int64_t tiles = (int64_t)outs * a.tiles * ttiles, fit = (int64_t)sms * (two ? 2 : 1);
-    for (a.split = 1; a.split < MAX_SPLIT && tiles * a.split * 2 <= fit && a.kbs >= a.split * 2 * 4;) a.split *= 2;
-    if (tiles * a.split >= ((int64_t)1 << 31) || ttiles > 65535) return fail(RTP_ESHAPE, "%s: too many tiles", fn);
-    const dim3 grid((unsigned)(outs * a.tiles * a.split), (unsigned)ttiles, 1);
+    const int64_t tiles = (int64_t)outs * a.tiles;
+    if (tiles * MAX_SPLIT >= ((int64_t)1 << 31)) return fail(RTP_ESHAPE, "%s: too many tiles", fn);
+    // K parts: as many CTAs as fit at once (two on an SM), at least 4 K blocks each
+    for (a.split = 1; a.split < MAX_SPLIT && tiles * a.split * 2 <= 2 * sms && a.kbs >= a.split * 2 * 4;) a.split *= 2;
     const size_t smem = (size_t)a.stages * stage + SMEM_EXTRA;
-    if (p.epi == LIN_GLU) return launch_t<LIN_GLU, false>(fn, a, grid, smem, stream);
-    if (p.out_f32) return launch_t<LIN_OUT, true>(fn, a, grid, smem, stream);
-    return launch_t<LIN_OUT, false>(fn, a, grid, smem, stream);
+    if (p.epi == LIN_GLU) return launch_t<LIN_GLU, false>(fn, a, (unsigned)tiles, smem, stream);
+    return p.out_f32 ? launch_t<LIN_OUT, true>(fn, a, (unsigned)tiles, smem, stream)
+                     : launch_t<LIN_OUT, false>(fn, a, (unsigned)tiles, smem, stream);
 }
 
 int take_linear_few_error(void* stream, uint32_t* code)
