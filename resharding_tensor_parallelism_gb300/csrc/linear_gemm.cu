@@ -64,6 +64,7 @@ int launch_linear_gemm(const char* fn, const LinGemm& p, cudaStream_t stream)
     for (int g = 0; g < LIN_MAX_RANKS; ++g) {
         a.bias[g] = static_cast<const __nv_bfloat16*>(p.bias[g]);
         a.residual[g] = static_cast<const __nv_bfloat16*>(p.residual[g]);
+        a.h[g] = static_cast<__nv_bfloat16*>(p.out2[g]);
     }
     a.has_bias = p.bias[0] != nullptr;
     a.has_residual = p.residual[0] != nullptr;

@@ -47,6 +47,7 @@ struct LinArgs {
     CUtensorMap ti[LIN_MAX_RANKS], ti2[LIN_MAX_RANKS];   // read by the epilogue: residual, or gate and up
     const __nv_bfloat16* bias[LIN_MAX_RANKS];
     const __nv_bfloat16* residual[LIN_MAX_RANKS];
+    __nv_bfloat16* h[LIN_MAX_RANKS];  // the buffers of to2 (LIN_OUT)
     int64_t ld;  // output row stride, elements
     int32_t groups, fused, kb_per_group, m_tiles, n_tiles, rows, cols;
     int32_t total_tiles, group_m, groups_in_n;
@@ -60,24 +61,10 @@ namespace {
 
 constexpr int BM = 256, BN = 256;
 constexpr uint32_t SUB = 64 * BK * 2;  // one 64 x 64 box, 8 KB
-// Epilogue warps: two for each quarter of the tensor memory's lanes, half of the
-// tile's columns each. Their code is bound by instruction latency (one warp a
-// scheduler took 8800-9500 cycles a tile, more than a product of K = 512), so two
-// warps a scheduler nearly halve it.
-constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr uint32_t TMEM_COLS = 2 * BN;
-constexpr int STAGES = 5;
 constexpr uint32_t A_BYTES = 128 * BK * 2, B_BYTES = 128 * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
-// Staging of an epilogue warp: 4 slots of 32 rows x 32 bf16 columns, 64-byte
-// swizzled as the TMA reads and writes them (a float32 chunk takes two, 128-byte
-// swizzled). In bf16 they hold the warp's whole 32 x 128 part of a tile, so that no
-// store is waited for within a tile. They cost one of six stages of the operand
-// ring, which did not slow the products.
-constexpr uint32_t SLOT_BYTES = 2048;
-constexpr uint32_t EPI_WARP_BYTES = 4 * SLOT_BYTES;
-constexpr size_t SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + EPI_WARPS * EPI_WARP_BYTES + 1024;
-static_assert(SMEM_BYTES <= 232448, "at most 227 KB of shared memory per CTA");
+constexpr uint32_t SLOT_BYTES = 2048;  // one staging slot: 32 rows x 32 bf16 columns
+
 
 constexpr int LIN_NOT_SPLIT = 1;     // (positive: not a status)
 constexpr int SPLIT_COST = 12;       // K blocks of time (0.28 us each) that a sum over the parts costs
@@ -141,6 +128,24 @@ __device__ __forceinline__ void mma_commit_both(uint32_t bar, uint16_t mask)
                  : "memory");
 }
 
+// Epilogue warps and shared memory of a kernel: the operand ring and, per epilogue
+// warp, a ring of staging slots (64-byte swizzled as the TMA reads and writes them; a
+// float32 chunk takes two, 128-byte swizzled).
+// Whole tiles: 4 warps with 4 slots, and 6 stages. 8 warps halve an epilogue, which
+// is bound by instruction latency, but next to a running product they cost power and
+// issue slots (8192 x 4096 x 16384 gated, training: 2.5-3 % slower).
+// SPLIT: nothing runs beside the one epilogue, so 8 warps; 5 stages where the
+// epilogue moves two to four times the data (LIN_GLU, LIN_DGLU) and has 4 slots.
+template <int CFG, bool SPLIT>
+struct Layout {
+    static constexpr bool deep = (CFG >> CFG_EPI_SHIFT) != LIN_OUT;
+    static constexpr int epi_warps = SPLIT ? 8 : 4, threads = 64 + 32 * epi_warps;
+    static constexpr int stages = SPLIT && deep ? 5 : 6, slots = SPLIT && !deep ? 2 : 4;
+    static constexpr uint32_t warp_bytes = slots * SLOT_BYTES;
+    static constexpr size_t bytes = stages * STAGE_BYTES + 1024 + epi_warps * warp_bytes + 1024;  // barriers, alignment
+    static_assert(bytes <= 232448, "at most 227 KB of shared memory per CTA");
+};
+
 // Instruction descriptor of tcgen05.mma kind::f16 (float32 D, bf16 A and B):
 // bit 15 A M-major, bit 16 B N-major, N >> 3 from bit 17, M >> 4 from bit 24.
 __host__ __device__ constexpr uint32_t idesc(bool a_t, bool b_t)
@@ -180,20 +185,23 @@ __device__ __forceinline__ void bulk_wait_read()
 // (both CTAs' TMA bytes), empty[s] in both (the leader's commit), acc_full[x] in
 // both, acc_empty[x] in the leader (the 4 epilogue warps of each CTA).
 template <int CFG, bool SPLIT>
-__global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_constant__ LinArgs a)
+__global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_kernel(const __grid_constant__ LinArgs a)
 {
     constexpr bool A_T = (CFG & CFG_A_T) != 0, B_T = (CFG & CFG_B_T) != 0, F32 = (CFG & CFG_F32) != 0;
     constexpr int EPI = CFG >> CFG_EPI_SHIFT;
     constexpr bool PLAIN = EPI == LIN_OUT && (A_T || B_T);  // gradients: the accumulator alone
     constexpr bool ACT = EPI != LIN_OUT || (CFG & CFG_ACT) != 0;
     constexpr int TILE_COLS = EPI == LIN_GLU ? BN / 2 : BN;
-    constexpr int WARP_COLS = TILE_COLS / 2, CHUNKS = WARP_COLS / 32;  // of an epilogue warp
+    using L = Layout<CFG, SPLIT>;
+    constexpr int STAGES = L::stages, SLOTS = L::slots, EPI_WARPS = L::epi_warps;
+    constexpr int HALVES = EPI_WARPS / 4;                                // column ranges of the epilogue warps
+    constexpr int WARP_COLS = TILE_COLS / HALVES, CHUNKS = WARP_COLS / 32;  // of an epilogue warp
     constexpr int STEP = ACT ? 16 : 32;                                // columns a step, one or two steps a chunk
     constexpr int PER = 32 / STEP;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5 + 4 * EPI_WARPS);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5 + SLOTS * EPI_WARPS);
     volatile uint32_t* abort_flag = tmem_slot + 1;
     const uint32_t bar0 = smem_u32(bars);
     auto full_bar = [&](int s) { return bar0 + 8u * (uint32_t)s; };
@@ -201,18 +209,18 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
     auto acc_full = [&](int x) { return bar0 + 8u * (uint32_t)(2 * STAGES + x); };
     auto acc_empty = [&](int x) { return bar0 + 8u * (uint32_t)(2 * STAGES + 2 + x); };
     const uint32_t drain_bar = bar0 + 8u * (uint32_t)(2 * STAGES + 4);
-    auto slot_bar = [&](int w, int s) { return bar0 + 8u * (uint32_t)(2 * STAGES + 5 + 4 * w + s); };
+    auto slot_bar = [&](int w, int s) { return bar0 + 8u * (uint32_t)(2 * STAGES + 5 + SLOTS * w + s); };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // SPLIT: a cluster of `split` pairs has one tile, each pair one part of its K
     // range. Otherwise a cluster is one pair, and takes tiles in turn.
-    const uint32_t rank = cluster_rank(), cta = rank & 1u, leader = rank & ~1u;
+    const uint32_t rank = cluster_rank(), cta = SPLIT ? rank & 1u : rank, leader = SPLIT ? rank & ~1u : 0u;
     const int parts = SPLIT ? a.split : 1, part = SPLIT ? (int)(rank >> 1) : 0;
     const int first = (int)cluster_id(), stride = SPLIT ? a.total_tiles : (int)num_clusters();
     const int kb0 = SPLIT ? (int)((int64_t)a.kbs * part / parts) : 0;
     const int kb1 = SPLIT ? (int)((int64_t)a.kbs * (part + 1) / parts) : a.kbs;
     // one barrier a thread: full and empty, acc_full, acc_empty, drain, the slots
-    constexpr int NBARS = 2 * STAGES + 5 + 4 * EPI_WARPS;
+    constexpr int NBARS = 2 * STAGES + 5 + SLOTS * EPI_WARPS;
     if (threadIdx.x < NBARS) {
         const int b = (int)threadIdx.x;
         mbar_init(bar0 + 8u * (uint32_t)b, b == 2 * STAGES + 2 || b == 2 * STAGES + 3 ? 2 * EPI_WARPS : 1);
@@ -322,7 +330,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
             const uint64_t desc_a0 = smem_desc(smem_u32(smem), A_T ? SUB : 16u, 1024u);
             const uint64_t desc_b0 = smem_desc(smem_u32(smem) + A_BYTES, B_T ? 16u : SUB, 1024u);
             bool ok = true;
-            const uint16_t both = (uint16_t)(3u << leader);
+            // (a constant for whole tiles: a mask in a register costs them 2 %)
+            const uint16_t both = SPLIT ? (uint16_t)(3u << leader) : (uint16_t)3;
             for (int tile = first; ok && tile < a.total_tiles; tile += stride) {
                 if (!wait_bar(acc_empty(acc), acc_phase ^ 1u, abort_flag, ERR_MMA_ACC)) {
                     ok = false;
@@ -364,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
         if (SPLIT) cluster_sync();
     } else {
         // ---------------- epilogue (both CTAs) ----------------
-        const uint32_t stage_epi = smem_u32(smem) + STAGES * STAGE_BYTES + 1024u + (uint32_t)(warp - 2) * EPI_WARP_BYTES;
+        const uint32_t stage_epi = smem_u32(smem) + STAGES * STAGE_BYTES + 1024u + (uint32_t)(warp - 2) * L::warp_bytes;
         const int quarter = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes; columns of the tile
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -374,9 +383,9 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
         const bool has_in = EPI == LIN_DGLU || (EPI == LIN_OUT && !PLAIN && !F32 && a.has_residual);
         const bool has_bias = EPI == LIN_OUT && !PLAIN && a.has_bias;
         const bool keep = !PLAIN && EPI != LIN_DGLU && a.keep;
-        // slots a chunk takes: 1, with a second operand or output 2; float32 columns are
-        // twice as wide
-        const uint32_t per_chunk = EPI == LIN_DGLU ? 2u : EPI == LIN_GLU ? (keep ? 3u : 1u) : F32 ? (keep ? 3u : 2u) : keep ? 2u : 1u;
+        // Slots a chunk takes: 1, with a second operand or output, or in float32, 2
+        // (LIN_GLU with kept pre-activations 3).
+        const uint32_t per_chunk = EPI == LIN_DGLU || F32 || (EPI == LIN_OUT && keep) ? 2u : EPI == LIN_GLU && keep ? 3u : 1u;
         for (int tile = first; tile < a.total_tiles; tile += stride) {
             int g, mt, nt;
             tile_coords(a, tile, g, mt, nt);
@@ -386,21 +395,21 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
             // The warp's chunks of 32 columns: its half of the tile, or, SPLIT, its share of
             // this part's: every `parts`-th chunk of the tile belongs to one part.
             const int tile_col = nt * TILE_COLS;
-            auto chunk_at = [&](int k) { return SPLIT ? 32 * ((2 * k + half) * parts + part) : half * WARP_COLS + 32 * k; };
+            auto chunk_at = [&](int k) { return SPLIT ? 32 * ((HALVES * k + half) * parts + part) : half * WARP_COLS + 32 * k; };
             int chunks = 0;  // warp-uniform
             if (row0 < a.rows)
                 while (chunks < CHUNKS && chunk_at(chunks) < min(TILE_COLS, a.cols - tile_col)) ++chunks;
-            auto slot_addr = [&](uint32_t s) { return stage_epi + (s & 3u) * SLOT_BYTES; };
+            auto slot_addr = [&](uint32_t s) { return stage_epi + (s & (SLOTS - 1)) * SLOT_BYTES; };
             // Operands of chunk c into its slots, by TMA: they cross the memory while
             // the tile is still being multiplied. One lane.
             auto fetch = [&](int c) {
-                const uint32_t s = (slot + (uint32_t)c * per_chunk) & 3u;
+                const uint32_t s = (slot + (uint32_t)c * per_chunk) & (SLOTS - 1);
                 in_flight |= 1u << s;
                 mbar_expect_tx(slot_bar(warp - 2, (int)s), EPI == LIN_DGLU ? 2 * SLOT_BYTES : SLOT_BYTES);
                 tma_load_2d(slot_addr(s), &a.ti[g], slot_bar(warp - 2, (int)s), tile_col + chunk_at(c), row0);
                 if (EPI == LIN_DGLU) tma_load_2d(slot_addr(s + 1), &a.ti2[g], slot_bar(warp - 2, (int)s), tile_col + chunk_at(c), row0);
             };
-            const int depth = (int)(4u / per_chunk);  // chunks whose slots exist at once
+            const int depth = (int)(SLOTS / per_chunk);  // chunks whose slots exist at once
             if (has_in && lane == 0 && chunks > 0) {
                 bulk_wait_read<0>();  // the last tile's stores have read the slots
                 for (int c = 0; c < min(chunks, depth); ++c) fetch(c);
@@ -457,11 +466,14 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
             // chunk (a store is one group of this lane, a float32 one reads two slots).
             auto acquire = [&]() {
                 if (lane == 0) {
-                    if (per_chunk == 1) bulk_wait_read<3>();
-                    else if (F32 && !keep) bulk_wait_read<1>();
-                    else if (per_chunk == 2) bulk_wait_read<2>();
-                    else if (EPI == LIN_GLU) bulk_wait_read<1>();
-                    else bulk_wait_read<0>();
+                    if constexpr (SLOTS == 2) {
+                        if (per_chunk == 1) bulk_wait_read<1>();
+                        else bulk_wait_read<0>();
+                    } else {
+                        if (per_chunk == 1) bulk_wait_read<3>();
+                        else if (!F32 && per_chunk == 2) bulk_wait_read<2>();
+                        else bulk_wait_read<1>();
+                    }
                 }
                 __syncwarp();
             };
@@ -476,7 +488,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
                 }
             };
             auto wait_in = [&](uint32_t s) {  // the chunk's operands have landed in slot s (and s + 1)
-                s &= 3u;
+                s &= SLOTS - 1;
                 int got = 1;
                 if (lane == 0) got = wait_bar(slot_bar(warp - 2, (int)s), (in_phase >> s) & 1u, abort_flag, ERR_EPILOGUE) ? 1 : 0;
                 if (got) {
@@ -485,10 +497,10 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
                 }
                 return __shfl_sync(0xffffffffu, got, 0) != 0;
             };
-            // The operands of the chunk after next, once the chunk before this one has
-            // left its slots (only where the slots do not hold the whole tile).
+            // The operands of a later chunk, once the chunk before this one has left its
+            // slots (where the slots do not hold the warp's whole part of the tile).
             auto refill = [&](int c) {
-                if (!has_in || c < 1 || c - 1 + depth >= chunks) return;
+                if (!has_in || c < 1 || c - 1 + depth >= chunks || depth < 2) return;
                 if (lane == 0) {
                     bulk_wait_read<0>();
                     fetch(c - 1 + depth);
@@ -530,7 +542,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
                 // and every MMA is done): column c, row r at float 128 c + r
                 const uint32_t dst = smem0 + 4u * (uint32_t)(quarter * 32 + lane);
 #pragma unroll 1
-                for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += STEP) {
+                for (int c = half * (BN / HALVES); c < (half + 1) * (BN / HALVES); c += STEP) {
                     tmem_load(taddr + (uint32_t)c, ra);
                     tmem_wait(ra);
 #pragma unroll
@@ -543,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
                 if (steps > 0) start(0, 0, ra);
 #pragma unroll 1
                 for (int c = 0; c < steps; ++c) {
-                    const uint32_t s = F32 && keep ? 0u : slot + (uint32_t)(c / PER) * per_chunk;
+                    const uint32_t s = slot + (uint32_t)(c / PER) * per_chunk;
                     float v[STEP];
                     take(c, 0, ra, v);
                     if (c + 1 < steps) start(c + 1, 0, ra);
@@ -564,7 +576,20 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
                                 }
                             }
                         }
-                        if (keep) put_bf16(s + (F32 ? 2u : 1u), c, v);
+                        if constexpr (F32) {  // the output takes both slots: h goes straight to memory
+                            if (keep && row < a.rows) {
+#pragma unroll
+                                for (int q = 0; q < STEP / 8; ++q) {
+                                    const int cq = tile_col + column(c) + 8 * q;
+                                    if (cq < a.cols)
+                                        *reinterpret_cast<uint4*>(a.h[g] + row * a.ld + cq) =
+                                            make_uint4(bf16x2(v[8 * q], v[8 * q + 1]), bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                                                       bf16x2(v[8 * q + 4], v[8 * q + 5]), bf16x2(v[8 * q + 6], v[8 * q + 7]));
+                                }
+                            }
+                        } else if (keep) {
+                            put_bf16(s + 1, c, v);
+                        }
                         if constexpr (ACT)
                             with_act(a.act, [&](auto tag) {
 #pragma unroll
@@ -586,14 +611,21 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
                             for (int j = 0; j < STEP; ++j) v[j] += x[j];
                         }
                     }
+                    const int c0 = tile_col + chunk_at(c / PER);
                     if constexpr (F32) put_f32(s, c, v);
                     else put_bf16(s, c, v);
-                    if (c % PER == PER - 1 || c + 1 == steps) {
-                        const int c0 = tile_col + chunk_at(c / PER);
+                    if (c % PER == PER - 1) {
                         refill(c / PER);
                         flush();
                         store(&a.to[g], s, c0);
-                        if (keep) store(&a.to2[g], s + (F32 ? 2u : 1u), c0);
+                        if (!F32 && keep) store(&a.to2[g], s + 1, c0);
+                        if (has_in && depth < 2 && c + 1 < steps) {  // one chunk at a time (a kept h beside it)
+                            if (lane == 0) {
+                                bulk_wait_read<0>();
+                                fetch(c / PER + 1);
+                            }
+                            __syncwarp();
+                        }
                     }
                 }
             } else if constexpr (EPI == LIN_GLU) {
@@ -624,7 +656,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
 #pragma unroll
                     for (int j = 0; j < STEP; ++j) v[j] *= u[j];
                     put_bf16(s, c, v);
-                    if (c % PER == PER - 1 || c + 1 == steps) {
+                    if (c % PER == PER - 1) {
                         const int c0 = tile_col + chunk_at(c / PER);
                         flush();
                         store(&a.to[g], s, c0);
@@ -656,7 +688,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
                     });
                     put_bf16(s, c, hg);
                     put_bf16(s + 1, c, hu);
-                    if (c % PER == PER - 1 || c + 1 == steps) {
+                    if (c % PER == PER - 1) {
                         const int c0 = tile_col + chunk_at(c / PER);
                         refill(c / PER);
                         flush();
@@ -669,7 +701,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");  // the next step's columns
                 break;
             }
-            if (!(F32 && keep)) slot = (slot + (uint32_t)chunks * per_chunk) & 3u;
+            slot = (slot + (uint32_t)chunks * per_chunk) & (SLOTS - 1);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_rank(acc_empty(acc), leader));
@@ -679,7 +711,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_gemm_kernel(const __grid_co
             }
         }
         if (lane == 0)  // after an abort: the loads still in flight land before the CTA leaves
-            for (int s = 0; s < 4; ++s)
+            for (int s = 0; s < SLOTS; ++s)
                 if ((in_flight >> s) & 1u) drain_wait(slot_bar(warp - 2, s), (in_phase >> s) & 1u);
         if (lane == 0) bulk_wait_all();  // every output tile written before the CTA leaves
         __syncwarp();
@@ -716,13 +748,13 @@ int resident_clusters(const char* fn, int ctas, int* n)
     std::atomic<int>& slot = known[dev][ctas / 2];
     *n = slot.load(std::memory_order_acquire);
     if (*n) return RTP_OK;
-    cudaError_t e = cudaFuncSetAttribute(linear_gemm_kernel<CFG, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    cudaError_t e = cudaFuncSetAttribute(linear_gemm_kernel<CFG, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<CFG, SPLIT>::bytes);
     if (e != cudaSuccess) return fail(RTP_ECUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr = cluster_of(ctas);
     cfg.gridDim = dim3((unsigned)(ctas * 64));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.blockDim = dim3(Layout<CFG, SPLIT>::threads);
+    cfg.dynamicSmemBytes = Layout<CFG, SPLIT>::bytes;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(n, linear_gemm_kernel<CFG, SPLIT>, &cfg);
@@ -763,8 +795,8 @@ int launch_t(const char* fn, LinArgs& args, cudaStream_t stream)
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas * clusters));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.blockDim = dim3(Layout<CFG, SPLIT>::threads);
+    cfg.dynamicSmemBytes = Layout<CFG, SPLIT>::bytes;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
