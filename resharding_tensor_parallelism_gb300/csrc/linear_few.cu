@@ -135,6 +135,14 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (warp == 2) {  // the descriptors this CTA will use, one a lane
+        const int kg = a.fused ? kb0 / a.kb_per_group + lane : g;
+        if (a.fused ? kg <= (kb1 - 1) / a.kb_per_group : lane == 0) {
+            prefetch_map(&a.tw[kg]);
+            prefetch_map(&a.tx[kg]);
+            if (EPI == LIN_GLU) prefetch_map(&a.tw[LIN_MAX_RANKS + kg]);
+        }
+    }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32((const void*)tmem_slot)),
                      "r"(a.tmem_cols)
@@ -238,6 +246,28 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
     // Every load has landed and every MMA is done when acc_bar completes, so the
     // ring's memory is free: token t, feature f at float t * 128 + f.
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // A thread takes 4 neighbouring output columns of one token, UNROLL such quads
+    // at a time: the loads of the other operands, then of the partials, of all of
+    // them are in flight together (one by one, each cost its full latency: the
+    // epilogue of 256 tokens took 50 us). The first quads' other operands are
+    // fetched while the product runs.
+    constexpr int QUADS = CTA_COLS / 4, UNROLL = 4;
+    const int step = a.split * THREADS, items = a.rows * QUADS;
+    float4 u[UNROLL], x[UNROLL];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j) {
+            const int i = i0 + j * step, t = i / QUADS, f = (i - t * QUADS) * 4;
+            u[j] = x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if constexpr (EPI == LIN_OUT) {
+                if (i >= items || f0 + f >= a.cols) continue;
+                if (a.bias[g]) u[j] = bf16x4(a.bias[g] + f0 + f);
+                if (a.residual[g]) x[j] = bf16x4(a.residual[g] + (int64_t)t * a.cols + f0 + f);
+            }
+        }
+    };
+    int i0 = part * THREADS + (int)threadIdx.x;
+    fetch(i0);
     int ok = 1;
     if (lane == 0) ok = wait_bar(acc_bar, 0, abort_flag, ERR_EPILOGUE) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -260,12 +290,6 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
     tc_fence_after();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(a.tmem_cols) : "memory");
-    // A thread takes 4 neighbouring output columns of one token, UNROLL such quads
-    // at a time: the loads of the other operands, then of the partials, of all of
-    // them are in flight together (one by one, each cost its full latency: the
-    // epilogue of 256 tokens took 50 us).
-    constexpr int QUADS = CTA_COLS / 4, UNROLL = 4;
-    const int step = a.split * THREADS, items = a.rows * QUADS;
     auto sum4 = [&](int t, int f) {
         const uint32_t addr = smem + 4u * (uint32_t)(t * FEAT + f);
         if (a.split == 1) return ld_shared_f4(addr);
@@ -273,17 +297,13 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
         for (int r = 1; r < a.split; ++r) v = add4(v, ld_cluster_f4(map_to_rank(addr, (uint32_t)r)));
         return v;
     };
-    for (int i0 = part * THREADS + (int)threadIdx.x; i0 < items; i0 += UNROLL * step) {
-        float4 v[UNROLL], u[UNROLL], x[UNROLL];
+    while (i0 < items) {
+        float4 v[UNROLL];
 #pragma unroll
         for (int j = 0; j < UNROLL; ++j) {
             const int i = i0 + j * step, t = i / QUADS, f = (i - t * QUADS) * 4;
-            v[j] = u[j] = x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (i >= items || f0 + f >= a.cols) continue;
-            if constexpr (EPI == LIN_OUT) {
-                if (a.bias[g]) u[j] = bf16x4(a.bias[g] + f0 + f);
-                if (a.residual[g]) x[j] = bf16x4(a.residual[g] + (int64_t)t * a.cols + f0 + f);
-            }
             v[j] = sum4(t, f);
             if constexpr (EPI == LIN_GLU) u[j] = sum4(t, 64 + f);
         }
@@ -310,6 +330,8 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
             if constexpr (F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out[g]) + at) = v[j];
             else store_bf16x4(static_cast<__nv_bfloat16*>(a.out[g]) + at, v[j]);
         }
+        i0 += UNROLL * step;
+        if (i0 < items) fetch(i0);
     }
     // No CTA leaves while a peer may still read its partial.
     if (a.split > 1) cluster_sync();
@@ -402,8 +424,14 @@ int launch_linear_few(const char* fn, const LinGemm& p, bool weights_ready, cuda
     a.weights_ready = weights_ready;
     const int64_t tiles = (int64_t)outs * a.tiles;
     if (tiles * MAX_SPLIT >= ((int64_t)1 << 31)) return fail(RTP_ESHAPE, "%s: too many tiles", fn);
-    // K parts: as many CTAs as fit at once (two on an SM), at least 4 K blocks each
-    for (a.split = 1; a.split < MAX_SPLIT && tiles * a.split * 2 <= 2 * sms && a.kbs >= a.split * 2 * 4;) a.split *= 2;
+    // K parts: one CTA an SM as long as each has 4 K blocks, two an SM as long as each
+    // has 8 (measured at 1 to 128 rows: 2048 x 2048 in 8 parts of 4 blocks 5.1 us, in 4
+    // of 8 5.9; the gated 1024 x 4096 x 1024 block in parts of 4 blocks at two CTAs an
+    // SM 14.0 us, of 8 blocks at one 12.8)
+    a.split = 1;
+    while (a.split < MAX_SPLIT && tiles * a.split * 2 <= 2 * sms &&
+           a.kbs >= 2 * a.split * (tiles * a.split * 2 <= sms ? 4 : 8))
+        a.split *= 2;
     const size_t smem = (size_t)a.stages * stage + SMEM_EXTRA;
     if (p.epi == LIN_GLU) return launch_t<LIN_GLU, false>(fn, a, (unsigned)tiles, smem, stream);
     return p.out_f32 ? launch_t<LIN_OUT, true>(fn, a, (unsigned)tiles, smem, stream)
