@@ -586,7 +586,8 @@ int rtp_tp_glu_backward(int P, int64_t M, int64_t K, int64_t F, int64_t N, const
  *   counted[n]  0: the tensor does not count (a replica of a piece that does: under
  *               a broadcast mesh dim only coordinate 0 counts); NULL: all count
  *   workspace   rtp_grad_workspace_bytes(n) bytes of device memory, 8-byte aligned,
- *               need not be initialised; not shared by calls that may overlap
+ *               its first 16 bytes zero before the first call (every call leaves them
+ *               zero); not shared by calls that may overlap
  *   norm        device pointer, receives the float32 norm
  * Sums are finished in float64 in a fixed order: results do not change from run to
  * run, and squares that overflow or underflow float32 do not spoil a norm that is a

@@ -909,7 +909,8 @@ class GradGroup:
             if len(counted) != n:
                 raise RtpError(-1, "GradGroup: %d counted flags for %d tensors" % (len(counted), n))
             self._counted = (ctypes.c_uint8 * max(1, n))(*counted)
-        self._ws = torch.empty((_load().rtp_grad_workspace_bytes(n) // 8,), dtype=torch.float64, device=self.device)
+        # zero once: every call leaves its counter zero
+        self._ws = torch.zeros((_load().rtp_grad_workspace_bytes(n) // 8,), dtype=torch.float64, device=self.device)
 
     def _table(self, name, ts):
         for i, t in enumerate(ts):

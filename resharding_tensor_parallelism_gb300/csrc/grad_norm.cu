@@ -3,11 +3,16 @@
 //   norm = sqrt(sum over counted tensors and their elements of g^2)
 //   c    = min(1, max_norm / (norm + 1e-6)),   g' = c g
 //
-// HBM bound. Two kernels: the first reads the counted gradients and leaves one
-// float64 sum per block; the second sums those in a fixed order (every block for
-// itself), and scales. Blocks and the chunks they take depend on the sizes and
-// the device alone, so results are the same from run to run. The second kernel
-// walks the chunks backwards: what the first one read last is still in L2.
+// HBM bound: every gradient is read for the norm, and read again and written for
+// the product; what the second pass finds in L2 it need not read from HBM. Two
+// kernels. The first leaves one float64 sum per block, and the last block to finish
+// adds them up in block order (the sums of all blocks read by every block of the
+// next kernel cost 6 us: one line of L2 for everyone). The second scales; it is a
+// programmatic dependent of the first and has its first chunk in registers before
+// that one has finished. Every block takes one run of chunks, forwards in the first
+// kernel, backwards in the second, which so begins with what was read last. Runs and
+// sums depend on the sizes and the device alone, so results are the same from run to
+// run.
 //
 // Squares are added in float32 over a thread's part of one chunk (at most 64
 // values, still in its registers) and across chunks in float64. A part whose
@@ -20,7 +25,6 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
-#include <type_traits>
 #include <vector>
 
 #include "rtp_internal.h"
@@ -29,10 +33,14 @@ namespace rtp {
 
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int BLOCKS_PER_SM = 4;
-constexpr int MAX_BLOCKS = 1216;        // partial sums of one launch
-constexpr int STEP_BYTES = THREADS * 16;  // one 16-byte vector a thread
+constexpr int THREADS = 256, BLOCKS_PER_SM = 4;
+constexpr int MAX_BLOCKS = 640;  // blocks, and partial sums, of one launch
+// The scale kernel over more than this runs one block of 512 threads per SM: fewer
+// streams of reads beside writes, and no streaming hints on them (805 MB: both passes
+// 373 us, with hints 377; 101 MB, half of it in L2, 4 blocks of 256 with hints 51.7,
+// without 54.2).
+constexpr uint64_t WIDE_BYTES = 256u << 20;
+constexpr int WIDE_THREADS = 512;
 
 struct Item {
     const void* src;
@@ -44,23 +52,24 @@ struct Item {
 template <int N>
 struct Table {
     Item items[N];
+    uint16_t first[MAX_BLOCKS + 1];  // item of each block's first chunk, and of the end
     int32_t n;
     uint32_t chunks;
 };
-constexpr int SMALL = 64, LARGE = 512;  // tensors of one launch (2 KB or 16 KB of parameters)
+constexpr int SMALL = 64, LARGE = 512;  // tensors of one launch (3 KB or 18 KB of parameters)
 
-// Item of chunk c (uniform over the block): the last one whose chunk0 is <= c.
-template <int N>
-__device__ __forceinline__ int find_item(const Table<N>& t, uint32_t c)
+__host__ __device__ __forceinline__ uint32_t run_begin(uint32_t chunks, int block, int blocks)
 {
-    int lo = 0, hi = t.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (t.items[mid].chunk0 <= c) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+    return (uint32_t)((uint64_t)chunks * (uint32_t)block / (uint32_t)blocks);
 }
+
+// What the kernels share in the workspace. The counter is zero before the first call
+// and zero again after every call.
+struct Shared {
+    unsigned finished;
+    float norm;
+    double partials[1];
+};
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -79,6 +88,7 @@ __device__ __forceinline__ void each(const uint4& v, bool bf16, Fn&& fn)
 __device__ __forceinline__ double block_sum(double v)
 {
     __shared__ double warp_sum[THREADS / 32];
+    __syncthreads();  // a previous sum has been read
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = v;
@@ -89,62 +99,99 @@ __device__ __forceinline__ double block_sum(double v)
     return v;
 }
 
-// A chunk is V vectors of 16 bytes a thread. Tensors whose address is not a
-// multiple of 16 go element by element.
-template <int V, int N>
-__global__ void __launch_bounds__(THREADS) grad_norm_kernel(const __grid_constant__ Table<N> t, double* partials)
+// Sum of the squares of V vectors (see the head of the file).
+template <int V>
+__device__ __forceinline__ double square_sum(const uint4 (&v)[V], bool bf16)
 {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) each(v[i], bf16, [&](float x) { s += x * x; });
+    if (s >= 0x1p-60f && s <= 0x1p100f) return (double)s;
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) any |= v[i].x | v[i].y | v[i].z | v[i].w;
+    double d = 0.0;
+    if (any & (bf16 ? 0x7FFF7FFFu : 0x7FFFFFFFu)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) each(v[i], bf16, [&](float x) { d += (double)x * (double)x; });
+    }
+    return d;
+}
+
+// One chunk of the table: V vectors of 16 bytes for each of T threads. Tensors whose
+// address is not a multiple of 16 have no vectors and go element by element, as do
+// the elements after a tensor's last whole vector.
+struct Chunk {
+    const Item* it;
+    bool bf16;
+    int64_t e0;           // first element
+    int left, nvec, per;  // elements, whole vectors, elements of a vector
+};
+template <int V, int T, int N>
+__device__ __forceinline__ Chunk chunk_of(const Table<N>& t, int& item, uint32_t c, bool both)
+{
+    while (item + 1 < t.n && t.items[item + 1].chunk0 <= c) ++item;
+    while (item > 0 && t.items[item].chunk0 > c) --item;
+    Chunk k;
+    k.it = &t.items[item];
+    k.bf16 = k.it->dtype == RTP_BF16;
+    k.per = k.bf16 ? 8 : 4;
+    k.e0 = (int64_t)(c - k.it->chunk0) * (V * T * k.per);
+    k.left = (int)min(k.it->numel - k.e0, (int64_t)(V * T * k.per));
+    const uintptr_t at = (uintptr_t)k.it->src | (both ? (uintptr_t)k.it->dst : 0);
+    k.nvec = (at & 15u) == 0 ? k.left / k.per : 0;
+    return k;
+}
+
+// all: the partial sums of the launches so far, this one's at `begin`; the last
+// launch's last block (last != 0) adds them all up.
+template <int V, int N>
+__global__ void __launch_bounds__(THREADS) grad_norm_kernel(const __grid_constant__ Table<N> t, Shared* sh, int begin,
+                                                            int last, float* norm)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     double acc = 0.0;
-    for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-        const Item& it = t.items[find_item(t, c)];
-        const bool bf16 = it.dtype == RTP_BF16;
-        const int per = bf16 ? 8 : 4;  // elements of a vector
-        const int64_t e0 = (int64_t)(c - it.chunk0) * (V * THREADS * per);
-        const int64_t left = min(it.numel - e0, (int64_t)(V * THREADS * per));
+    int item = t.first[blockIdx.x];
+    const uint32_t c1 = run_begin(t.chunks, (int)blockIdx.x + 1, (int)gridDim.x);
+    for (uint32_t c = run_begin(t.chunks, (int)blockIdx.x, (int)gridDim.x); c < c1; ++c) {
+        const Chunk k = chunk_of<V, THREADS>(t, item, c, false);
+        const uint4* p = static_cast<const uint4*>(k.it->src) + k.e0 / k.per;
         uint4 v[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (((uintptr_t)it.src & 15u) == 0) {
-            const int64_t vec0 = e0 / per;
-            const int nvec = (int)(left / per), tail = (int)(left - (int64_t)nvec * per);
-            const uint4* p = static_cast<const uint4*>(it.src) + vec0;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int at = i * THREADS + (int)threadIdx.x;
-                if (at < nvec) v[i] = __ldg(p + at);
-            }
-            if ((int)threadIdx.x < tail) {  // the elements after the last whole vector, one a thread
-                const int64_t e = e0 + (int64_t)nvec * per + threadIdx.x;
-                const float x = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(it.src)[e])
-                                     : static_cast<const float*>(it.src)[e];
-                acc += (double)x * (double)x;
-            }
-        } else {
-            for (int e = threadIdx.x; e < (int)left; e += THREADS) {
-                const float x = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(it.src)[e0 + e])
-                                     : static_cast<const float*>(it.src)[e0 + e];
-                acc += (double)x * (double)x;
-            }
-            continue;
+        for (int i = 0; i < V; ++i) {
+            const int at = i * THREADS + (int)threadIdx.x;
+            v[i] = at < k.nvec ? __ldg(p + at) : make_uint4(0u, 0u, 0u, 0u);
         }
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) each(v[i], bf16, [&](float x) { s += x * x; });
-        if (s >= 0x1p-60f && s <= 0x1p100f) {
-            acc += (double)s;
-        } else {
-            uint32_t any = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i) any |= v[i].x | v[i].y | v[i].z | v[i].w;
-            if (any & 0x7FFF7FFFu || (!bf16 && any & 0x7FFFFFFFu)) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) each(v[i], bf16, [&](float x) { acc += (double)x * (double)x; });
-            }
+        for (int i = k.nvec * k.per + (int)threadIdx.x; i < k.left; i += THREADS) {
+            const float x = k.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(k.it->src)[k.e0 + i])
+                                   : static_cast<const float*>(k.it->src)[k.e0 + i];
+            acc += (double)x * (double)x;
+        }
+        acc += square_sum<V>(v, k.bf16);
+    }
+    const double mine = block_sum(acc);
+    __shared__ bool closing;
+    if (threadIdx.x == 0) {
+        sh->partials[begin + (int)blockIdx.x] = mine;
+        closing = false;
+        if (last) {
+            __threadfence();
+            closing = atomicAdd(&sh->finished, 1u) == gridDim.x - 1;
         }
     }
-    const double total = block_sum(acc);
-    if (threadIdx.x == 0) partials[blockIdx.x] = total;
+    __syncthreads();
+    if (!closing) return;
+    // every block's sum is there (earlier launches' blocks are complete)
+    __threadfence();
+    double s = 0.0;
+    for (int i = threadIdx.x; i < begin + (int)gridDim.x; i += THREADS) s += __ldcg(sh->partials + i);
+    const float total = (float)sqrt(block_sum(s));
+    if (threadIdx.x == 0) {
+        sh->finished = 0u;
+        sh->norm = total;
+        *norm = total;
+    }
 }
 
 __device__ __forceinline__ uint32_t scale2(uint32_t w, float c)
@@ -153,62 +200,59 @@ __device__ __forceinline__ uint32_t scale2(uint32_t w, float c)
            ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(hi_f(w) * c)) << 16);
 }
 
-template <int V, int N>
-__global__ void __launch_bounds__(THREADS) grad_scale_kernel(const __grid_constant__ Table<N> t, const double* partials,
-                                                             int n_partials, float max_norm, float* norm, int in_place)
+__device__ __forceinline__ uint4 scaled(const uint4& v, bool bf16, float f)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    double s = 0.0;
-    for (int i = threadIdx.x; i < n_partials; i += THREADS) s += __ldcg(partials + i);
-    const float total = (float)sqrt(block_sum(s));
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
-    float k = max_norm / (total + 1e-6f);
-    if (k > 1.0f) k = 1.0f;  // a NaN stays one
-    if (in_place && k == 1.0f) return;
-    for (uint32_t b = blockIdx.x; b < t.chunks; b += gridDim.x) {
-        const uint32_t c = t.chunks - 1 - b;
-        const Item& it = t.items[find_item(t, c)];
-        const bool bf16 = it.dtype == RTP_BF16;
-        const int per = bf16 ? 8 : 4;
-        const int64_t e0 = (int64_t)(c - it.chunk0) * (V * THREADS * per);
-        const int64_t left = min(it.numel - e0, (int64_t)(V * THREADS * per));
-        if ((((uintptr_t)it.src | (uintptr_t)it.dst) & 15u) == 0) {
-            const int nvec = (int)(left / per), tail = (int)(left - (int64_t)nvec * per);
-            const uint4* p = static_cast<const uint4*>(it.src) + e0 / per;
-            uint4* q = static_cast<uint4*>(it.dst) + e0 / per;
-            uint4 v[V];
+    if (bf16) return make_uint4(scale2(v.x, f), scale2(v.y, f), scale2(v.z, f), scale2(v.w, f));
+    return make_uint4(__float_as_uint(__uint_as_float(v.x) * f), __float_as_uint(__uint_as_float(v.y) * f),
+                      __float_as_uint(__uint_as_float(v.z) * f), __float_as_uint(__uint_as_float(v.w) * f));
+}
+
+// (__ldg although the call may be in place: a chunk is read before its own block
+// writes it, and by no other)
+template <int V, int T, int N>
+__global__ void __launch_bounds__(T) grad_scale_kernel(const __grid_constant__ Table<N> t, const Shared* sh, float max_norm,
+                                                      int in_place)
+{
+    const uint32_t c0 = run_begin(t.chunks, (int)blockIdx.x, (int)gridDim.x);
+    uint32_t c = run_begin(t.chunks, (int)blockIdx.x + 1, (int)gridDim.x);
+    int item = t.first[blockIdx.x + 1];
+    auto load = [&](const Chunk& k, uint4 (&v)[V]) {
+        const uint4* p = static_cast<const uint4*>(k.it->src) + k.e0 / k.per;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int at = i * THREADS + (int)threadIdx.x;
-                if (at < nvec) v[i] = __ldcs(p + at);
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int at = i * THREADS + (int)threadIdx.x;
-                if (at >= nvec) break;
-                uint4 w;
-                if (bf16) w = make_uint4(scale2(v[i].x, k), scale2(v[i].y, k), scale2(v[i].z, k), scale2(v[i].w, k));
-                else
-                    w = make_uint4(__float_as_uint(__uint_as_float(v[i].x) * k), __float_as_uint(__uint_as_float(v[i].y) * k),
-                                   __float_as_uint(__uint_as_float(v[i].z) * k), __float_as_uint(__uint_as_float(v[i].w) * k));
-                __stcs(q + at, w);
-            }
-            if ((int)threadIdx.x < tail) {
-                const int64_t e = e0 + (int64_t)nvec * per + threadIdx.x;
-                if (bf16)
-                    static_cast<__nv_bfloat16*>(it.dst)[e] =
-                        __float2bfloat16_rn(__bfloat162float(static_cast<const __nv_bfloat16*>(it.src)[e]) * k);
-                else static_cast<float*>(it.dst)[e] = static_cast<const float*>(it.src)[e] * k;
-            }
-        } else {
-            for (int i = threadIdx.x; i < (int)left; i += THREADS) {
-                const int64_t e = e0 + i;
-                if (bf16)
-                    static_cast<__nv_bfloat16*>(it.dst)[e] =
-                        __float2bfloat16_rn(__bfloat162float(static_cast<const __nv_bfloat16*>(it.src)[e]) * k);
-                else static_cast<float*>(it.dst)[e] = static_cast<const float*>(it.src)[e] * k;
-            }
+        for (int i = 0; i < V; ++i) {
+            const int at = i * T + (int)threadIdx.x;
+            if (at < k.nvec) v[i] = T == WIDE_THREADS ? __ldg(p + at) : __ldcs(p + at);
         }
+    };
+    uint4 v[V], next[V];
+    Chunk k;
+    if (c > c0) load(k = chunk_of<V, T>(t, item, c - 1, true), v);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float f = max_norm / (__ldcg(&sh->norm) + 1e-6f);
+    if (f > 1.0f) f = 1.0f;  // a NaN stays one
+    if (in_place && f == 1.0f) return;
+    while (c > c0) {
+        Chunk kn = k;
+        if (c - 1 > c0) load(kn = chunk_of<V, T>(t, item, c - 2, true), next);
+        uint4* q = static_cast<uint4*>(k.it->dst) + k.e0 / k.per;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int at = i * T + (int)threadIdx.x;
+            if (at >= k.nvec) continue;
+            if (T == WIDE_THREADS) q[at] = scaled(v[i], k.bf16, f);
+            else __stcs(q + at, scaled(v[i], k.bf16, f));
+        }
+        for (int i = k.nvec * k.per + (int)threadIdx.x; i < k.left; i += T) {
+            const int64_t e = k.e0 + i;
+            if (k.bf16)
+                static_cast<__nv_bfloat16*>(k.it->dst)[e] =
+                    __float2bfloat16_rn(__bfloat162float(static_cast<const __nv_bfloat16*>(k.it->src)[e]) * f);
+            else static_cast<float*>(k.it->dst)[e] = static_cast<const float*>(k.it->src)[e] * f;
+        }
+        --c;
+        k = kn;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = next[i];
     }
 }
 
@@ -231,70 +275,99 @@ int sm_count(const char* fn, int* n)
 
 size_t esize(int dtype) { return dtype == RTP_F32 ? 4 : 2; }
 
-// The launches of one pass over `items` (chunk0 not yet set): call(table, blocks, index of launch).
-template <int V, int N, class Call>
-int each_launch(std::vector<Item>& items, int blocks, Call&& call)
+// The launches of one pass over `items` (chunk0 not yet set), in chunks of
+// chunk_bytes: call(table, blocks, index of launch, last one).
+template <int N, class Call>
+int each_launch(std::vector<Item>& items, uint64_t chunk_bytes, int blocks, Call&& call)
 {
     static thread_local Table<N> t;
     size_t i = 0;
-    for (int launch = 0; i < items.size(); ++launch) {
+    for (int launch = 0; launch == 0 || i < items.size(); ++launch) {
         t.n = 0;
         uint64_t chunks = 0;
         for (; i < items.size() && t.n < N; ++i) {
             const uint64_t bytes = (uint64_t)items[i].numel * esize((int)items[i].dtype);
-            const uint64_t add = (bytes + (uint64_t)V * STEP_BYTES - 1) / ((uint64_t)V * STEP_BYTES);
+            const uint64_t add = (bytes + chunk_bytes - 1) / chunk_bytes;
             if (t.n > 0 && chunks + add > 0x7fffffffu) break;
             items[i].chunk0 = (uint32_t)chunks;
             t.items[t.n++] = items[i];
             chunks += add;
         }
         t.chunks = (uint32_t)chunks;
-        int st = call(t, (int)std::min<uint64_t>(chunks, (uint64_t)blocks), launch);
+        const int grid = (int)std::max<uint64_t>(1, std::min<uint64_t>(chunks, (uint64_t)blocks));
+        for (int b = 0, it = 0; b <= grid; ++b) {
+            while (it + 1 < t.n && t.items[it + 1].chunk0 <= run_begin(t.chunks, b, grid)) ++it;
+            t.first[b] = (uint16_t)it;
+        }
+        int st = call(t, grid, launch, i >= items.size());
         if (st) return st;
     }
     return RTP_OK;
 }
 
+// The norm pass: V vectors a thread and chunk. Programmatic dependents of what ran
+// before, which they wait for.
 template <int V, int N>
-int run(const char* fn, std::vector<Item>& counted, std::vector<Item>& all, double* partials, bool clip, float max_norm,
-        bool in_place, float* norm, int blocks, cudaStream_t stream)
+int norm_pass(const char* fn, std::vector<Item>& counted, Shared* sh, float* norm, int blocks, cudaStream_t stream)
 {
-    int n_partials = 0;
-    int st = each_launch<V, N>(counted, blocks, [&](const Table<N>& t, int grid, int) {
-        grad_norm_kernel<V, N><<<grid, THREADS, 0, stream>>>(t, partials + n_partials);
-        n_partials += grid;
-        cudaError_t e = cudaGetLastError();
-        return e == cudaSuccess ? RTP_OK : fail(RTP_ECUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
-    });
-    if (st) return st;
-    auto scale = [&](const Table<N>& t, int grid, int launch) {
-        cudaLaunchConfig_t cfg = {};
+    int begin = 0;
+    return each_launch<N>(counted, (uint64_t)V * THREADS * 16, blocks, [&](const Table<N>& t, int grid, int, bool last) {
         cudaLaunchAttribute attr[1];
-        // The first launch follows the norm kernel and may be set up while that one
-        // finishes. The later ones follow a kernel that does not announce dependents.
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.gridDim = dim3((unsigned)std::max(grid, 1));
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)grid);
         cfg.blockDim = dim3(THREADS);
         cfg.stream = stream;
         cfg.attrs = attr;
-        cfg.numAttrs = launch == 0 ? 1 : 0;
-        cudaError_t e = cudaLaunchKernelEx(&cfg, grad_scale_kernel<V, N>, t, (const double*)partials, n_partials, max_norm,
-                                           launch == 0 ? norm : (float*)nullptr, in_place ? 1 : 0);
+        cfg.numAttrs = 1;
+        cudaError_t e = cudaLaunchKernelEx(&cfg, grad_norm_kernel<V, N>, t, sh, begin, last ? 1 : 0, norm);
+        begin += grid;
         return e == cudaSuccess ? RTP_OK : fail(RTP_ECUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
-    };
-    if (!clip || all.empty()) {  // the norm alone
-        static thread_local Table<N> none;
-        none.n = 0;
-        none.chunks = 0;
-        return scale(none, 1, 0);
-    }
-    return each_launch<V, N>(all, blocks, scale);
+    });
 }
 
-// Launches of at most LARGE tensors; one more for each time 2^31 chunks are full
-// (8 TB of gradients: never).
-int64_t workspace_bytes(int n) { return (int64_t)((n + SMALL - 1) / SMALL + 1) * MAX_BLOCKS * 8; }
+// The scale pass. Its first launch is a programmatic dependent of the norm kernel,
+// which announced it after its own wait: the gradients were written before either
+// began. Later launches follow kernels that announce nothing.
+template <int V, int T, int N>
+int scale_pass(const char* fn, std::vector<Item>& all, const Shared* sh, float max_norm, bool in_place, int blocks,
+               cudaStream_t stream)
+{
+    return each_launch<N>(all, (uint64_t)V * T * 16, blocks, [&](const Table<N>& t, int grid, int launch, bool) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)grid);
+        cfg.blockDim = dim3(T);
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = launch == 0 ? 1 : 0;
+        cudaError_t e = cudaLaunchKernelEx(&cfg, grad_scale_kernel<V, T, N>, t, sh, max_norm, in_place ? 1 : 0);
+        return e == cudaSuccess ? RTP_OK : fail(RTP_ECUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+    });
+}
+
+template <int N>
+int run(const char* fn, std::vector<Item>& counted, std::vector<Item>& all, uint64_t bytes, Shared* sh, bool clip,
+        float max_norm, bool in_place, float* norm, int sms, cudaStream_t s)
+{
+    // Chunks of 32 KB keep 8 loads in flight a thread; when there are too few of them
+    // for every block, smaller ones spread the work over the SMs, and one block per SM
+    // takes the norm: the blocks count themselves out on one word.
+    const int blocks = std::min(sms * BLOCKS_PER_SM, MAX_BLOCKS);
+    const bool fine = bytes / (uint64_t)blocks < 8u * THREADS * 16;
+    int st = fine ? norm_pass<2, N>(fn, counted, sh, norm, std::min(sms, MAX_BLOCKS), s)
+                  : norm_pass<8, N>(fn, counted, sh, norm, blocks, s);
+    if (st || !clip || all.empty()) return st;
+    if (bytes >= WIDE_BYTES) return scale_pass<8, WIDE_THREADS, N>(fn, all, sh, max_norm, in_place, std::min(sms, MAX_BLOCKS), s);
+    if (fine) return scale_pass<1, THREADS, N>(fn, all, sh, max_norm, in_place, blocks, s);
+    return scale_pass<4, THREADS, N>(fn, all, sh, max_norm, in_place, blocks, s);
+}
+
+// One launch for each LARGE tensors (and for each 2^31 chunks, 8 TB: never).
+int64_t workspace_bytes(int n) { return 16 + (int64_t)(n / LARGE + 1) * MAX_BLOCKS * 8; }
 
 int norm_impl(const char* fn, int n, const int32_t* dtypes, const int64_t* numels, const void* const* grads,
               const uint8_t* counted, bool clip, float max_norm, void* const* out, void* workspace, float* norm,
@@ -346,19 +419,10 @@ int norm_impl(const char* fn, int n, const int32_t* dtypes, const int64_t* numel
     const bool in_place = clip && !out;
     int sms = 0, st;
     if ((st = sm_count(fn, &sms))) return st;
-    const int blocks = std::min(sms * BLOCKS_PER_SM, MAX_BLOCKS);
-    const uint64_t per_block = bytes / (uint64_t)blocks;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    double* ws = static_cast<double*>(workspace);
-    auto go = [&](auto v) {
-        constexpr int V = decltype(v)::value;
-        if (all.size() <= SMALL) return run<V, SMALL>(fn, in, all, ws, clip, max_norm, in_place, norm, blocks, s);
-        return run<V, LARGE>(fn, in, all, ws, clip, max_norm, in_place, norm, blocks, s);
-    };
-    // Chunks of 32 KB keep 8 loads in flight a thread; when there are too few of
-    // them for every block, chunks of 4 KB spread the work over the SMs.
-    if (per_block >= 8u * STEP_BYTES) return go(std::integral_constant<int, 8>());
-    return go(std::integral_constant<int, 1>());
+    Shared* sh = static_cast<Shared*>(workspace);
+    if (all.size() <= SMALL) return run<SMALL>(fn, in, all, bytes, sh, clip, max_norm, in_place, norm, sms, s);
+    return run<LARGE>(fn, in, all, bytes, sh, clip, max_norm, in_place, norm, sms, s);
 }
 
 }  // namespace
