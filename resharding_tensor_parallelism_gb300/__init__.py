@@ -236,9 +236,16 @@ def shard_box(shape: Sequence[int], spec: Spec, rank: int):
 
 # ---- data movement ----------------------------------------------------------------
 
+_T = None
+
+
 def _torch():
-    import torch
-    return torch
+    """The torch module, imported on first use (an import statement costs 0.3 us a call)."""
+    global _T
+    if _T is None:
+        import torch
+        _T = torch
+    return _T
 
 
 def _dtype_code(t) -> int:
@@ -253,7 +260,7 @@ def _dtype_code(t) -> int:
 def _stream_ptr(stream) -> Optional[int]:
     torch = _torch()
     if stream is None:  # the current stream's handle, without building a Stream object (3 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
@@ -323,10 +330,11 @@ def _device_of(t) -> int:
     torch = _torch()
     if not t.is_cuda:
         raise RtpError(-1, "tensors must live on the GPU")
-    if t.get_device() != torch.cuda.current_device():
+    device = t.get_device()
+    if device != torch._C._cuda_getDevice():
         raise RtpError(-1, "tensors are on %s but the current CUDA device is %d" % (t.device,
                                                                                   torch.cuda.current_device()))
-    return t.get_device()
+    return device
 
 
 def shard(full, spec: Spec, out=None, stream=None):
@@ -923,7 +931,7 @@ class GradGroup:
 
     def _begin(self, stream):
         torch = _torch()
-        if torch.cuda.current_device() != self.device.index:
+        if torch._C._cuda_getDevice() != self.device.index:
             raise RtpError(-1, "GradGroup: tensors are on %s but the current CUDA device is %d" % (
                 self.device, torch.cuda.current_device()))
         return _new(1, (), torch.float32, self.device.index, stream)[0]

@@ -295,9 +295,15 @@ int each_launch(std::vector<Item>& items, uint64_t chunk_bytes, int blocks, Call
         }
         t.chunks = (uint32_t)chunks;
         const int grid = (int)std::max<uint64_t>(1, std::min<uint64_t>(chunks, (uint64_t)blocks));
-        for (int b = 0, it = 0; b <= grid; ++b) {
-            while (it + 1 < t.n && t.items[it + 1].chunk0 <= run_begin(t.chunks, b, grid)) ++it;
-            t.first[b] = (uint16_t)it;
+        // item `it` holds the first chunk of the blocks b with run_begin(b) >= its chunk0,
+        // that is b >= chunk0 * grid / chunks, up to the next item's
+        for (int it = 0, b = 0; it < std::max(t.n, 1); ++it) {
+            int end = grid + 1;
+            if (it + 1 < t.n) {
+                const uint64_t at = ((uint64_t)t.items[it + 1].chunk0 * (uint64_t)grid + t.chunks - 1) / t.chunks;
+                end = (int)std::min<uint64_t>(at, (uint64_t)grid + 1);
+            }
+            for (; b < end; ++b) t.first[b] = (uint16_t)it;
         }
         int st = call(t, grid, launch, i >= items.size());
         if (st) return st;
@@ -386,6 +392,9 @@ int norm_impl(const char* fn, int n, const int32_t* dtypes, const int64_t* numel
     };
     std::vector<Range> ranges;
     uint64_t bytes = 0;
+    in.reserve((size_t)n);
+    all.reserve((size_t)n);
+    ranges.reserve((size_t)n * 2);
     for (int i = 0; i < n; ++i) {
         if (dtypes[i] != RTP_F32 && dtypes[i] != RTP_BF16) return fail(RTP_EINVAL, "%s: tensor %d is of unknown type %d", fn, i, dtypes[i]);
         if (numels[i] < 0 || numels[i] >= (int64_t)1 << 44) return fail(RTP_ESHAPE, "%s: tensor %d has %lld elements", fn, i, (long long)numels[i]);

@@ -12,12 +12,13 @@ namespace rtp {
 namespace {
 
 // dH = dOut * act'(H) in bf16, and db = column sums of the unrounded dH.
-// HBM bound (reads dOut and H, writes dH once). A cluster of 8 blocks takes a
-// strip of 64 columns (one 128-byte line of each row), the blocks taking the
-// rows in turn; a thread owns 8 columns (16-byte loads) of every 32nd row of its
-// block, sums them in float32, and the block's 32 row lanes, then the cluster's 8
-// blocks over distributed shared memory, are added in a fixed order.
-constexpr int SUM_THREADS = 256, SUM_COLS = 64, SUM_SPLIT = 8;
+// HBM bound (reads dOut and H, writes dH once). A cluster of 8 blocks takes a strip
+// of COLS columns, the blocks taking the rows in turn; a thread owns 8 columns
+// (16-byte loads), sums them in float32 over its rows, and the block's row lanes,
+// then the cluster's 8 blocks over distributed shared memory, are added in a fixed
+// order. Strips of 256 columns (512 bytes of a row) where there are enough of them
+// for the GPU, of 64 otherwise.
+constexpr int SUM_THREADS = 256, SUM_SPLIT = 8;
 
 struct SumArgs {
     const __nv_bfloat16* dout[LIN_MAX_RANKS];
@@ -28,13 +29,15 @@ struct SumArgs {
     int32_t cols, act;
 };
 
+template <int COLS>
 __global__ void __launch_bounds__(SUM_THREADS) act_grad_kernel(const __grid_constant__ SumArgs a)
 {
-    __shared__ float part[32][SUM_COLS + 1];
-    __shared__ float sums[SUM_COLS];
+    constexpr int COL_LANES = COLS / 8, ROW_LANES = SUM_THREADS / COL_LANES;
+    __shared__ float part[ROW_LANES][COLS + 1];
+    __shared__ float sums[COLS];
     const int g = blockIdx.z, cr = (int)cluster_rank();
-    const int cl = threadIdx.x & 7, rl = threadIdx.x >> 3;
-    const int col = (int)blockIdx.x * SUM_COLS + cl * 8;
+    const int cl = threadIdx.x % COL_LANES, rl = threadIdx.x / COL_LANES;
+    const int col = (int)blockIdx.x * COLS + cl * 8;
     const bool in = col < a.cols;
     const bool has_h = a.h[g] != nullptr;
     float sum[8] = {};
@@ -42,7 +45,7 @@ __global__ void __launch_bounds__(SUM_THREADS) act_grad_kernel(const __grid_cons
         with_act(has_h ? a.act : RTP_ACT_NONE, [&](auto tag) {
             constexpr int ACT = decltype(tag)::value;
 #pragma unroll 4
-            for (int64_t r = cr * 32 + rl; r < a.rows; r += 32 * SUM_SPLIT) {
+            for (int64_t r = cr * ROW_LANES + rl; r < a.rows; r += ROW_LANES * SUM_SPLIT) {
                 const int64_t at = r * a.cols + col;
                 const uint4 d = __ldg(reinterpret_cast<const uint4*>(a.dout[g] + at));
                 float v[8] = {bf16_lo(d.x), bf16_hi(d.x), bf16_lo(d.y), bf16_hi(d.y),
@@ -69,14 +72,14 @@ __global__ void __launch_bounds__(SUM_THREADS) act_grad_kernel(const __grid_cons
 #pragma unroll
     for (int j = 0; j < 8; ++j) part[rl][cl * 8 + j] = sum[j];
     __syncthreads();
-    if (threadIdx.x < SUM_COLS) {
+    if (threadIdx.x < COLS) {
         float s = 0.0f;
-        for (int r = 0; r < 32; ++r) s += part[r][threadIdx.x];
+        for (int r = 0; r < ROW_LANES; ++r) s += part[r][threadIdx.x];
         sums[threadIdx.x] = s;
     }
     cluster_sync();
-    const int c = (int)blockIdx.x * SUM_COLS + (int)threadIdx.x;
-    if (cr == 0 && threadIdx.x < SUM_COLS && c < a.cols) {
+    const int c = (int)blockIdx.x * COLS + (int)threadIdx.x;
+    if (cr == 0 && threadIdx.x < COLS && c < a.cols) {
         float s = 0.0f;
         for (int r = 0; r < SUM_SPLIT; ++r) {
             float v;
@@ -99,12 +102,14 @@ int launch_act_grad(const char* fn, const SumArgs& a, int groups, cudaStream_t s
     attr[0].val.clusterDim.x = 1;
     attr[0].val.clusterDim.y = SUM_SPLIT;
     attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)((a.cols + SUM_COLS - 1) / SUM_COLS), SUM_SPLIT, (unsigned)groups);
+    const bool wide = (int64_t)(a.cols / 256) * SUM_SPLIT * groups >= 256;
+    const int cols = wide ? 256 : 64;
+    cfg.gridDim = dim3((unsigned)((a.cols + cols - 1) / cols), SUM_SPLIT, (unsigned)groups);
     cfg.blockDim = dim3(SUM_THREADS);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, act_grad_kernel, a);
+    cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, act_grad_kernel<256>, a) : cudaLaunchKernelEx(&cfg, act_grad_kernel<64>, a);
     if (e != cudaSuccess) return fail(RTP_ECUDA, "%s: activation gradient launch failed: %s", fn, cudaGetErrorString(e));
     return RTP_OK;
 }
