@@ -636,8 +636,20 @@ def _tables():
         except ImportError as e:
             raise ImportError("_table.so is not built (%s); run `python -c \"import __graft_entry__ as g; g.build()\"`"
                               % e) from e
+        _table.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.rtp_tp_linear, _lib.rtp_tp_glu)])
         _ext = _table
     return _ext
+
+
+def _on_gpu(X) -> bool:
+    return getattr(X[0] if type(X) is list and X else X, "is_cuda", False)
+
+
+def _called(got):
+    """The outputs of a call that the extension made whole; None when it did not take the arguments."""
+    if type(got) is int:
+        _check(got)
+    return got
 
 
 def _table_of(fn: str, name: str, ts, n: int, shape, dtype, device: int) -> bytes:
@@ -726,6 +738,12 @@ def tp_linear(X, W_shards, split: str = "column", bias=None, act: str = "none", 
     Returns the list of outputs, or (outputs, H) with keep_h (or H given): the bf16 pre-activations that
     tp_linear_backward reads."""
     fn = "tp_linear"
+    if (out is None and H is None and not keep_h and out_dtype is None and stream is None and
+            split in ("column", "row") and _on_gpu(X)):
+        got = _called((_ext or _tables()).linear(X, W_shards, split == "row", bias, residual, _act_code(act),
+                                                 _torch()._C._cuda_getDevice(), _stream_ptr(None) or 0))
+        if got is not None:
+            return got
     bf16 = _torch().bfloat16
     X, W = _listed(X), _listed(W_shards)
     row, P, M, K, N, Kp, Np = _linear_shapes(fn, X, W, split)
@@ -833,6 +851,11 @@ def tp_glu(X, Ag_shards, Au_shards, B_shards, act: str = "silu", residual=None, 
     """Gated feed-forward block on P = len(Ag_shards) virtual ranks:
     Z = sum_i (act(X Ag_i) * (X Au_i)) B_i + residual, bf16 [M, N] (or float32: out_dtype, or by `Z`).
     Y: P bf16 [M, F/P] scratch buffers, allocated when not given. Returns Z."""
+    if Y is None and Z is None and out_dtype is None and stream is None and _on_gpu(X):
+        got = _called((_ext or _tables()).glu(X, Ag_shards, Au_shards, B_shards, residual, _act_code(act),
+                                              _torch()._C._cuda_getDevice(), _stream_ptr(None) or 0))
+        if got is not None:
+            return got
     return _glu_forward("tp_glu", X, _listed(Ag_shards), _listed(Au_shards), _listed(B_shards), act, residual, [Y], Z,
                         out_dtype, stream)[0]
 

@@ -1,8 +1,10 @@
-// Python extension of the binding: allocates lists of buffers, and checks a list of torch tensors against the
-// type, shape and device that a call will touch, and returns their addresses as
-// one table of 64-bit pointers. The same checks as the binding's Python loop, at
-// about 20 ns a tensor instead of 500: a call on 8 ranks passes 20 to 60
-// tensors, and a decoded token's product takes the GPU about as long as that loop.
+// Python extension of the binding: checks lists of torch tensors against the type,
+// shape and device that a call will touch, and returns their addresses as one table
+// of 64-bit pointers; allocates lists of buffers; and makes the two calls of a
+// decoding loop (a linear layer, a gated block) whole. The same checks as the
+// binding's Python code, at about 20 ns a tensor instead of 500: a call on 8 ranks
+// passes 20 to 60 tensors, and a decoded token's product takes the GPU about as long
+// as that loop.
 #include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -144,7 +146,161 @@ PyObject* buffers(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     }
 }
 
+// ---- whole calls -------------------------------------------------------------------
+
+using LinearFn = int (*)(int, int, int64_t, int64_t, int64_t, const void* const*, const void* const*, const void* const*,
+                         const void* const*, int, int, void* const*, void* const*, void*);
+using GluFn = int (*)(int, int64_t, int64_t, int64_t, int64_t, const void*, const void* const*, const void* const*,
+                      const void* const*, const void*, int, void* const*, int, void*, void*);
+LinearFn linear_fn = nullptr;
+GluFn glu_fn = nullptr;
+
+// bind(address of rtp_tp_linear, address of rtp_tp_glu)
+PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t nargs)
+{
+    if (nargs != 2) {
+        PyErr_SetString(PyExc_TypeError, "bind(linear, glu)");
+        return nullptr;
+    }
+    const auto a = PyLong_AsUnsignedLongLong(args[0]), b = PyLong_AsUnsignedLongLong(args[1]);
+    if (PyErr_Occurred()) return nullptr;
+    linear_fn = reinterpret_cast<LinearFn>((uintptr_t)a);
+    glu_fn = reinterpret_cast<GluFn>((uintptr_t)b);
+    Py_RETURN_NONE;
+}
+
+constexpr int MAX_RANKS = 8;
+
+bool fits(const at::Tensor& t, at::IntArrayRef shape, long device)
+{
+    return t.scalar_type() == at::kBFloat16 && t.sizes() == shape && placed(t, device);
+}
+
+// The addresses of the n bf16 tensors of a list (or of one tensor, n = 1).
+bool addresses(PyObject* o, Py_ssize_t n, at::IntArrayRef shape, long device, const void** out)
+{
+    if (THPVariable_Check(o)) {
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (n != 1 || !fits(t, shape, device)) return false;
+        out[0] = t.data_ptr();
+        return true;
+    }
+    if (!PyList_Check(o) || PyList_GET_SIZE(o) != n) return false;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        PyObject* e = PyList_GET_ITEM(o, i);
+        if (!THPVariable_Check(e)) return false;
+        const at::Tensor& t = THPVariable_Unpack(e);
+        if (!fits(t, shape, device)) return false;
+        out[i] = t.data_ptr();
+    }
+    return true;
+}
+
+// Shape of a matrix, or of the first one of a list.
+bool matrix(PyObject* o, int64_t* rows, int64_t* cols, long device)
+{
+    if (PyList_Check(o) && PyList_GET_SIZE(o) > 0) o = PyList_GET_ITEM(o, 0);
+    if (!THPVariable_Check(o)) return false;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.dim() != 2 || !t.is_cuda() || t.get_device() != device) return false;
+    *rows = t.size(0);
+    *cols = t.size(1);
+    return true;
+}
+
+at::TensorOptions bf16_on(long device)
+{
+    return at::TensorOptions().dtype(at::kBFloat16).device(c10::Device(c10::kCUDA, (c10::DeviceIndex)device));
+}
+
+// linear(X, W, row, bias, residual, act, device, stream): rtp_tp_linear with new bf16
+// outputs. Returns their list; a status; or None when an argument is not what the
+// call takes (the Python code then says which).
+PyObject* linear(PyObject*, PyObject* const* args, Py_ssize_t nargs)
+{
+    if (nargs != 8 || !linear_fn) {
+        PyErr_SetString(PyExc_TypeError, "linear(X, W, row, bias, residual, act, device, stream)");
+        return nullptr;
+    }
+    const bool row = args[2] == Py_True;
+    const long act = PyLong_AsLong(args[5]), device = PyLong_AsLong(args[6]);
+    const unsigned long long stream = PyLong_AsUnsignedLongLong(args[7]);
+    if (PyErr_Occurred()) return nullptr;
+    if (!PyList_Check(args[1])) Py_RETURN_NONE;
+    const Py_ssize_t P = PyList_GET_SIZE(args[1]);
+    int64_t M, Kx, Kp, Np;
+    if (P < 1 || P > MAX_RANKS || !matrix(args[0], &M, &Kx, device) || !matrix(args[1], &Kp, &Np, device)) Py_RETURN_NONE;
+    const Py_ssize_t outs = row ? 1 : P;
+    const void *x[MAX_RANKS], *w[MAX_RANKS], *b[MAX_RANKS], *r[MAX_RANKS];
+    void* o[MAX_RANKS];
+    const bool has_b = args[3] != Py_None, has_r = args[4] != Py_None;
+    if (!addresses(args[0], row ? P : 1, {M, Kp}, device, x) || !addresses(args[1], P, {Kp, Np}, device, w) ||
+        (has_b && !addresses(args[3], outs, {Np}, device, b)) || (has_r && !addresses(args[4], outs, {M, Np}, device, r)))
+        Py_RETURN_NONE;
+    PyObject* list = PyList_New(outs);
+    if (!list) return nullptr;
+    try {
+        for (Py_ssize_t i = 0; i < outs; ++i) {
+            at::Tensor t = at::empty({M, Np}, bf16_on(device));
+            o[i] = t.data_ptr();
+            PyObject* e = THPVariable_Wrap(std::move(t));
+            if (!e) {
+                Py_DECREF(list);
+                return nullptr;
+            }
+            PyList_SET_ITEM(list, i, e);
+        }
+    } catch (const std::exception&) {  // out of memory: the Python code raises it
+        Py_DECREF(list);
+        Py_RETURN_NONE;
+    }
+    const int rc = linear_fn(row ? 1 : 0, (int)P, M, row ? Kp * P : Kp, row ? Np : Np * P, x, w, has_b ? b : nullptr,
+                             has_r ? r : nullptr, (int)act, 1, nullptr, o, reinterpret_cast<void*>((uintptr_t)stream));
+    if (rc == 0) return list;
+    Py_DECREF(list);
+    return PyLong_FromLong(rc);
+}
+
+// glu(X, Ag, Au, B, residual, act, device, stream): rtp_tp_glu with a new bf16 Z and
+// scratch for Y; returns as linear() does.
+PyObject* glu(PyObject*, PyObject* const* args, Py_ssize_t nargs)
+{
+    if (nargs != 8 || !glu_fn) {
+        PyErr_SetString(PyExc_TypeError, "glu(X, Ag, Au, B, residual, act, device, stream)");
+        return nullptr;
+    }
+    const long act = PyLong_AsLong(args[5]), device = PyLong_AsLong(args[6]);
+    const unsigned long long stream = PyLong_AsUnsignedLongLong(args[7]);
+    if (PyErr_Occurred()) return nullptr;
+    if (!PyList_Check(args[1])) Py_RETURN_NONE;
+    const Py_ssize_t P = PyList_GET_SIZE(args[1]);
+    int64_t M, K, Kg, Fp, Fb, N;
+    if (P < 1 || P > MAX_RANKS || !matrix(args[0], &M, &K, device) || !matrix(args[1], &Kg, &Fp, device) ||
+        !matrix(args[3], &Fb, &N, device))
+        Py_RETURN_NONE;
+    const void *x[1], *g[MAX_RANKS], *u[MAX_RANKS], *b[MAX_RANKS], *r[1] = {nullptr};
+    if (!addresses(args[0], 1, {M, K}, device, x) || !addresses(args[1], P, {K, Fp}, device, g) ||
+        !addresses(args[2], P, {K, Fp}, device, u) || !addresses(args[3], P, {Fp, N}, device, b) ||
+        (args[4] != Py_None && !addresses(args[4], 1, {M, N}, device, r)))
+        Py_RETURN_NONE;
+    at::Tensor Y, Z;
+    try {
+        Y = at::empty({P, M, Fp}, bf16_on(device));
+        Z = at::empty({M, N}, bf16_on(device));
+    } catch (const std::exception&) {
+        Py_RETURN_NONE;
+    }
+    void* y[MAX_RANKS];
+    for (Py_ssize_t i = 0; i < P; ++i) y[i] = static_cast<char*>(Y.data_ptr()) + i * M * Fp * 2;
+    const int rc = glu_fn((int)P, M, K, Fp * P, N, x[0], g, u, b, r[0], (int)act, y, 1, Z.data_ptr(),
+                          reinterpret_cast<void*>((uintptr_t)stream));
+    return rc == 0 ? THPVariable_Wrap(std::move(Z)) : PyLong_FromLong(rc);
+}
+
 PyMethodDef methods[] = {
+    {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(bind)), METH_FASTCALL, nullptr},
+    {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(linear)), METH_FASTCALL, nullptr},
+    {"glu", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(glu)), METH_FASTCALL, nullptr},
     {"buffers", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(buffers)), METH_FASTCALL, nullptr},
     {"table", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(table)), METH_FASTCALL, nullptr},
     {"like", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(like)), METH_FASTCALL, nullptr},

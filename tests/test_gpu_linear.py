@@ -118,6 +118,76 @@ def test_full_size_and_run_to_run_bits():
         assert torch.equal(first, rtp.tp_linear(few, W, split="row")[0])
 
 
+def test_refusals_on_the_gpu():
+    """Calls that a decoding loop makes refuse wrong buffers with the message of the checked path."""
+    X, W, b, R, _, _ = _case("row", 2, 5, 64, 72, True, True, 2)
+    good = rtp.tp_linear(X, W, split="row", bias=b, residual=R)
+    for kw, status in ((dict(bias=[b[0][:64]]), -2), (dict(bias=[b[0].float()]), -2), (dict(residual=[R[0].t()]), -2),
+                       (dict(residual=[R[0].cpu()]), -1), (dict(act="swish"), -1), (dict(split="rows"), -1),
+                       (dict(bias=b * 2), -1)):
+        with pytest.raises(rtp.RtpError) as e:
+            rtp.tp_linear(X, W, **{**dict(split="row", bias=b, residual=R), **kw})
+        assert e.value.status == status, kw
+    for X2, W2, status in ((X[:1], W, -1), ([x[:, :8].contiguous() for x in X], W, -2), (X, [w.float() for w in W], -2),
+                           ([X[0], X[1].t().contiguous().t()], W, -1), ([x.cpu() for x in X], W, -1)):
+        with pytest.raises(rtp.RtpError) as e:
+            rtp.tp_linear(X2, W2, split="row")
+        assert e.value.status == status
+    with pytest.raises(rtp.RtpError) as e:  # refused by the library itself
+        rtp.tp_linear([x[:, :12].contiguous() for x in X], [w[:12].contiguous() for w in W], split="row")
+    assert e.value.status == -2 and "multiples of 8" in str(e.value)
+    with pytest.raises(rtp.RtpError):
+        rtp.tp_glu(X[0], [W[0]] * 2, [W[0]], [W[0]] * 2)
+    assert torch.equal(rtp.tp_linear(X, W, split="row", bias=b[0], residual=R[0])[0], good[0])
+    assert torch.equal(rtp.tp_linear(tuple(X), tuple(W), split="row", bias=b, residual=R)[0], good[0])
+
+
+def test_outputs_past_two_to_the_31_elements():
+    """Row offsets past 2^31 elements: the last rows of a 262,147 x 8,200 output, and of its gradient's input."""
+    M, K, N = 262147, 64, 8200
+    X, W = _normal((M, K), seed=1), [_normal((K, N), 0.2, seed=2)]
+    b, R = [_normal((N,), 0.5, seed=3)], [torch.zeros((M, N), dtype=BF16, device="cuda")]
+    R[0][-5:] = 1.5
+    out = rtp.tp_linear(X, W, bias=b, residual=R, act="relu")[0]
+    rows = [0, 1, 261888, M - 257, M - 6, M - 5, M - 1]
+    (h, e), = _pre("column", [X[rows]], W, b)
+    a = p64.act("relu", h) + R[0][rows].double()
+    p64.check("long output", out[rows], a, e + p64.act_eval_bound(a, h) + 2.0 ** -23 * a.abs(), p64.BF16_REL)
+    _, dW, db = rtp.tp_linear_backward(X, W, [out], H=[out], act="relu")
+    d = (out.float() * (out > 0)).to(BF16)
+    cols = [0, 63, 64, 8199]
+    ref, e = p64.product(X.T, d[:, cols])
+    p64.check("long dW", dW[0][:, cols], ref, e, p64.BF16_REL)
+    p64.check("long db", db[0][cols], d[:, cols].double().sum(0), p64.acc_bound(M, d[:, cols].double().abs().sum(0)),
+              2.0 ** -23)
+
+
+def test_two_threads_on_their_own_streams():
+    """Concurrent calls keep their launch arguments and results apart."""
+    import threading
+
+    cases = [_case("row", 4, m, 512, 264, True, True, 100 + m) for m in (3, 300)]
+    want = [rtp.tp_linear(X, W, split="row", bias=b, residual=R)[0] for X, W, b, R, _, _ in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        X, W, b, R, _, _ = cases[i]
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(200):
+                if not torch.equal(rtp.tp_linear(X, W, split="row", bias=b, residual=R)[0], want[i]):
+                    bad.append(i)
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def test_no_rows():
     W = [torch.ones((16, 8), dtype=BF16, device="cuda")] * 2
     out = rtp.tp_linear(torch.empty((0, 16), dtype=BF16, device="cuda"), W, act="silu", keep_h=True)
