@@ -636,7 +636,8 @@ def _tables():
         except ImportError as e:
             raise ImportError("_table.so is not built (%s); run `python -c \"import __graft_entry__ as g; g.build()\"`"
                               % e) from e
-        _table.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.rtp_tp_linear, _lib.rtp_tp_glu)])
+        _table.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.rtp_tp_linear, _lib.rtp_tp_glu,
+                                                                          _lib.rtp_clip_grad_norm)])
         _ext = _table
     return _ext
 
@@ -940,8 +941,13 @@ class GradGroup:
             if len(counted) != n:
                 raise RtpError(-1, "GradGroup: %d counted flags for %d tensors" % (len(counted), n))
             self._counted = (ctypes.c_uint8 * max(1, n))(*counted)
+        # addresses of the tables, for the extension
+        self._at = [n] + [0 if a is None else ctypes.addressof(a)
+                          for a in (self._dtypes, self._numels, self._ptrs, self._counted)]
         # zero once: every call leaves its counter zero
         self._ws = torch.zeros((_load().rtp_grad_workspace_bytes(n) // 8,), dtype=torch.float64, device=self.device)
+        self._at.append(self._ws.data_ptr())
+        self._index = self.device.index
 
     def _table(self, name, ts):
         for i, t in enumerate(ts):
@@ -969,6 +975,11 @@ class GradGroup:
     def clip(self, max_norm: float, out=None, stream=None):
         """Scales every tensor by min(1, max_norm / (norm + 1e-6)), in place or into the tensors of `out` (same types
         and sizes). Returns (norm, tensors)."""
+        if stream is None and _torch()._C._cuda_getDevice() == self._index:
+            norm = _called((_ext or _tables()).clip(*self._at, max_norm, out, self.grads, self._index,
+                                                    _stream_ptr(None) or 0))
+            if norm is not None:
+                return norm, (self.grads if out is None else out)
         norm = self._begin(stream)
         optr = None
         if out is not None:

@@ -1,7 +1,7 @@
 // Python extension of the binding: checks lists of torch tensors against the type,
 // shape and device that a call will touch, and returns their addresses as one table
-// of 64-bit pointers; allocates lists of buffers; and makes the two calls of a
-// decoding loop (a linear layer, a gated block) whole. The same checks as the
+// of 64-bit pointers; allocates lists of buffers; and makes the calls that take the
+// GPU least (a linear layer, a gated block, clipping) whole. The same checks as the
 // binding's Python code, at about 20 ns a tensor instead of 500: a call on 8 ranks
 // passes 20 to 60 tensors, and a decoded token's product takes the GPU about as long
 // as that loop.
@@ -152,18 +152,23 @@ using LinearFn = int (*)(int, int, int64_t, int64_t, int64_t, const void* const*
                          const void* const*, int, int, void* const*, void* const*, void*);
 using GluFn = int (*)(int, int64_t, int64_t, int64_t, int64_t, const void*, const void* const*, const void* const*,
                       const void* const*, const void*, int, void* const*, int, void*, void*);
+using ClipFn = int (*)(int, const int32_t*, const int64_t*, const void* const*, const uint8_t*, float, void* const*, void*,
+                       float*, void*);
 LinearFn linear_fn = nullptr;
 GluFn glu_fn = nullptr;
+ClipFn clip_fn = nullptr;
 
-// bind(address of rtp_tp_linear, address of rtp_tp_glu)
+// bind(addresses of rtp_tp_linear, rtp_tp_glu, rtp_clip_grad_norm)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t nargs)
 {
-    if (nargs != 2) {
-        PyErr_SetString(PyExc_TypeError, "bind(linear, glu)");
+    if (nargs != 3) {
+        PyErr_SetString(PyExc_TypeError, "bind(linear, glu, clip)");
         return nullptr;
     }
-    const auto a = PyLong_AsUnsignedLongLong(args[0]), b = PyLong_AsUnsignedLongLong(args[1]);
+    const auto a = PyLong_AsUnsignedLongLong(args[0]), b = PyLong_AsUnsignedLongLong(args[1]),
+               c = PyLong_AsUnsignedLongLong(args[2]);
     if (PyErr_Occurred()) return nullptr;
+    clip_fn = reinterpret_cast<ClipFn>((uintptr_t)c);
     linear_fn = reinterpret_cast<LinearFn>((uintptr_t)a);
     glu_fn = reinterpret_cast<GluFn>((uintptr_t)b);
     Py_RETURN_NONE;
@@ -297,7 +302,50 @@ PyObject* glu(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     return rc == 0 ? THPVariable_Wrap(std::move(Z)) : PyLong_FromLong(rc);
 }
 
+// clip(n, dtypes, numels, grads, counted, workspace, max_norm, out, tensors, device,
+// stream): rtp_clip_grad_norm on a group's tables (addresses) with a new norm tensor;
+// out: None (in place) or a list like `tensors`. Returns as linear() does.
+PyObject* clip(PyObject*, PyObject* const* args, Py_ssize_t nargs)
+{
+    if (nargs != 11 || !clip_fn || !PyList_Check(args[8])) {
+        PyErr_SetString(PyExc_TypeError,
+                        "clip(n, dtypes, numels, grads, counted, workspace, max_norm, out, tensors, device, stream)");
+        return nullptr;
+    }
+    const long n = PyLong_AsLong(args[0]), device = PyLong_AsLong(args[9]);
+    unsigned long long at[5], stream = PyLong_AsUnsignedLongLong(args[10]);
+    for (int i = 0; i < 5; ++i) at[i] = PyLong_AsUnsignedLongLong(args[1 + i]);
+    const double max_norm = PyFloat_AsDouble(args[6]);
+    if (PyErr_Occurred()) return nullptr;
+    if (n < 0 || PyList_GET_SIZE(args[8]) != n) Py_RETURN_NONE;
+    try {
+        std::vector<void*> out;
+        if (args[7] != Py_None) {
+            if (!PyList_Check(args[7]) || PyList_GET_SIZE(args[7]) != n) Py_RETURN_NONE;
+            out.resize((size_t)n + 1);  // never without storage: a NULL table means in place
+            for (Py_ssize_t i = 0; i < n; ++i) {
+                PyObject *a = PyList_GET_ITEM(args[7], i), *b = PyList_GET_ITEM(args[8], i);
+                if (!THPVariable_Check(a) || !THPVariable_Check(b)) Py_RETURN_NONE;
+                const at::Tensor &t = THPVariable_Unpack(a), &r = THPVariable_Unpack(b);
+                if (t.scalar_type() != r.scalar_type() || t.sizes() != r.sizes() || !placed(t, device)) Py_RETURN_NONE;
+                out[(size_t)i] = t.data_ptr();
+            }
+        }
+        at::Tensor norm = at::empty(at::IntArrayRef{}, at::TensorOptions().dtype(at::kFloat).device(
+                                                           c10::Device(c10::kCUDA, (c10::DeviceIndex)device)));
+        auto p = [&](int i) { return reinterpret_cast<void*>((uintptr_t)at[i]); };
+        const int rc = clip_fn((int)n, static_cast<const int32_t*>(p(0)), static_cast<const int64_t*>(p(1)),
+                               static_cast<const void* const*>(p(2)), static_cast<const uint8_t*>(p(3)), (float)max_norm,
+                               out.empty() ? nullptr : out.data(), p(4), norm.data_ptr<float>(),
+                               reinterpret_cast<void*>((uintptr_t)stream));
+        return rc == 0 ? THPVariable_Wrap(std::move(norm)) : PyLong_FromLong(rc);
+    } catch (const std::exception&) {
+        Py_RETURN_NONE;
+    }
+}
+
 PyMethodDef methods[] = {
+    {"clip", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(clip)), METH_FASTCALL, nullptr},
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(bind)), METH_FASTCALL, nullptr},
     {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(linear)), METH_FASTCALL, nullptr},
     {"glu", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(glu)), METH_FASTCALL, nullptr},
