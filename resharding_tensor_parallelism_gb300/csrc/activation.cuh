@@ -19,9 +19,23 @@ namespace rtp {
 
 namespace {
 
-// 1 / (1 + e^-v) with the fast exponential and quotient: 2 + 1.2 |v| and 2 ulp, which
-// is below 2^-19 relative where the result is above 2^-24, far below bf16's 2^-9
-__device__ __forceinline__ float logistic(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+// e^v and 1 / v by the approximate base-2 exponential and reciprocal instructions
+// (2^-22 and 1 ulp; subnormal results and operands count as zero): e^v is off by
+// 2^-22 + |v| 2^-24 relative (the rounding of v log2 e), far below bf16's 2^-9.
+__device__ __forceinline__ float exp_fast(float v)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.44269504088896340736f));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float logistic(float v) { return rcp_fast(1.0f + exp_fast(-v)); }
 
 constexpr float kTanhScale = 1.5957691216057307f;  // 2 sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
@@ -29,8 +43,8 @@ constexpr float kTanhCubic = 0.044715f;
 // Phi(x); e receives e^(-x^2 / 2).
 __device__ __forceinline__ float normal_cdf(float x, float& e)
 {
-    e = __expf(-0.5f * x * x);
-    const float t = __fdividef(1.0f, 1.0f + 0.3275911f * 0.70710678118654752440f * fabsf(x));
+    e = exp_fast(-0.5f * x * x);
+    const float t = rcp_fast(1.0f + 0.3275911f * 0.70710678118654752440f * fabsf(x));
     const float p = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
     const float tail = 0.5f * p * e;
     return x < 0.0f ? tail : 1.0f - tail;

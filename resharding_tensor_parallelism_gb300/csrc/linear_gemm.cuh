@@ -114,10 +114,12 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr));
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr));
     return v;
 }
 // The barrier at the same address in both CTAs of a pair (mask: their ranks in the cluster).
@@ -196,8 +198,15 @@ __global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_ke
     constexpr int STAGES = L::stages, SLOTS = L::slots, EPI_WARPS = L::epi_warps;
     constexpr int HALVES = EPI_WARPS / 4;                                // column ranges of the epilogue warps
     constexpr int WARP_COLS = TILE_COLS / HALVES, CHUNKS = WARP_COLS / 32;  // of an epilogue warp
-    constexpr int STEP = ACT ? 16 : 32;                                // columns a step, one or two steps a chunk
+    // Columns a step, one or two steps a chunk. 32 halve the steps' fixed latency in a
+    // whole tile's epilogue (4096 x 512 x 4096 with SiLU: 41.0 us at 16, 33.6 at 32);
+    // beside the long products of LIN_GLU, and with 8 warps, 16 measured better (8192 x
+    // 4096 x 16384, training: 1932 us against 1975; 256 x 2048 x 2048, split: 11.2 against
+    // 12.7).
+    constexpr int STEP = SPLIT || EPI == LIN_GLU ? 16 : 32;
     constexpr int PER = 32 / STEP;
+    constexpr uint32_t PART_BYTES = 128 * BN * 4;  // SPLIT: a part's accumulator in shared memory
+    static_assert(!SPLIT || PART_BYTES + L::epi_warps * 4096u <= L::stages * STAGE_BYTES, "in the operand ring's memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
@@ -524,13 +533,31 @@ __global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_ke
             };
             auto take = [&](int c, int up, uint32_t (&r)[STEP], float (&v)[STEP]) {
                 if constexpr (SPLIT) {
-                    const uint32_t at = smem0 + 4u * (uint32_t)((column(c) + up) * 128 + quarter * 32 + lane);
+                    // Summed in 128-byte pieces of a column (a request of 32 scattered 16-byte
+                    // pieces takes the cluster's network many times as long), and turned to
+                    // one row a lane in the warp's own 4 KB behind the accumulator.
+                    const uint32_t in_col = 16u * (uint32_t)(lane & 7), own = smem0 + PART_BYTES + (uint32_t)(warp - 2) * 4096u +
+                                                                              (up ? 128u * STEP : 0u);
+                    const uint32_t at = smem0 + 512u * (uint32_t)(column(c) + up + (lane >> 3)) + 128u * (uint32_t)quarter + in_col;
+                    float4 sum[STEP / 4];
+                    for (int p = 0; p < parts; ++p) {
+                        const uint32_t from = map_to_rank(at, (uint32_t)(2 * p) + cta);
+                        float4 w[STEP / 4];
 #pragma unroll
-                    for (int j = 0; j < STEP; ++j) v[j] = ld_cluster_f32(map_to_rank(at + 512u * j, cta));
-                    for (int p = 1; p < parts; ++p) {
+                        for (int q = 0; q < STEP / 4; ++q) w[q] = ld_cluster_f4(from + 2048u * q);
 #pragma unroll
-                        for (int j = 0; j < STEP; ++j) v[j] += ld_cluster_f32(map_to_rank(at + 512u * j, (uint32_t)(2 * p) + cta));
+                        for (int q = 0; q < STEP / 4; ++q)
+                            sum[q] = p ? make_float4(sum[q].x + w[q].x, sum[q].y + w[q].y, sum[q].z + w[q].z, sum[q].w + w[q].w) : w[q];
                     }
+                    __syncwarp();  // the last step's columns have been read
+#pragma unroll
+                    for (int q = 0; q < STEP / 4; ++q)
+                        st_shared_v4(own + 128u * (uint32_t)(4 * q + (lane >> 3)) + in_col, __float_as_uint(sum[q].x),
+                                     __float_as_uint(sum[q].y), __float_as_uint(sum[q].z), __float_as_uint(sum[q].w));
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < STEP; ++j)
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[j]) : "r"(own + 128u * (uint32_t)j + 4u * (uint32_t)lane) : "memory");
                 } else {
                     tmem_wait(r);
 #pragma unroll
