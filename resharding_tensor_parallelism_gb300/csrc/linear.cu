@@ -2,6 +2,7 @@
 // block: argument checks, choice of kernel, launch order, and the backward's
 // element-wise step with the bias gradient.
 #include <cstring>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "linear.h"
@@ -115,14 +116,62 @@ int launch_act_grad(const char* fn, const SumArgs& a, int groups, cudaStream_t s
     return RTP_OK;
 }
 
+// The same product's rows from `first` on.
+LinGemm rows_from(const LinGemm& p, int64_t first)
+{
+    LinGemm r = p;
+    r.rows = p.rows - first;
+    auto shift = [first](auto& q, int64_t row_bytes) {
+        if (q) q = (std::remove_reference_t<decltype(q)>)((uintptr_t)q + (uintptr_t)(first * row_bytes));
+    };
+    for (int g = 0; g < LIN_MAX_GROUPS; ++g) {
+        shift(r.A[g], p.kdim * 2);
+        shift(r.out[g], p.cols * (p.out_f32 ? 4 : 2));
+    }
+    for (int g = 0; g < LIN_MAX_RANKS; ++g) {
+        shift(r.out2[g], p.cols * 2);
+        shift(r.out3[g], p.cols * 2);
+        shift(r.residual[g], p.cols * 2);
+    }
+    return r;
+}
+
+// Rows behind the last whole row tile that the few-row kernel takes (0: none). The pair
+// kernel multiplies a nearly empty row tile like a full one; where these tiles begin a
+// wave of their own, the weights read once more cost less than that wave. Pair kernel
+// alone -> both, 1 and 48 rows over: 768 x 4096 x 6144 (24 column tiles) 47.5 -> 39.3 and
+// 41.3 us, 1024 x 16384 x 4096 (16) 158 -> 108 and 111, 2304 x 2048 x 2048 (8) 28.8 -> 25.8
+// and 27.0. The other side: 2048 x 4096 x 9728 (38) 109 -> 113 and 117, 1024 x 1024 x 4096
+// (16, 16 K blocks) 20.5 -> 19.9 and 21.0; with 96 and 128 rows over most of the gain is gone.
+// At the limits (64 rows, 25 column tiles, 32 K blocks) 28.8 -> 29.4.
+int64_t rest_rows(const LinGemm& p)
+{
+    constexpr int64_t MAX_REST = 64, MIN_K = 32 * 64;
+    const int64_t rest = p.rows % LIN_TILE_ROWS, m_tiles = p.rows / LIN_TILE_ROWS;
+    const int64_t k = p.kdim * (p.fused ? p.groups : 1);
+    int sms = 0;
+    if (!rest || rest > MAX_REST || !m_tiles || k < MIN_K || linear_sms(&sms) || sms < 2) return 0;
+    const int64_t pairs = sms / 2, tile_cols = p.epi == LIN_GLU ? LIN_TILE_COLS / 2 : LIN_TILE_COLS;
+    const int64_t n_tiles = (p.fused ? 1 : p.groups) * ((p.cols + tile_cols - 1) / tile_cols);
+    if (3 * n_tiles > pairs) return 0;
+    const int64_t waves = (n_tiles * (m_tiles + 1) + pairs - 1) / pairs;
+    return waves > (n_tiles * m_tiles + pairs - 1) / pairs ? rest : 0;
+}
+
 // A forward product: the few-row kernel up to LIN_FEW_ROWS rows, the pair kernel
-// beyond. Few-row time over pair time, products of 2048 x 2048 to 8192 x 28672: 0.57 to
+// beyond, or both (rest_rows). Few-row time over pair time, products of 2048 x 2048 to 8192 x 28672: 0.57 to
 // 0.88 at 48 rows, 0.73 to 0.99 at 96, 0.78 to 1.04 at 128 (the largest: 88 us against
 // 93; 4096 x 16384 on 8 ranks: 32.4 against 31.4).
 int forward(const char* fn, const LinGemm& p, bool weights_ready, cudaStream_t stream)
 {
     if (p.rows <= LIN_FEW_ROWS) return launch_linear_few(fn, p, weights_ready, stream);
-    return launch_linear_gemm(fn, p, stream);
+    const int64_t rest = rest_rows(p);
+    if (!rest) return launch_linear_gemm(fn, p, stream);
+    LinGemm top = p;
+    top.rows = p.rows - rest;
+    int st = launch_linear_gemm(fn, top, stream);
+    // the pair kernel waits for its predecessors and does not write B, so B is ready
+    return st ? st : launch_linear_few(fn, rows_from(p, top.rows), true, stream);
 }
 
 #define TRY(call)          \

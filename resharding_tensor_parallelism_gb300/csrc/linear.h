@@ -41,13 +41,16 @@ struct LinGemm {
     const void* aux2[LIN_MAX_RANKS] = {};
 };
 
-// The 2-SM pair kernel (linear_gemm.cu): any LinGemm.
+// The 2-SM pair kernel (linear_gemm.cu): any LinGemm, in tiles of 256 x 256 (LIN_GLU:
+// 128 columns of the output).
+constexpr int LIN_TILE_ROWS = 256, LIN_TILE_COLS = 256;
 int launch_linear_gemm(const char* fn, const LinGemm& g, cudaStream_t stream);
 // The few-row kernel (linear_few.cu): LIN_OUT and LIN_GLU, at most
 // LIN_FEW_ROWS rows, no transposed operands. weights_ready: nothing queued on the
 // stream since a kernel that waited for its own predecessor writes B, so B may be
 // read before the previous kernel has finished.
 constexpr int LIN_FEW_ROWS = 128;
+int linear_sms(int* n);  // SMs of the current device; 0: found
 int launch_linear_few(const char* fn, const LinGemm& g, bool weights_ready, cudaStream_t stream);
 
 int take_linear_gemm_error(void* stream, uint32_t* code);

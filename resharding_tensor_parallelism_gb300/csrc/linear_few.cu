@@ -341,20 +341,6 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
 
 // ---- host side --------------------------------------------------------------------
 
-int sm_count(int* n)
-{
-    static std::atomic<int> sms[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return RTP_ECUDA;
-    int v = sms[dev].load(std::memory_order_acquire);
-    if (!v) {
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) return RTP_ECUDA;
-        sms[dev].store(v, std::memory_order_release);
-    }
-    *n = v;
-    return RTP_OK;
-}
-
 template <int EPI, bool F32>
 int launch_t(const char* fn, const Args& args, unsigned tiles, size_t smem, cudaStream_t stream)
 {
@@ -388,10 +374,24 @@ int launch_t(const char* fn, const Args& args, unsigned tiles, size_t smem, cuda
 
 }  // namespace
 
+int linear_sms(int* n)
+{
+    static std::atomic<int> sms[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return RTP_ECUDA;
+    int v = sms[dev].load(std::memory_order_acquire);
+    if (!v) {
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) return RTP_ECUDA;
+        sms[dev].store(v, std::memory_order_release);
+    }
+    *n = v;
+    return RTP_OK;
+}
+
 int launch_linear_few(const char* fn, const LinGemm& p, bool weights_ready, cudaStream_t stream)
 {
     int st, sms = 0;
-    if (sm_count(&sms)) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
+    if (linear_sms(&sms)) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
     static thread_local Args a;
     std::memset(&a, 0, sizeof a);
     const int cta_cols = p.epi == LIN_GLU ? FEAT / 2 : FEAT;

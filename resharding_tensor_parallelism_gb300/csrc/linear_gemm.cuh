@@ -60,7 +60,7 @@ struct LinArgs {
 
 namespace {
 
-constexpr int BM = 256, BN = 256;
+constexpr int BM = LIN_TILE_ROWS, BN = LIN_TILE_COLS;
 constexpr uint32_t SUB = 64 * BK * 2;  // one 64 x 64 box, 8 KB
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr uint32_t A_BYTES = 128 * BK * 2, B_BYTES = 128 * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;

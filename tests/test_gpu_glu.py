@@ -93,6 +93,14 @@ def test_ragged_sizes(P, M, K, F, N, train):
     _forward(P, M, K, F, N, "gelu_tanh", residual=M % 2 == 1, train=train, seed=K)
 
 
+@pytest.mark.parametrize("P,K,F,N", [(1, 2048, 3192, 264), (5, 2056, 5 * 520, 6152), (2, 64, 2 * 1032, 6392)])
+@pytest.mark.parametrize("over", [1, 64])
+@pytest.mark.parametrize("train", [False, True])
+def test_rows_left_over_by_the_last_whole_tile(P, K, F, N, over, train):
+    """25 column tiles in the first product, the second, or both: up to 64 rows over go to the few-row kernel."""
+    _forward(P, 768 + over, K, F, N, "silu", train=train, seed=over)
+
+
 @pytest.mark.parametrize("act", ["none", "gelu", "gelu_tanh", "silu", "relu"])
 @pytest.mark.parametrize("M", [23, 270])
 @pytest.mark.parametrize("out_dtype", [BF16, F32])

@@ -92,6 +92,25 @@ def test_ragged_sizes(split, P, M, K, N):
     _run_and_check(split, P, M, K, N, "none", True, True, seed=K)
 
 
+@pytest.mark.parametrize("split,P,K,N", [("column", 5, 2048, 5 * 1048), ("column", 1, 2056, 6392), ("row", 2, 2 * 1032, 6152)])
+@pytest.mark.parametrize("over", [1, 17, 64, 65])
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_rows_left_over_by_the_last_whole_tile(split, P, K, N, over, out_dtype):
+    """25 column tiles and a little over 768 rows: up to 64 rows over go to the few-row kernel."""
+    _run_and_check(split, P, 768 + over, K, N, "gelu", True, True, out_dtype, keep_h=split == "column", seed=over)
+
+
+def test_rows_left_over_read_weights_written_just_before():
+    X, W, b, R, outs, Np = _case("column", 1, 777, 2048, 6400, True, True, 5)
+    want = rtp.tp_linear(X[0], W, bias=b, residual=R)[0].clone()
+    late = torch.zeros_like(W[0])
+    for _ in range(20):
+        late.zero_()
+        late.copy_(W[0])
+        got = rtp.tp_linear(X[0], [late], bias=b, residual=R)[0]
+        assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("act", ["none", "gelu", "gelu_tanh", "silu", "relu"])
 @pytest.mark.parametrize("bias,residual", [(False, False), (True, False), (False, True), (True, True)])
 @pytest.mark.parametrize("M", [21, 290])
