@@ -13,6 +13,7 @@ Names mirror the C ABI in ``include/rtp.h``:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -697,16 +698,22 @@ def _matrix(fn: str, name: str, t):
     return t.shape
 
 
-def _new(n: int, shape, dtype, device: int, stream=None) -> list:
-    """n fresh buffers of one shape, owned by the stream the call runs on: memory that torch hands out again is ordered
-    on its owning stream only, and scratch is dropped when the call returns."""
+def _allocating_on(stream):
+    """Context in which torch allocates, and launches, on the stream that a call was given (None: the current one).
+    Memory that torch hands out again is ordered on its owning stream only, and scratch is dropped when the call
+    returns: it has to be owned by the stream that the call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
     torch = _torch()
-    code = F32 if dtype is torch.float32 else BF16
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def _new(n: int, shape, dtype, device: int, stream=None) -> list:
+    """n fresh buffers of one shape, owned by the stream the call runs on."""
+    code = F32 if dtype is _torch().float32 else BF16
     if stream is None:
         return (_ext or _tables()).buffers(n, shape, code, device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    with torch.cuda.stream(stream):
+    with _allocating_on(stream):
         return _tables().buffers(n, shape, code, device)
 
 
@@ -923,9 +930,10 @@ class GradGroup:
     """The gradients of a program's tensors (rank pieces, float32 and bf16 mixed), for their global norm and clipping.
     Keeps the tensors, their tables and the workspace, as a training loop keeps its gradient buffers; the values are
     read at each call. counted[i] False: tensor i is a replica (counted_pieces) that is clipped but not counted. Calls
-    on one group that may overlap on the GPU share its workspace and must be ordered by the caller."""
+    on one group that may overlap on the GPU share its workspace and must be ordered by the caller. stream: where the
+    workspace is allocated and zeroed (default: the current stream)."""
 
-    def __init__(self, grads, counted=None):
+    def __init__(self, grads, counted=None, stream=None):
         torch = _torch()
         self.grads = list(grads)
         n = len(self.grads)
@@ -945,7 +953,8 @@ class GradGroup:
         self._at = [n] + [0 if a is None else ctypes.addressof(a)
                           for a in (self._dtypes, self._numels, self._ptrs, self._counted)]
         # zero once: every call leaves its counter zero
-        self._ws = torch.zeros((_load().rtp_grad_workspace_bytes(n) // 8,), dtype=torch.float64, device=self.device)
+        with _allocating_on(stream):
+            self._ws = torch.zeros((_load().rtp_grad_workspace_bytes(n) // 8,), dtype=torch.float64, device=self.device)
         self._at.append(self._ws.data_ptr())
         self._index = self.device.index
 
@@ -1001,12 +1010,12 @@ class GradGroup:
 
 def grad_norm(grads, counted=None, stream=None):
     """Global norm of a list of gradients (GradGroup.norm without keeping a group)."""
-    return GradGroup(grads, counted).norm(stream)
+    return GradGroup(grads, counted, stream).norm(stream)
 
 
 def clip_grad_norm(grads, max_norm: float, counted=None, out=None, stream=None):
     """Clips a list of gradients by their global norm (GradGroup.clip without keeping a group)."""
-    return GradGroup(grads, counted).clip(max_norm, out, stream)
+    return GradGroup(grads, counted, stream).clip(max_norm, out, stream)
 
 
 def device_error(stream=None) -> int:
