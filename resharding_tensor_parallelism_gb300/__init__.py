@@ -955,8 +955,13 @@ class GradGroup:
         # zero once: every call leaves its counter zero
         with _allocating_on(stream):
             self._ws = torch.zeros((_load().rtp_grad_workspace_bytes(n) // 8,), dtype=torch.float64, device=self.device)
+            self._zeroed = None
+            if not torch.cuda.is_current_stream_capturing():
+                self._zeroed = torch.cuda.current_stream(self.device).record_event()
+            self._index = self.device.index
+            # handles of the streams that may use the workspace as it is: the one that zeroed it, and those of _join
+            self._joined = {torch._C._cuda_getCurrentRawStream(self._index) or None}
         self._at.append(self._ws.data_ptr())
-        self._index = self.device.index
 
     def _table(self, name, ts):
         for i, t in enumerate(ts):
@@ -967,29 +972,49 @@ class GradGroup:
                 raise RtpError(-1, "GradGroup: %s[%d] is on %s, the group on %s" % (name, i, t.device, self.device))
         return _i64([t.numel() for t in ts])
 
+    def _join(self, handle):
+        """The first call on another stream than the workspace's own: that stream waits until the workspace is zero, and
+        keeps it, should the group be dropped, until its work is done. A capturing stream can do neither: a capture
+        begins with all earlier work complete, and its graph is replayed only as long as the group is kept."""
+        torch = _torch()
+        s = torch.cuda.ExternalStream(handle, self.device) if handle else torch.cuda.default_stream(self.device)
+        with torch.cuda.stream(s):
+            if torch.cuda.is_current_stream_capturing():
+                return
+            if self._zeroed is not None:
+                s.wait_event(self._zeroed)
+        self._ws.record_stream(s)
+        self._joined.add(handle)
+
     def _begin(self, stream):
+        """(the norm's buffer, the handle of the stream to run on)"""
         torch = _torch()
         if torch._C._cuda_getDevice() != self.device.index:
             raise RtpError(-1, "GradGroup: tensors are on %s but the current CUDA device is %d" % (
                 self.device, torch.cuda.current_device()))
-        return _new(1, (), torch.float32, self.device.index, stream)[0]
+        handle = _stream_ptr(stream)
+        if handle not in self._joined:
+            self._join(handle)
+        return _new(1, (), torch.float32, self.device.index, stream)[0], handle
 
     def norm(self, stream=None):
         """The global norm, a float32 scalar tensor on the GPU."""
-        norm = self._begin(stream)
+        norm, handle = self._begin(stream)
         _check(_load().rtp_grad_norm(len(self.grads), self._dtypes, self._numels, self._ptrs, self._counted,
-                                     self._ws.data_ptr(), norm.data_ptr(), _stream_ptr(stream)))
+                                     self._ws.data_ptr(), norm.data_ptr(), handle))
         return norm
 
     def clip(self, max_norm: float, out=None, stream=None):
         """Scales every tensor by min(1, max_norm / (norm + 1e-6)), in place or into the tensors of `out` (same types
         and sizes). Returns (norm, tensors)."""
         if stream is None and _torch()._C._cuda_getDevice() == self._index:
-            norm = _called((_ext or _tables()).clip(*self._at, max_norm, out, self.grads, self._index,
-                                                    _stream_ptr(None) or 0))
+            handle = _stream_ptr(None)
+            if handle not in self._joined:
+                self._join(handle)
+            norm = _called((_ext or _tables()).clip(*self._at, max_norm, out, self.grads, self._index, handle or 0))
             if norm is not None:
                 return norm, (self.grads if out is None else out)
-        norm = self._begin(stream)
+        norm, handle = self._begin(stream)
         optr = None
         if out is not None:
             out = _listed(out)
@@ -1003,8 +1028,7 @@ class GradGroup:
                 raise RtpError(-2, "GradGroup: out[%d] is %s %s on %s, expected contiguous %s %s on %s" % (
                     optr, o.dtype, tuple(o.shape), o.device, g.dtype, tuple(g.shape), self.device))
         _check(_load().rtp_clip_grad_norm(len(self.grads), self._dtypes, self._numels, self._ptrs, self._counted,
-                                          float(max_norm), optr, self._ws.data_ptr(), norm.data_ptr(),
-                                          _stream_ptr(stream)))
+                                          float(max_norm), optr, self._ws.data_ptr(), norm.data_ptr(), handle))
         return norm, (self.grads if out is None else out)
 
 

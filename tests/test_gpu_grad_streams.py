@@ -97,3 +97,64 @@ def test_one_call_forms_whose_kernels_run_late():
             _same(norm, got, want, before, 0.05)
         torch.cuda.synchronize()
         del filled
+
+
+def _call(group, how, side):
+    """norm, or clip in place, on `side`: by the argument, or as the current stream."""
+    if how.endswith("current"):
+        with torch.cuda.stream(side):
+            return (group.norm(), []) if how.startswith("norm") else group.clip(0.05)
+    return (group.norm(stream=side), []) if how.startswith("norm") else group.clip(0.05, stream=side)
+
+
+HOW = ["norm by argument", "norm, current", "clip by argument", "clip, current"]
+
+
+@pytest.mark.parametrize("how", HOW)
+def test_kept_group_built_on_a_busy_stream_and_used_on_another(how):
+    grads = _grads(seed=2)
+    before, want = [t.clone() for t in grads], _exact(grads)
+    side = _ready_stream()
+    group = rtp.GradGroup(grads)
+    norm, got = _call(group, how, side)
+    side.synchronize()
+    with torch.cuda.stream(side):
+        _same(norm, got, want, before, 0.05)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("how", HOW)
+def test_kept_group_dropped_while_another_stream_uses_it(how):
+    grads = _grads(seed=3)
+    before, want = [t.clone() for t in grads], _exact(grads)
+    group = rtp.GradGroup(grads)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(CYCLES)
+    norm, got = _call(group, how, side)
+    del group
+    filled = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in (512, 5136, 5632, 6144) for _ in range(50)]
+    side.synchronize()
+    with torch.cuda.stream(side):
+        _same(norm, got, want, before, 0.05)
+    torch.cuda.synchronize()
+    del filled
+
+
+def test_kept_group_first_used_in_a_capture():
+    grads = _grads(seed=4)
+    before, want = [t.clone() for t in grads], _exact(grads)
+    out = [torch.empty_like(t) for t in grads]
+    group = rtp.GradGroup(grads)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm, _ = group.clip(0.05, out=out)
+    for _ in range(2):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        _same(norm, out, want, before, 0.05)
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        rtp.GradGroup(grads).norm()  # built and used within one capture
