@@ -940,18 +940,13 @@ class GradGroup:
         if n and not self.grads[0].is_cuda:
             raise RtpError(-1, "GradGroup: tensors must live on the GPU")
         self.device = self.grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
-        self._numels = self._table("grads", self.grads)
-        self._dtypes = _i32([_dtype_code(g) for g in self.grads])
-        self._ptrs = _ptrs([g.data_ptr() for g in self.grads])
+        self._tabulate()
         self._counted = None
         if counted is not None:
             counted = [bool(c) for c in counted]
             if len(counted) != n:
                 raise RtpError(-1, "GradGroup: %d counted flags for %d tensors" % (len(counted), n))
             self._counted = (ctypes.c_uint8 * max(1, n))(*counted)
-        # addresses of the tables, for the extension
-        self._at = [n] + [0 if a is None else ctypes.addressof(a)
-                          for a in (self._dtypes, self._numels, self._ptrs, self._counted)]
         # zero once: every call leaves its counter zero
         with _allocating_on(stream):
             self._ws = torch.zeros((_load().rtp_grad_workspace_bytes(n) // 8,), dtype=torch.float64, device=self.device)
@@ -961,7 +956,24 @@ class GradGroup:
             self._index = self.device.index
             # handles of the streams that may use the workspace as it is: the one that zeroed it, and those of _join
             self._joined = {torch._C._cuda_getCurrentRawStream(self._index) or None}
-        self._at.append(self._ws.data_ptr())
+        # the arguments that a clipping call passes on: how many, and addresses
+        self._at = [n, *self._tables_at, 0 if self._counted is None else ctypes.addressof(self._counted), self._ws.data_ptr()]
+
+    def _tabulate(self):
+        self._numels = self._table("grads", self.grads)
+        self._dtypes = _i32([_dtype_code(g) for g in self.grads])
+        self._ptrs = _ptrs([g.data_ptr() for g in self.grads])
+        self._tables_at = [ctypes.addressof(a) for a in (self._dtypes, self._numels, self._ptrs)]
+
+    def _refresh(self):
+        """Tables of the tensors as they are now: a tensor's storage can be replaced under it (``g.data = ...``, ``set_``),
+        and the one tabulated be freed."""
+        if _tables().unchanged(*self._at[:4], self.grads, self._index):
+            return
+        if len(self.grads) != self._at[0]:
+            raise RtpError(-1, "GradGroup: %d tensors, built over %d" % (len(self.grads), self._at[0]))
+        self._tabulate()
+        self._at[1:4] = self._tables_at
 
     def _table(self, name, ts):
         for i, t in enumerate(ts):
@@ -992,6 +1004,7 @@ class GradGroup:
         if torch._C._cuda_getDevice() != self.device.index:
             raise RtpError(-1, "GradGroup: tensors are on %s but the current CUDA device is %d" % (
                 self.device, torch.cuda.current_device()))
+        self._refresh()
         handle = _stream_ptr(stream)
         if handle not in self._joined:
             self._join(handle)

@@ -302,9 +302,47 @@ PyObject* glu(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     return rc == 0 ? THPVariable_Wrap(std::move(Z)) : PyLong_FromLong(rc);
 }
 
+// Whether the tables of a group still say what its tensors are: a tensor's storage
+// can be replaced under it, and the one tabulated be freed.
+bool same(PyObject* list, const int32_t* dtypes, const int64_t* numels, const void* const* at, long device)
+{
+    for (Py_ssize_t i = 0; i < PyList_GET_SIZE(list); ++i) {
+        PyObject* o = PyList_GET_ITEM(list, i);
+        if (!THPVariable_Check(o)) return false;
+        const at::Tensor& t = THPVariable_Unpack(o);
+        at::ScalarType want;
+        if (!scalar_type(dtypes[i], &want) || t.scalar_type() != want || t.numel() != numels[i]) return false;
+        if (numels[i] > 0 && (!placed(t, device) || t.data_ptr() != at[i])) return false;
+    }
+    return true;
+}
+
+// unchanged(n, dtypes, numels, grads, tensors, device) -> bool
+PyObject* unchanged(PyObject*, PyObject* const* args, Py_ssize_t nargs)
+{
+    if (nargs != 6 || !PyList_Check(args[4])) {
+        PyErr_SetString(PyExc_TypeError, "unchanged(n, dtypes, numels, grads, tensors, device)");
+        return nullptr;
+    }
+    const long n = PyLong_AsLong(args[0]), device = PyLong_AsLong(args[5]);
+    unsigned long long at[3];
+    for (int i = 0; i < 3; ++i) at[i] = PyLong_AsUnsignedLongLong(args[1 + i]);
+    if (PyErr_Occurred()) return nullptr;
+    try {
+        auto p = [&](int i) { return reinterpret_cast<void*>((uintptr_t)at[i]); };
+        return PyBool_FromLong(PyList_GET_SIZE(args[4]) == n &&
+                               same(args[4], static_cast<const int32_t*>(p(0)), static_cast<const int64_t*>(p(1)),
+                                    static_cast<const void* const*>(p(2)), device));
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
 // clip(n, dtypes, numels, grads, counted, workspace, max_norm, out, tensors, device,
 // stream): rtp_clip_grad_norm on a group's tables (addresses) with a new norm tensor;
-// out: None (in place) or a list like `tensors`. Returns as linear() does.
+// out: None (in place) or a list like `tensors`. Returns as linear() does, None also
+// where the tables are not of `tensors` any more.
 PyObject* clip(PyObject*, PyObject* const* args, Py_ssize_t nargs)
 {
     if (nargs != 11 || !clip_fn || !PyList_Check(args[8])) {
@@ -318,7 +356,11 @@ PyObject* clip(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     const double max_norm = PyFloat_AsDouble(args[6]);
     if (PyErr_Occurred()) return nullptr;
     if (n < 0 || PyList_GET_SIZE(args[8]) != n) Py_RETURN_NONE;
+    auto p = [&](int i) { return reinterpret_cast<void*>((uintptr_t)at[i]); };
     try {
+        if (!same(args[8], static_cast<const int32_t*>(p(0)), static_cast<const int64_t*>(p(1)),
+                  static_cast<const void* const*>(p(2)), device))
+            Py_RETURN_NONE;
         std::vector<void*> out;
         if (args[7] != Py_None) {
             if (!PyList_Check(args[7]) || PyList_GET_SIZE(args[7]) != n) Py_RETURN_NONE;
@@ -333,7 +375,6 @@ PyObject* clip(PyObject*, PyObject* const* args, Py_ssize_t nargs)
         }
         at::Tensor norm = at::empty(at::IntArrayRef{}, at::TensorOptions().dtype(at::kFloat).device(
                                                            c10::Device(c10::kCUDA, (c10::DeviceIndex)device)));
-        auto p = [&](int i) { return reinterpret_cast<void*>((uintptr_t)at[i]); };
         const int rc = clip_fn((int)n, static_cast<const int32_t*>(p(0)), static_cast<const int64_t*>(p(1)),
                                static_cast<const void* const*>(p(2)), static_cast<const uint8_t*>(p(3)), (float)max_norm,
                                out.empty() ? nullptr : out.data(), p(4), norm.data_ptr<float>(),
@@ -346,6 +387,7 @@ PyObject* clip(PyObject*, PyObject* const* args, Py_ssize_t nargs)
 
 PyMethodDef methods[] = {
     {"clip", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(clip)), METH_FASTCALL, nullptr},
+    {"unchanged", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(unchanged)), METH_FASTCALL, nullptr},
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(bind)), METH_FASTCALL, nullptr},
     {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(linear)), METH_FASTCALL, nullptr},
     {"glu", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(glu)), METH_FASTCALL, nullptr},
