@@ -1019,14 +1019,14 @@ class GradGroup:
 
     def clip(self, max_norm: float, out=None, stream=None):
         """Scales every tensor by min(1, max_norm / (norm + 1e-6)), in place or into the tensors of `out` (same types
-        and sizes). Returns (norm, tensors)."""
+        and sizes). Returns (norm, list of the tensors written)."""
         if stream is None and _torch()._C._cuda_getDevice() == self._index:
             handle = _stream_ptr(None)
             if handle not in self._joined:
                 self._join(handle)
             norm = _called((_ext or _tables()).clip(*self._at, max_norm, out, self.grads, self._index, handle or 0))
             if norm is not None:
-                return norm, (self.grads if out is None else out)
+                return norm, (list(self.grads) if out is None else out)
         norm, handle = self._begin(stream)
         optr = None
         if out is not None:
@@ -1042,7 +1042,7 @@ class GradGroup:
                     optr, o.dtype, tuple(o.shape), o.device, g.dtype, tuple(g.shape), self.device))
         _check(_load().rtp_clip_grad_norm(len(self.grads), self._dtypes, self._numels, self._ptrs, self._counted,
                                           float(max_norm), optr, self._ws.data_ptr(), norm.data_ptr(), handle))
-        return norm, (self.grads if out is None else out)
+        return norm, (list(self.grads) if out is None else out)
 
 
 def grad_norm(grads, counted=None, stream=None):

@@ -107,3 +107,20 @@ def test_changed_groups_that_are_refused():
         for call in (group.norm, lambda: group.clip(1.0)):
             with pytest.raises(error):
                 call()
+
+
+@pytest.mark.gpu
+def test_the_result_is_the_callers_list():
+    """What a caller does with the list that clip returns does not change the group, nor does the list given to it."""
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    grads = [torch.ones(5, device="cuda"), torch.ones(9, device="cuda")]
+    group = rtp.GradGroup(grads)
+    for kw in ({}, {"stream": torch.cuda.current_stream()}):
+        _, got = group.clip(1e9, **kw)
+        assert type(got) is list and all(a is b for a, b in zip(got, grads))
+        got.pop()
+    grads.pop()
+    assert abs(float(group.norm()) - 14 ** 0.5) <= 2.0 ** -17 * 14 ** 0.5
+    out = [torch.empty(5, device="cuda"), torch.empty(9, device="cuda")]
+    assert group.clip(1e9, out=out)[1] is out
