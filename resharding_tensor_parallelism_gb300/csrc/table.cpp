@@ -6,6 +6,7 @@
 // passes 20 to 60 tensors, and a decoded token's product takes the GPU about as long
 // as that loop.
 #include <ATen/ops/empty.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -54,20 +55,15 @@ PyObject* table(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     for (Py_ssize_t d = 0; d < nd; ++d) shape[d] = PyLong_AsLongLong(PyTuple_GET_ITEM(args[1], d));
     if (PyErr_Occurred()) return nullptr;
     const at::IntArrayRef sizes(shape, (size_t)nd);
-    try {
-        std::vector<uint64_t> out((size_t)n);
-        for (Py_ssize_t i = 0; i < n; ++i) {
-            PyObject* o = PyList_GET_ITEM(args[0], i);
-            if (!THPVariable_Check(o)) return PyLong_FromSsize_t(i);
-            const at::Tensor& t = THPVariable_Unpack(o);
-            if (t.scalar_type() != want || t.sizes() != sizes || !placed(t, device)) return PyLong_FromSsize_t(i);
-            out[(size_t)i] = (uint64_t)(uintptr_t)t.data_ptr();
-        }
-        return pointers(out);
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
+    std::vector<uint64_t> out((size_t)n);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        PyObject* o = PyList_GET_ITEM(args[0], i);
+        if (!THPVariable_Check(o)) return PyLong_FromSsize_t(i);
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (t.scalar_type() != want || t.sizes() != sizes || !placed(t, device)) return PyLong_FromSsize_t(i);
+        out[(size_t)i] = (uint64_t)(uintptr_t)t.data_ptr();
     }
+    return pointers(out);
 }
 
 // like(tensors, references, device) -> bytes, or the index of the first tensor
@@ -82,20 +78,15 @@ PyObject* like(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     const long device = PyLong_AsLong(args[2]);
     if (PyErr_Occurred()) return nullptr;
     const Py_ssize_t n = PyList_GET_SIZE(args[0]);
-    try {
-        std::vector<uint64_t> out((size_t)n);
-        for (Py_ssize_t i = 0; i < n; ++i) {
-            PyObject *a = PyList_GET_ITEM(args[0], i), *b = PyList_GET_ITEM(args[1], i);
-            if (!THPVariable_Check(a) || !THPVariable_Check(b)) return PyLong_FromSsize_t(i);
-            const at::Tensor &t = THPVariable_Unpack(a), &r = THPVariable_Unpack(b);
-            if (t.scalar_type() != r.scalar_type() || t.sizes() != r.sizes() || !placed(t, device)) return PyLong_FromSsize_t(i);
-            out[(size_t)i] = (uint64_t)(uintptr_t)t.data_ptr();
-        }
-        return pointers(out);
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
+    std::vector<uint64_t> out((size_t)n);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        PyObject *a = PyList_GET_ITEM(args[0], i), *b = PyList_GET_ITEM(args[1], i);
+        if (!THPVariable_Check(a) || !THPVariable_Check(b)) return PyLong_FromSsize_t(i);
+        const at::Tensor &t = THPVariable_Unpack(a), &r = THPVariable_Unpack(b);
+        if (t.scalar_type() != r.scalar_type() || t.sizes() != r.sizes() || !placed(t, device)) return PyLong_FromSsize_t(i);
+        out[(size_t)i] = (uint64_t)(uintptr_t)t.data_ptr();
     }
+    return pointers(out);
 }
 
 // buffers(n, shape, dtype code, device) -> list of n new tensors (torch.empty of
@@ -328,15 +319,10 @@ PyObject* unchanged(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     unsigned long long at[3];
     for (int i = 0; i < 3; ++i) at[i] = PyLong_AsUnsignedLongLong(args[1 + i]);
     if (PyErr_Occurred()) return nullptr;
-    try {
-        auto p = [&](int i) { return reinterpret_cast<void*>((uintptr_t)at[i]); };
-        return PyBool_FromLong(PyList_GET_SIZE(args[4]) == n &&
-                               same(args[4], static_cast<const int32_t*>(p(0)), static_cast<const int64_t*>(p(1)),
-                                    static_cast<const void* const*>(p(2)), device));
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
-    }
+    auto p = [&](int i) { return reinterpret_cast<void*>((uintptr_t)at[i]); };
+    return PyBool_FromLong(PyList_GET_SIZE(args[4]) == n &&
+                           same(args[4], static_cast<const int32_t*>(p(0)), static_cast<const int64_t*>(p(1)),
+                                static_cast<const void* const*>(p(2)), device));
 }
 
 // clip(n, dtypes, numels, grads, counted, workspace, max_norm, out, tensors, device,
@@ -385,16 +371,35 @@ PyObject* clip(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     }
 }
 
-PyMethodDef methods[] = {
-    {"clip", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(clip)), METH_FASTCALL, nullptr},
-    {"unchanged", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(unchanged)), METH_FASTCALL, nullptr},
-    {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(bind)), METH_FASTCALL, nullptr},
-    {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(linear)), METH_FASTCALL, nullptr},
-    {"glu", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(glu)), METH_FASTCALL, nullptr},
-    {"buffers", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(buffers)), METH_FASTCALL, nullptr},
-    {"table", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(table)), METH_FASTCALL, nullptr},
-    {"like", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(like)), METH_FASTCALL, nullptr},
-    {nullptr, nullptr, 0, nullptr}};
+// A method of the module. No C++ exception leaves it: tensors that torch itself wraps,
+// or that have no storage, raise from the very calls that ask for their addresses.
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* method(PyObject* self, PyObject* const* args, Py_ssize_t nargs) noexcept
+{
+    try {
+        return F(self, args, nargs);
+    } catch (python_error& e) {
+        e.restore();
+    } catch (const c10::Error& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
+    } catch (const std::bad_alloc&) {
+        PyErr_NoMemory();
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        PyErr_SetString(PyExc_RuntimeError, "an unknown C++ exception");
+    }
+    return nullptr;
+}
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyMethodDef entry(const char* name)
+{
+    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(method<F>)), METH_FASTCALL, nullptr};
+}
+
+PyMethodDef methods[] = {entry<bind>("bind"),       entry<table>("table"),         entry<like>("like"),
+                         entry<buffers>("buffers"), entry<linear>("linear"),       entry<glu>("glu"),
+                         entry<clip>("clip"),       entry<unchanged>("unchanged"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_table", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
