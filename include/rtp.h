@@ -660,11 +660,27 @@ int rtp_wait_selftest(int kernel, unsigned long long limit_ns, uint32_t* out, rt
  *                        both layouts' piece extents before use, so a shift that
  *                        leaves the piece returns RTP_EINVAL, nothing launched;
  *   RTP_HOOK_FAIL_ALLOC  the next planning step fails as if host memory ran
- *                        out: the call returns RTP_ENOMEM, nothing launched.
+ *                        out: the call returns RTP_ENOMEM, nothing launched;
+ *   RTP_HOOK_NO_CLUSTERS the next product of rtp_tp_linear, rtp_tp_glu or their
+ *                        gradients with more than 128 rows finds no room for
+ *                        clusters of `arg` or more CTAs (a device without such a
+ *                        group of SMs) and runs in the forms that need none.
  * RTP_EINVAL for an unknown hook.
  */
-enum { RTP_HOOK_NONE = 0, RTP_HOOK_PLAN_SHIFT = 1, RTP_HOOK_FAIL_ALLOC = 2 };
+enum { RTP_HOOK_NONE = 0, RTP_HOOK_PLAN_SHIFT = 1, RTP_HOOK_FAIL_ALLOC = 2, RTP_HOOK_NO_CLUSTERS = 3 };
 int rtp_test_hook(int hook, int64_t arg);
+
+/*
+ * How many kernels of each form the calling thread's rtp_tp_linear, rtp_tp_glu and
+ * gradient calls have launched since it last asked (no page counterpart: tests see
+ * by it which form carried a product). Host only.
+ *   counts[RTP_PRODUCT_FEW]    the kernel for up to 128 rows
+ *   counts[RTP_PRODUCT_WHOLE]  clusters of one SM pair, taking whole tiles
+ *   counts[2 .. 4]             clusters of that many pairs, each pair multiplying one
+ *                              part of its tile's K range
+ */
+enum { RTP_PRODUCT_FEW = 0, RTP_PRODUCT_WHOLE = 1, RTP_PRODUCT_FORMS = 5 };
+int rtp_product_launches(int32_t* counts);
 
 /*
  * Text of the last error on the calling thread ("" if none): the reason the

@@ -111,6 +111,7 @@ def _load():
         "rtp_device_error": [vp, u32p],
         "rtp_wait_selftest": [c_int, ctypes.c_ulonglong, vp, vp],
         "rtp_test_hook": [c_int, ctypes.c_int64],
+        "rtp_product_launches": [i32p],
         "rtp_tp_mlp_overlap": [c_int, P(c_int)],
         "rtp_tp_mlp_sp": [c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, vpp, vpp, vpp, vpp,
                           vpp, vp],
@@ -1077,14 +1078,24 @@ def wait_selftest(limit_ns: int, out=None, stream=None, kernel: int = 0):
     return out
 
 
-HOOK_NONE, HOOK_PLAN_SHIFT, HOOK_FAIL_ALLOC = 0, 1, 2
+HOOK_NONE, HOOK_PLAN_SHIFT, HOOK_FAIL_ALLOC, HOOK_NO_CLUSTERS = 0, 1, 2, 3
 
 
 def test_hook(hook: int, arg: int = 0) -> None:
     """Arms a one-shot host-side fault for this thread's next reshard plan
     (rtp_test_hook): HOOK_PLAN_SHIFT moves a planned destination offset by
-    `arg` elements, HOOK_FAIL_ALLOC fails the planner's next allocation."""
+    `arg` elements, HOOK_FAIL_ALLOC fails the planner's next allocation; or,
+    HOOK_NO_CLUSTERS, for its next product of more than 128 rows: clusters of
+    `arg` or more CTAs find no room."""
     _check(_load().rtp_test_hook(int(hook), int(arg)))
+
+
+def product_launches() -> dict:
+    """Launches of each form by this thread's tp_linear, tp_glu and gradient calls since it last asked: "few" (up to 128
+    rows), "whole" (tiles of one SM pair), and 2, 3, 4 (pairs that share a tile's K range)."""
+    counts = (ctypes.c_int32 * 5)()
+    _check(_load().rtp_product_launches(counts))
+    return dict(zip(("few", "whole", 2, 3, 4), counts))
 
 
 def version() -> str:

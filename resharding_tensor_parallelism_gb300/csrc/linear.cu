@@ -587,4 +587,14 @@ int rtp_tp_glu_backward(int P, int64_t M, int64_t K, int64_t F, int64_t N, const
     });
 }
 
+int rtp_product_launches(int32_t* counts)
+{
+    if (!counts) return fail(RTP_EINVAL, "rtp_product_launches: NULL argument");
+    for (int i = 0; i < RTP_PRODUCT_FORMS; ++i) {
+        counts[i] = product_launches[i];
+        product_launches[i] = 0;
+    }
+    return RTP_OK;
+}
+
 }  // extern "C"

@@ -53,6 +53,9 @@ constexpr int LIN_FEW_ROWS = 128;
 int linear_sms(int* n);  // SMs of the current device; 0: found
 int launch_linear_few(const char* fn, const LinGemm& g, bool weights_ready, cudaStream_t stream);
 
+// This thread's launches by form (rtp_product_launches).
+extern thread_local int32_t product_launches[RTP_PRODUCT_FORMS];
+
 int take_linear_gemm_error(void* stream, uint32_t* code);
 int take_linear_split_error(void* stream, uint32_t* code);
 int take_linear_few_error(void* stream, uint32_t* code);

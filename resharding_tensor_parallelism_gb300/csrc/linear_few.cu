@@ -369,10 +369,13 @@ int launch_t(const char* fn, const Args& args, unsigned tiles, size_t smem, cuda
     cfg.numAttrs = 2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
     if (e != cudaSuccess) return fail(RTP_ECUDA, "%s: few-row launch failed: %s", fn, cudaGetErrorString(e));
+    ++product_launches[RTP_PRODUCT_FEW];
     return RTP_OK;
 }
 
 }  // namespace
+
+thread_local int32_t product_launches[RTP_PRODUCT_FORMS];
 
 int linear_sms(int* n)
 {

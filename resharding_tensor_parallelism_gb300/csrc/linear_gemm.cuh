@@ -764,9 +764,9 @@ inline cudaLaunchAttribute cluster_of(int ctas)
     return a;
 }
 
-// Resident clusters of `ctas` CTAs on the current device, asked once per device and
-// size (racing first calls compute the same value); sets the kernel's shared-memory
-// limit on the way.
+// Resident clusters of `ctas` CTAs on the current device, 0 where none fits (a device
+// or partition may have no such group of SMs), asked once per device and size (racing
+// first calls compute the same value); sets the kernel's shared-memory limit on the way.
 template <int CFG, bool SPLIT>
 int resident_clusters(const char* fn, int ctas, int* n)
 {
@@ -774,8 +774,8 @@ int resident_clusters(const char* fn, int ctas, int* n)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
     std::atomic<int>& slot = known[dev][ctas / 2];
-    *n = slot.load(std::memory_order_acquire);
-    if (*n) return RTP_OK;
+    *n = slot.load(std::memory_order_acquire) - 1;  // 0: not asked yet
+    if (*n >= 0) return RTP_OK;
     cudaError_t e = cudaFuncSetAttribute(linear_gemm_kernel<CFG, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<CFG, SPLIT>::bytes);
     if (e != cudaSuccess) return fail(RTP_ECUDA, "%s: cudaFuncSetAttribute: %s", fn, cudaGetErrorString(e));
     cudaLaunchConfig_t cfg = {};
@@ -786,8 +786,11 @@ int resident_clusters(const char* fn, int ctas, int* n)
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(n, linear_gemm_kernel<CFG, SPLIT>, &cfg);
-    if (e != cudaSuccess || *n <= 0) return fail(RTP_ECUDA, "%s: cudaOccupancyMaxActiveClusters: %s", fn, cudaGetErrorString(e));
-    slot.store(*n, std::memory_order_release);
+    if (e != cudaSuccess || *n < 0) {
+        cudaGetLastError();
+        *n = 0;
+    }
+    slot.store(*n + 1, std::memory_order_release);
     return RTP_OK;
 }
 
@@ -800,14 +803,16 @@ int launch_t(const char* fn, LinArgs& args, cudaStream_t stream)
         // more K blocks than adding it up costs.
         args.split = 1;
         double best = args.kbs;
+        int64_t none_from = INT64_MAX;  // CTAs of the clusters that are taken not to fit
+        take_hook(RTP_HOOK_NO_CLUSTERS, &none_from);
         for (int s = 2; s <= 4; ++s) {
+            const double cost = (double)args.kbs / s + SPLIT_COST + s;
+            if (args.kbs < 4 * s || cost >= best || 2 * s >= none_from) continue;
             int n = 0, st = resident_clusters<CFG, SPLIT>(fn, 2 * s, &n);
             if (st) return st;
-            const double cost = (double)args.kbs / s + SPLIT_COST + s;
-            if (args.total_tiles <= n && args.kbs >= 4 * s && cost < best) {
-                best = cost;
-                args.split = s;
-            }
+            if (args.total_tiles > n) continue;
+            best = cost;
+            args.split = s;
         }
         if (args.split == 1) return LIN_NOT_SPLIT;
         ctas = 2 * args.split;
@@ -815,6 +820,7 @@ int launch_t(const char* fn, LinArgs& args, cudaStream_t stream)
     } else {
         int st = resident_clusters<CFG, SPLIT>(fn, 2, &clusters);
         if (st) return st;
+        if (clusters <= 0) return fail(RTP_ECUDA, "%s: no pair of SMs fits a product's cluster", fn);
         if (args.total_tiles < clusters) clusters = args.total_tiles;
     }
     if (clusters <= 0) return RTP_OK;
@@ -830,6 +836,7 @@ int launch_t(const char* fn, LinArgs& args, cudaStream_t stream)
     cfg.numAttrs = 2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, linear_gemm_kernel<CFG, SPLIT>, args);
     if (e != cudaSuccess) return fail(RTP_ECUDA, "%s: product launch failed: %s", fn, cudaGetErrorString(e));
+    ++product_launches[SPLIT ? args.split : RTP_PRODUCT_WHOLE];
     return RTP_OK;
 }
 

@@ -113,6 +113,14 @@ void inject_alloc_fault()
     }
 }
 
+bool take_hook(int hook, int64_t* arg)
+{
+    if (g_hook != hook) return false;
+    g_hook = RTP_HOOK_NONE;
+    *arg = g_hook_arg;
+    return true;
+}
+
 int check_task_bounds(const char* fn, const std::vector<PlanTask>& tasks, const std::vector<int64_t>& src_vol,
                       const std::vector<int64_t>& dst_vol)
 {
@@ -457,7 +465,7 @@ int rtp_reshard_forms(rtp_dtype dtype, int ndim, const int64_t* shape, const rtp
 
 int rtp_test_hook(int hook, int64_t arg)
 {
-    if (hook != RTP_HOOK_NONE && hook != RTP_HOOK_PLAN_SHIFT && hook != RTP_HOOK_FAIL_ALLOC)
+    if (hook < RTP_HOOK_NONE || hook > RTP_HOOK_NO_CLUSTERS)
         return fail(RTP_EINVAL, "rtp_test_hook: unknown hook %d", hook);
     g_hook = hook;
     g_hook_arg = arg;

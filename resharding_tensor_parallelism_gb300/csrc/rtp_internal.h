@@ -91,6 +91,8 @@ int check_task_bounds(const char* fn, const std::vector<PlanTask>& tasks, const 
 // throws std::bad_alloc when the allocation-failure hook is armed (and
 // disarms it); it marks the host allocations of planning.
 void inject_alloc_fault();
+// Whether `hook` was armed: disarms it and gives its argument.
+bool take_hook(int hook, int64_t* arg);
 
 // ---- launches (boxing.cu) --------------------------------------------------------------
 // Executes planned tasks on `stream`; src/dst buffer arrays are indexed by Ref::rank.
