@@ -643,7 +643,8 @@ int rtp_device_error(rtp_stream stream, uint32_t* code);
  *             waits give up, record code 16 and the block stops: out[0] = 1.
  *   limit_ns  in [1e6, 1e9] (1 ms to 1 s), else RTP_EINVAL
  *   out       device pointer to 2 uint32 (16-byte aligned, caller-owned)
- * Asynchronous on `stream`.
+ * Asynchronous on `stream`. Products launched after kernel 1 may be set up beside it
+ * (they are programmatic dependents) and wait for its end.
  */
 int rtp_wait_selftest(int kernel, unsigned long long limit_ns, uint32_t* out, rtp_stream stream);
 
@@ -664,10 +665,18 @@ int rtp_wait_selftest(int kernel, unsigned long long limit_ns, uint32_t* out, rt
  *   RTP_HOOK_NO_CLUSTERS the next product of rtp_tp_linear, rtp_tp_glu or their
  *                        gradients with more than 128 rows finds no room for
  *                        clusters of `arg` or more CTAs (a device without such a
- *                        group of SMs) and runs in the forms that need none.
- * RTP_EINVAL for an unknown hook.
+ *                        group of SMs) and runs in the forms that need none;
+ *   RTP_HOOK_WAIT_LIMIT  the waits of their next kernel for up to 128 rows give up
+ *                        after `arg` ns (1 ms to 4 s) without progress instead of 4 s.
+ * RTP_EINVAL for an unknown hook or a limit outside its range.
  */
-enum { RTP_HOOK_NONE = 0, RTP_HOOK_PLAN_SHIFT = 1, RTP_HOOK_FAIL_ALLOC = 2, RTP_HOOK_NO_CLUSTERS = 3 };
+enum {
+    RTP_HOOK_NONE = 0,
+    RTP_HOOK_PLAN_SHIFT = 1,
+    RTP_HOOK_FAIL_ALLOC = 2,
+    RTP_HOOK_NO_CLUSTERS = 3,
+    RTP_HOOK_WAIT_LIMIT = 4
+};
 int rtp_test_hook(int hook, int64_t arg);
 
 /*

@@ -1078,7 +1078,7 @@ def wait_selftest(limit_ns: int, out=None, stream=None, kernel: int = 0):
     return out
 
 
-HOOK_NONE, HOOK_PLAN_SHIFT, HOOK_FAIL_ALLOC, HOOK_NO_CLUSTERS = 0, 1, 2, 3
+HOOK_NONE, HOOK_PLAN_SHIFT, HOOK_FAIL_ALLOC, HOOK_NO_CLUSTERS, HOOK_WAIT_LIMIT = 0, 1, 2, 3, 4
 
 
 def test_hook(hook: int, arg: int = 0) -> None:
@@ -1086,7 +1086,8 @@ def test_hook(hook: int, arg: int = 0) -> None:
     (rtp_test_hook): HOOK_PLAN_SHIFT moves a planned destination offset by
     `arg` elements, HOOK_FAIL_ALLOC fails the planner's next allocation; or,
     HOOK_NO_CLUSTERS, for its next product of more than 128 rows: clusters of
-    `arg` or more CTAs find no room."""
+    `arg` or more CTAs find no room; HOOK_WAIT_LIMIT, for its next one of up to
+    128 rows: waits give up after `arg` ns."""
     _check(_load().rtp_test_hook(int(hook), int(arg)))
 
 

@@ -47,6 +47,7 @@ struct Args {
     int32_t rows, cols, ntok, tmem_cols;
     int32_t split, stages;
     int32_t act, keep, weights_ready;
+    unsigned long long wait_ns;  // limit of a wait for this kernel's own progress
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
             uint32_t phase = early == a.stages ? 1u : 0u;
             int issued = early;
             for (int i = early; i < n; ++i) {
-                if (!wait_bar(empty_bar(s), phase ^ 1u, abort_flag, ERR_PRODUCER)) break;
+                if (!wait_bar(empty_bar(s), phase ^ 1u, abort_flag, ERR_PRODUCER, a.wait_ns)) break;
                 mbar_expect_tx(full_bar(s), stage_bytes);
                 load_w(i, s);
                 load_x(i, s);
@@ -217,8 +218,12 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
             int s = 0;
             uint32_t phase = 0;
             bool ok = true;
+            // The rows are fetched once the previous kernel is complete, so nothing is
+            // lost by waiting for it here too, and the limit of the waits below then
+            // covers this kernel's progress, not that kernel's run time.
+            asm volatile("griddepcontrol.wait;" ::: "memory");
             for (int i = 0; i < n; ++i) {
-                if (!wait_bar(full_bar(s), phase, abort_flag, ERR_MMA_STAGE)) {
+                if (!wait_bar(full_bar(s), phase, abort_flag, ERR_MMA_STAGE, a.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
     int i0 = part * THREADS + (int)threadIdx.x;
     fetch(i0);
     int ok = 1;
-    if (lane == 0) ok = wait_bar(acc_bar, 0, abort_flag, ERR_EPILOGUE) ? 1 : 0;
+    if (lane == 0) ok = wait_bar(acc_bar, 0, abort_flag, ERR_EPILOGUE, a.wait_ns) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
     tc_fence_after();
     if (ok) {
@@ -427,6 +432,9 @@ int launch_linear_few(const char* fn, const LinGemm& p, bool weights_ready, cuda
     a.cols = (int)p.cols;
     a.act = p.act;
     a.weights_ready = weights_ready;
+    int64_t wait_ns = (int64_t)WAIT_LIMIT_NS;
+    take_hook(RTP_HOOK_WAIT_LIMIT, &wait_ns);
+    a.wait_ns = (unsigned long long)wait_ns;
     const int64_t tiles = (int64_t)outs * a.tiles;
     if (tiles * MAX_SPLIT >= ((int64_t)1 << 31)) return fail(RTP_ESHAPE, "%s: too many tiles", fn);
     // K parts: one CTA an SM as long as each has 4 K blocks, two an SM as long as each

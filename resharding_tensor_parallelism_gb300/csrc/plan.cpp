@@ -465,8 +465,10 @@ int rtp_reshard_forms(rtp_dtype dtype, int ndim, const int64_t* shape, const rtp
 
 int rtp_test_hook(int hook, int64_t arg)
 {
-    if (hook < RTP_HOOK_NONE || hook > RTP_HOOK_NO_CLUSTERS)
+    if (hook < RTP_HOOK_NONE || hook > RTP_HOOK_WAIT_LIMIT)
         return fail(RTP_EINVAL, "rtp_test_hook: unknown hook %d", hook);
+    if (hook == RTP_HOOK_WAIT_LIMIT && (arg < 1000000 || arg > 4000000000))
+        return fail(RTP_EINVAL, "rtp_test_hook: limit %lld ns outside [1 ms, 4 s]", (long long)arg);
     g_hook = hook;
     g_hook_arg = arg;
     g_plan_cache.clear();  // the next reshard or shard plans afresh
