@@ -935,6 +935,20 @@ class GradGroup:
     workspace is allocated and zeroed (default: the current stream)."""
 
     def __init__(self, grads, counted=None, stream=None):
+        self._set_up(grads, counted, stream)
+        torch = _torch()
+        with _allocating_on(stream):  # when the workspace is zero, for other streams (_join)
+            if not torch.cuda.is_current_stream_capturing():
+                self._zeroed = torch.cuda.current_stream(self.device).record_event()
+
+    @classmethod
+    def _for_one_call(cls, grads, counted, stream):
+        """A group for one call on the stream given, which needs no event for other streams (15 us)."""
+        group = cls.__new__(cls)
+        group._set_up(grads, counted, stream)
+        return group
+
+    def _set_up(self, grads, counted, stream):
         torch = _torch()
         self.grads = list(grads)
         n = len(self.grads)
@@ -952,8 +966,6 @@ class GradGroup:
         with _allocating_on(stream):
             self._ws = torch.zeros((_load().rtp_grad_workspace_bytes(n) // 8,), dtype=torch.float64, device=self.device)
             self._zeroed = None
-            if not torch.cuda.is_current_stream_capturing():
-                self._zeroed = torch.cuda.current_stream(self.device).record_event()
             self._index = self.device.index
             # handles of the streams that may use the workspace as it is: the one that zeroed it, and those of _join
             self._joined = {torch._C._cuda_getCurrentRawStream(self._index) or None}
@@ -1048,12 +1060,12 @@ class GradGroup:
 
 def grad_norm(grads, counted=None, stream=None):
     """Global norm of a list of gradients (GradGroup.norm without keeping a group)."""
-    return GradGroup(grads, counted, stream).norm(stream)
+    return GradGroup._for_one_call(grads, counted, stream).norm(stream)
 
 
 def clip_grad_norm(grads, max_norm: float, counted=None, out=None, stream=None):
     """Clips a list of gradients by their global norm (GradGroup.clip without keeping a group)."""
-    return GradGroup(grads, counted, stream).clip(max_norm, out, stream)
+    return GradGroup._for_one_call(grads, counted, stream).clip(max_norm, out, stream)
 
 
 def device_error(stream=None) -> int:
