@@ -1,12 +1,15 @@
 // The activations of rtp_tp_linear and rtp_tp_glu (rtp_act) and their
 // derivatives, in float32 on the float32 accumulator.
-//   GELU       x Phi(x);  d = Phi(x) + x phi(x).  Phi from formula 7.1.26 of Abramowitz
-//              and Stegun, "Handbook of Mathematical Functions" (erfc z = (a1 t + ... +
-//              a5 t^5) e^(-z^2), t = 1 / (1 + p z), absolute error below 1.5e-7), with
-//              z = |x| / sqrt 2: its exponential is that of phi, so value and slope
-//              together take one exponential and one quotient, and the lower tail is
-//              not a difference from 1. With erff and expf the element-wise step of the
-//              linear layer's backward (16384 x 4096) was bound by arithmetic: 168 us.
+//   GELU       x Phi(x);  d = Phi(x) + x phi(x).  Phi(-|x|) = e^(-x^2 / 2) R(|x|), where
+//              R(a) = e^(a^2 / 2) Phi(-a) is smooth, falls from 1/2 like 1 / (a sqrt(2 pi)),
+//              and is a polynomial of degree 7 in t = 1 / (1 + 0.34 a): weighted least
+//              squares on Chebyshev nodes in t, reweighted by the error until it was level
+//              (Lawson's method), for |x| up to 14.6, where Phi underflows. In float32 it is
+//              within 4e-7 of R up to |x| = 4 and 5e-6 beyond, Phi within 2e-7: the tail is
+//              relative to itself, not a difference from 1. Its exponential is that of phi, so
+//              value and slope together take one exponential and one quotient. With erff and
+//              expf the element-wise step of the linear layer's backward (16384 x 4096) was
+//              bound by arithmetic: 168 us.
 //   GELU_TANH  x s(2z), z = sqrt(2 / pi) (x + 0.044715 x^3), since (1 + tanh z) / 2 = s(2z),
 //              s(v) = 1 / (1 + e^-v); this form keeps its relative accuracy where tanh z is near -1
 //   SILU       x s(x);  d = s(x) (1 + x (1 - s(x)))
@@ -21,13 +24,15 @@ namespace {
 
 // e^v and 1 / v by the approximate base-2 exponential and reciprocal instructions
 // (2^-22 and 1 ulp; subnormal results and operands count as zero): e^v is off by
-// 2^-22 + |v| 2^-24 relative (the rounding of v log2 e), far below bf16's 2^-9.
-__device__ __forceinline__ float exp_fast(float v)
+// 2^-22 + |v| 2^-24 relative (the rounding of v log2 e; GELU's exponent is rounded
+// twice more), at most 2^-15, against bf16's 2^-8.
+__device__ __forceinline__ float exp2_fast(float v)
 {
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.44269504088896340736f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+__device__ __forceinline__ float exp_fast(float v) { return exp2_fast(v * 1.44269504088896340736f); }
 __device__ __forceinline__ float rcp_fast(float v)
 {
     float r;
@@ -43,10 +48,11 @@ constexpr float kTanhCubic = 0.044715f;
 // Phi(x); e receives e^(-x^2 / 2).
 __device__ __forceinline__ float normal_cdf(float x, float& e)
 {
-    e = exp_fast(-0.5f * x * x);
-    const float t = rcp_fast(1.0f + 0.3275911f * 0.70710678118654752440f * fabsf(x));
-    const float p = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-    const float tail = 0.5f * p * e;
+    e = exp2_fast(x * (x * (-0.5f * 1.44269504088896340736f)));
+    const float t = rcp_fast(1.0f + 0.34f * fabsf(x));
+    const float r = -5.8135998e-05f + t * (1.3688410e-01f + t * (1.2466286e-01f + t * (1.7229286e-01f + t * (-5.8451386e-02f +
+                    t * (2.9221521e-01f + t * (-2.1582676e-01f + t * 4.8281305e-02f))))));
+    const float tail = r * e;
     return x < 0.0f ? tail : 1.0f - tail;
 }
 
