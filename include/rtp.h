@@ -465,7 +465,12 @@ int rtp_tp_mlp_noalloc(int P, int64_t M, int64_t K, int64_t F, int64_t N, const 
                        const void* const* B_shards, float* Z, rtp_stream stream);
 
 /* Activations of rtp_tp_linear and rtp_tp_glu: identity; x Phi(x) (erf); its tanh
- * form x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2; x / (1 + e^-x); max(x, 0). */
+ * form x (1 + tanh(z)) / 2, z = sqrt(2 / pi) (x + 0.044715 x^3); x / (1 + e^-x); max(x, 0).
+ * Of the float32 pre-activation x, in float32. Values that stay float32 are within
+ * 2^-21 (SILU), 2^-19 (GELU) and 2^-21 (1 + 2 |z|) (GELU_TANH) of themselves. Values that
+ * are rounded to bf16, and slopes, use approximate exponentials: the value rounded is
+ * within 2^-13 of itself, and exponentials below 2^-126 count as zero (SILU below -87).
+ * rtp_tp_mlp's GELU is (1 + erff) / 2, whose lower tail is a difference from 1. */
 typedef enum {
     RTP_ACT_NONE = 0,
     RTP_ACT_GELU = 1,

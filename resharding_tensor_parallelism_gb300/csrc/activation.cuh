@@ -14,6 +14,13 @@
 //              s(v) = 1 / (1 + e^-v); this form keeps its relative accuracy where tanh z is near -1
 //   SILU       x s(x);  d = s(x) (1 + x (1 - s(x)))
 //   RELU       max(x, 0), a NaN passes;  d = 1 for x > 0
+// Values that are rounded to bf16, and slopes, take the approximate exponential below.
+// Values that stay float32 (FINE) take expf, and GELU one degree more (c = 0.3, within
+// 6e-8 of R, 8e-7 with the roundings) and what float32 drops of x^2: relative to
+// themselves they are off by at most 2^-21 (SILU), 2^-19 (GELU), 2^-21 (1 + 2 |z|)
+// (GELU_TANH, whose argument is rounded too). 4096 x 512 x 4096, float32, against the
+// approximate forms: SILU 32.6 -> 35.7 us, GELU_TANH 33.7 -> 37.5, GELU 34.8 -> 43.1;
+// with normcdff and the rounded reciprocal 105, 113 and 97 (bf16 outputs: 33.7, 34.9, 36.1).
 #pragma once
 
 #include "rtp.h"
@@ -45,23 +52,49 @@ __device__ __forceinline__ float logistic(float v) { return rcp_fast(1.0f + exp_
 constexpr float kTanhScale = 1.5957691216057307f;  // 2 sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
 
-// Phi(x); e receives e^(-x^2 / 2).
+// Phi(x); e receives e^(-x^2 / 2). FINE: the exponent with the part of x^2 that float32
+// drops (|x| is held to 20, where Phi has underflowed, so that x^2 stays finite).
+template <bool FINE>
 __device__ __forceinline__ float normal_cdf(float x, float& e)
 {
-    e = exp2_fast(x * (x * (-0.5f * 1.44269504088896340736f)));
-    const float t = rcp_fast(1.0f + 0.34f * fabsf(x));
-    const float r = -5.8135998e-05f + t * (1.3688410e-01f + t * (1.2466286e-01f + t * (1.7229286e-01f + t * (-5.8451386e-02f +
-                    t * (2.9221521e-01f + t * (-2.1582676e-01f + t * 4.8281305e-02f))))));
+    float r;
+    if constexpr (FINE) {
+        const float a = fminf(fabsf(x), 20.0f), sq = a * a, rest = fmaf(a, a, -sq);
+        e = expf(-0.5f * sq);
+        e = fmaf(e, -0.5f * rest, e);
+        const float t = rcp_fast(1.0f + 0.3f * a);
+        r = 7.4024868e-06f + t * (1.19483696e-01f + t * (1.21948972e-01f + t * (9.45713255e-02f + t * (1.42799533e-01f +
+            t * (-7.68893970e-02f + t * (2.28995354e-01f + t * (-1.69328611e-01f + t * 3.84117550e-02f)))))));
+    } else {
+        e = exp2_fast(x * (x * (-0.5f * 1.44269504088896340736f)));
+        const float t = rcp_fast(1.0f + 0.34f * fabsf(x));
+        r = -5.8135998e-05f + t * (1.3688410e-01f + t * (1.2466286e-01f + t * (1.7229286e-01f + t * (-5.8451386e-02f +
+            t * (2.9221521e-01f + t * (-2.1582676e-01f + t * 4.8281305e-02f))))));
+    }
     const float tail = r * e;
     return x < 0.0f ? tail : 1.0f - tail;
 }
 
-template <int ACT>
+// x s(u) for u of x's sign, float32: s(u) = 1 / (1 + e^-u), or, below 0, e^u / (1 + e^u).
+// Below -80 e^u counts as nothing beside 1, and is multiplied in as two halves, so
+// that no factor is subnormal before the value is.
+__device__ __forceinline__ float logistic_times(float x, float u)
+{
+    const bool low = u < -80.0f;
+    const float e = expf(low ? 0.5f * u : -fabsf(u));
+    return (u < 0.0f ? x * e : x) * (low ? e : rcp_fast(1.0f + e));
+}
+
+template <int ACT, bool FINE = false>
 __device__ __forceinline__ float act_value(float x)
 {
+    if constexpr (FINE) {
+        if constexpr (ACT == RTP_ACT_GELU_TANH) return logistic_times(x, kTanhScale * (x + kTanhCubic * x * x * x));
+        if constexpr (ACT == RTP_ACT_SILU) return logistic_times(x, x);
+    }
     if constexpr (ACT == RTP_ACT_GELU) {
         float e;
-        return x * normal_cdf(x, e);
+        return x * normal_cdf<FINE>(x, e);
     }
     if constexpr (ACT == RTP_ACT_GELU_TANH) return x * logistic(kTanhScale * (x + kTanhCubic * x * x * x));
     if constexpr (ACT == RTP_ACT_SILU) return x * logistic(x);
@@ -75,7 +108,7 @@ __device__ __forceinline__ void act_both(float x, float& a, float& d)
 {
     if constexpr (ACT == RTP_ACT_GELU) {
         float e;
-        const float cdf = normal_cdf(x, e);
+        const float cdf = normal_cdf<false>(x, e);
         a = x * cdf;
         d = cdf + 0.39894228040143267794f * x * e;
     } else if constexpr (ACT == RTP_ACT_GELU_TANH) {

@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
             }
             with_act(a.act, [&](auto tag) {
                 constexpr int ACT = decltype(tag)::value;
-                v[j] = make_float4(act_value<ACT>(v[j].x), act_value<ACT>(v[j].y), act_value<ACT>(v[j].z),
-                                   act_value<ACT>(v[j].w));
+                v[j] = make_float4(act_value<ACT, F32>(v[j].x), act_value<ACT, F32>(v[j].y), act_value<ACT, F32>(v[j].z),
+                                   act_value<ACT, F32>(v[j].w));
             });
             v[j] = EPI == LIN_GLU ? mul4(v[j], u[j]) : add4(v[j], x[j]);
             if constexpr (F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out[g]) + at) = v[j];

@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_ke
                         if constexpr (ACT)
                             with_act(a.act, [&](auto tag) {
 #pragma unroll
-                                for (int j = 0; j < STEP; ++j) v[j] = act_value<decltype(tag)::value>(v[j]);
+                                for (int j = 0; j < STEP; ++j) v[j] = act_value<decltype(tag)::value, F32>(v[j]);
                             });
                         if (F32 ? a.has_residual != 0 : has_in) {
                             float x[STEP] = {};

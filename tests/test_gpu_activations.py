@@ -77,3 +77,44 @@ def test_bf16_outputs_are_rounded_once(act, M, what):
     err = 2.0 ** -13 * ref.abs() + TINY
     bad = ~((got >= (ref - err).to(BF16)) & (got <= (ref + err).to(BF16)))
     assert not bool(bad.any()), (act, float(x[bad][0]), float(got[bad][0]), float(ref[bad][0]), int(bad.sum()))
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M,K,form", [(128, 8, "few"), (256, 8, "whole"), (256, 2056, 4)])
+def test_float32_outputs_keep_float32(act, M, K, form):
+    """Relative to the value, tails included: e^u is off by at most one unit (2^-23), or twice as much where it is
+    multiplied in as two halves, the reciprocal by one unit, and three roundings of 2^-24 follow: 3.5 2^-23, held to
+    2^-21. tanh's argument u is off by at most 8 roundings of 2^-24 first: |u| 2^-21 more. GELU's polynomial is within
+    8e-7 with its roundings and its quotient's, the exponential within 3 2^-24, two roundings follow: 1.1e-6, held to
+    2^-19. Below 2^-126 numbers are spaced 2^-149. The bias gives the numbers between bf16's."""
+    x = _bf16_numbers(-13.5 if act == "gelu" else -10.0 if act == "gelu_tanh" else -100.0, 40.0)
+    bias = torch.tensor([0, 1, -1, 3, -5, 7, 11, -13], device="cuda").mul(2.0 ** -12).to(BF16)
+    W = torch.zeros((K, 8), dtype=BF16, device="cuda")
+    W[0] = 1
+
+    def call(X, act):
+        wide = torch.zeros((M, K), dtype=BF16, device="cuda")
+        wide[:, 0] = X[:, 0]
+        rtp.product_launches()
+        got = rtp.tp_linear(wide, [W], act=act, bias=[bias], out_dtype=F32)[0]
+        assert rtp.product_launches()[form] == 1
+        return got
+
+    got = _through(x, act, M, call).double()
+    x = (x.float()[:, None] + bias.float()).double()  # one float32 addition, as the kernel's
+    ref = _exact(act, x)
+    u = 2 * (2 / torch.pi) ** 0.5 * (x + 0.044715 * x ** 3)
+    rel = 2.0 ** -19 if act == "gelu" else 2.0 ** -21 * (1 + u.abs()) if act == "gelu_tanh" else 2.0 ** -21
+    bad = ~((got - ref).abs() <= rel * ref.abs() + 2.0 ** -140)
+    assert not bool(bad.any()), (act, float(x[bad][0]), float(got[bad][0]), float(ref[bad][0]), int(bad.sum()))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M", [16, 256])
+def test_special_values(dtype, M):
+    """NaN stays, +inf stays, 0 stays, and numbers far out give x or 0, in every activation."""
+    x = torch.tensor([float("nan"), float("inf"), 0.0, -0.0, 3e38, -3e38, 1e25, -1e25, 200.0, -200.0], device="cuda").to(BF16)
+    for act in ("gelu", "gelu_tanh", "silu", "relu"):
+        got = _through(x, act, M, _linear(dtype))
+        assert bool(got[0].isnan()) and float(got[1]) == float("inf") and not bool(got[2:4].any())
+        assert got[4:].tolist() == [v if v > 0 else 0.0 for v in x[4:].tolist()], act
