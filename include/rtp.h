@@ -648,7 +648,7 @@ int rtp_device_error(rtp_stream stream, uint32_t* code);
  *             waits give up, record code 16 and the block stops: out[0] = 1.
  *   limit_ns  in [1e6, 1e9] (1 ms to 1 s), else RTP_EINVAL
  *   out       device pointer to 2 uint32 (16-byte aligned, caller-owned)
- * Asynchronous on `stream`. Products launched after kernel 1 may be set up beside it
+ * Asynchronous on `stream`. Products launched after kernel 0 may be set up beside it
  * (they are programmatic dependents) and wait for its end.
  */
 int rtp_wait_selftest(int kernel, unsigned long long limit_ns, uint32_t* out, rtp_stream stream);

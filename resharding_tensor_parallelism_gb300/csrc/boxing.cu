@@ -98,11 +98,9 @@ __device__ __noinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned lo
 // Self-test of the bounded wait above: every thread of one block waits (as a
 // staged chunk does) on an mbarrier whose transaction bytes never arrive; the
 // waits give up after limit_ns, record kErrBulkWait, and the block agrees to
-// stop. out[0] = 1 when the block stopped on the failed wait. Kernels launched as its
-// programmatic dependents may begin beside it, as beside a product.
+// stop. out[0] = 1 when the block stopped on the failed wait.
 __global__ void bulk_wait_selftest_kernel(unsigned long long limit_ns, uint32_t* out)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ __align__(8) uint64_t bar;
     if (threadIdx.x == 0) {
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(su32(&bar)) : "memory");

@@ -139,9 +139,11 @@ struct GemmArgs {
 // Self-test of the bounded wait: two threads wait on an mbarrier that nothing
 // completes. The first gives up after limit_ns, records ERR_SELFTEST and raises
 // the abort flag; the second leaves on the flag. out[w] = 1 if waiter w gave up.
-// The mbarrier is never armed or awaited again, so nothing is left in flight.
+// The mbarrier is never armed or awaited again, so nothing is left in flight. Kernels
+// launched as its programmatic dependents may begin beside it, as beside a product.
 __global__ void wait_selftest_kernel(unsigned long long limit_ns, uint32_t* out)
 {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ __align__(8) uint64_t bar;
     __shared__ uint32_t abort_word;
     volatile uint32_t* abort_flag = &abort_word;
