@@ -505,8 +505,10 @@ enum { RTP_SPLIT_COLUMN = 0, RTP_SPLIT_ROW = 1 };
  * multiples of 8 (RTP_ESHAPE); P <= 8 (RTP_EUNSUPPORTED); pointers 16-byte
  * aligned, no overlap of outputs with anything (RTP_EINVAL for the alignment; an
  * overlap is not detected). M == 0 launches nothing, and buffers of M rows may then
- * be NULL. Errors leave nothing launched; nothing is allocated; results do not
- * change from run to run.
+ * be NULL. Arguments are checked before the first launch: RTP_EINVAL, RTP_ESHAPE and
+ * RTP_EUNSUPPORTED leave nothing launched. RTP_ECUDA (a launch that failed) leaves the
+ * kernels queued that the call had launched before it. Nothing is allocated; results
+ * do not change from run to run.
  * A product with few rows or few tiles cuts its K range over a cluster of SMs, so a
  * row's bits may depend on how many rows go with it.
  * Like the GEMMs of rtp_tp_mlp, the products are launched as programmatic

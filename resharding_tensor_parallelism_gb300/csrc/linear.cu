@@ -143,7 +143,11 @@ LinGemm rows_from(const LinGemm& p, int64_t first)
 // 41.3 us, 1024 x 16384 x 4096 (16) 158 -> 108 and 111, 2304 x 2048 x 2048 (8) 28.8 -> 25.8
 // and 27.0. The other side: 2048 x 4096 x 9728 (38) 109 -> 113 and 117, 1024 x 1024 x 4096
 // (16, 16 K blocks) 20.5 -> 19.9 and 21.0; with 96 and 128 rows over most of the gain is gone.
-// At the limits (64 rows, 25 column tiles, 32 K blocks) 28.8 -> 29.4.
+// At the limits (64 rows, 25 column tiles, 32 K blocks) 28.8 -> 29.4. Between 25 and 38
+// column tiles (4 to 8 row tiles, 1 and 64 rows over) 32 K blocks come out even or lose:
+// 30 tiles 38.9 -> 39.5 and 39.0 -> 40.9 us, 36 tiles 38.7 -> 39.1 and 39.0 -> 41.2; with 64 K
+// blocks both would still gain, 64.9 -> 57.7 and 65.3 -> 60.2, 84.6 -> 80.2 and 84.8 -> 82.4.
+// The limit on column tiles is the one that holds for every K.
 int64_t rest_rows(const LinGemm& p)
 {
     constexpr int64_t MAX_REST = 64, MIN_K = 32 * 64;

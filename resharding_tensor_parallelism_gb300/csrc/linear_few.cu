@@ -405,7 +405,8 @@ int launch_linear_few(const char* fn, const LinGemm& p, bool weights_ready, cuda
     const int cta_cols = p.epi == LIN_GLU ? FEAT / 2 : FEAT;
     a.ntok = (int)((p.rows + 15) / 16 * 16);
     for (a.tmem_cols = 32; a.tmem_cols < a.ntok;) a.tmem_cols *= 2;
-    // the ring also has to hold a partial tile (512 bytes a token): 64 KB of at least 96
+    // The ring also holds a partial tile, 512 bytes a token: 64 KB at most, while the
+    // smallest ring (96 tokens, 3 stages of 28 KB) has 84.
     const size_t stage = W_BYTES + (size_t)a.ntok * (BK * 2);
     a.stages = (int)((SMEM_LIMIT - SMEM_EXTRA) / stage);
     if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
