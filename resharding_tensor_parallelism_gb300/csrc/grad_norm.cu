@@ -23,8 +23,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
-#include <cstring>
 #include <vector>
 
 #include "rtp_internal.h"
@@ -258,21 +256,6 @@ __global__ void __launch_bounds__(T) grad_scale_kernel(const __grid_constant__ T
 
 // ---- host side --------------------------------------------------------------------
 
-int sm_count(const char* fn, int* n)
-{
-    static std::atomic<int> sms[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
-    int v = sms[dev].load(std::memory_order_acquire);
-    if (!v) {
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
-            return fail(RTP_ECUDA, "%s: cudaDeviceGetAttribute failed", fn);
-        sms[dev].store(v, std::memory_order_release);
-    }
-    *n = v;
-    return RTP_OK;
-}
-
 size_t esize(int dtype) { return dtype == RTP_F32 ? 4 : 2; }
 
 // The launches of one pass over `items` (chunk0 not yet set), in chunks of
@@ -426,8 +409,8 @@ int norm_impl(const char* fn, int n, const int32_t* dtypes, const int64_t* numel
         if (!best || r.hi > best->hi) best = &r;
     }
     const bool in_place = clip && !out;
-    int sms = 0, st;
-    if ((st = sm_count(fn, &sms))) return st;
+    int sms = 0;
+    if (device_sms(&sms)) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Shared* sh = static_cast<Shared*>(workspace);
     if (all.size() <= SMALL) return run<SMALL>(fn, in, all, bytes, sh, clip, max_norm, in_place, norm, sms, s);

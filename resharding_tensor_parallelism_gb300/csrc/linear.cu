@@ -154,7 +154,7 @@ int64_t rest_rows(const LinGemm& p)
     const int64_t rest = p.rows % LIN_TILE_ROWS, m_tiles = p.rows / LIN_TILE_ROWS;
     const int64_t k = p.kdim * (p.fused ? p.groups : 1);
     int sms = 0;
-    if (!rest || rest > MAX_REST || !m_tiles || k < MIN_K || linear_sms(&sms) || sms < 2) return 0;
+    if (!rest || rest > MAX_REST || !m_tiles || k < MIN_K || device_sms(&sms) || sms < 2) return 0;
     const int64_t pairs = sms / 2, tile_cols = p.epi == LIN_GLU ? LIN_TILE_COLS / 2 : LIN_TILE_COLS;
     const int64_t n_tiles = (p.fused ? 1 : p.groups) * ((p.cols + tile_cols - 1) / tile_cols);
     if (3 * n_tiles > pairs) return 0;

@@ -50,7 +50,6 @@ int launch_linear_gemm(const char* fn, const LinGemm& g, cudaStream_t stream);
 // stream since a kernel that waited for its own predecessor writes B, so B may be
 // read before the previous kernel has finished.
 constexpr int LIN_FEW_ROWS = 128;
-int linear_sms(int* n);  // SMs of the current device; 0: found
 int launch_linear_few(const char* fn, const LinGemm& g, bool weights_ready, cudaStream_t stream);
 
 // This thread's launches by form (rtp_product_launches).

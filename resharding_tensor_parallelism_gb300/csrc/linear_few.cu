@@ -50,13 +50,6 @@ struct Args {
     unsigned long long wait_ns;  // limit of a wait for this kernel's own progress
 };
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-}
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate)
 {
@@ -70,25 +63,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(cluster_addr));
-    return v;
 }
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr)
 {
@@ -285,6 +259,7 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
         for (int c = 16 * (warp >> 2); c < a.rows; c += 16 * (THREADS / 128)) {
             uint32_t r[16];
             tmem_ld_16cols(taddr + (uint32_t)c, r);
+            tmem_ld_wait(r);
             const uint32_t dst = smem + 4u * (uint32_t)(c * FEAT + quarter * 32 + lane);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
@@ -382,7 +357,7 @@ int launch_t(const char* fn, const Args& args, unsigned tiles, size_t smem, cuda
 
 thread_local int32_t product_launches[RTP_PRODUCT_FORMS];
 
-int linear_sms(int* n)
+int device_sms(int* n)
 {
     static std::atomic<int> sms[64];
     int dev = 0;
@@ -399,7 +374,7 @@ int linear_sms(int* n)
 int launch_linear_few(const char* fn, const LinGemm& p, bool weights_ready, cudaStream_t stream)
 {
     int st, sms = 0;
-    if (linear_sms(&sms)) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
+    if (device_sms(&sms)) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
     static thread_local Args a;
     std::memset(&a, 0, sizeof a);
     const int cta_cols = p.epi == LIN_GLU ? FEAT / 2 : FEAT;
@@ -452,16 +427,6 @@ int launch_linear_few(const char* fn, const LinGemm& p, bool weights_ready, cuda
                      : launch_t<LIN_OUT, false>(fn, a, (unsigned)tiles, smem, stream);
 }
 
-int take_linear_few_error(void* stream, uint32_t* code)
-{
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_tp_error, sizeof v, 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_tp_error, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return fail(RTP_ECUDA, "rtp_device_error: %s", cudaGetErrorString(cudaGetLastError()));
-    *code = v;
-    return RTP_OK;
-}
+int take_linear_few_error(void* stream, uint32_t* code) { return take_tp_error(stream, code); }
 
 }  // namespace rtp

@@ -6,21 +6,10 @@ namespace rtp {
 
 namespace {
 
-// Map of a row-major [rows, cols] buffer that the epilogue stores to or reads from:
-// boxes of 32 x 32, swizzled by the width of their rows.
+// Map of a whole row-major [rows, cols] buffer that the epilogue stores to or reads from.
 int epi_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, bool f32)
 {
-    auto fn = encode_fn();
-    if (!fn) return fail(RTP_ECUDA, "epilogue map: cuTensorMapEncodeTiled is unavailable");
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)(cols * (f32 ? 4 : 2))};
-    cuuint32_t box[2] = {32u, 32u};
-    cuuint32_t estr[2] = {1u, 1u};
-    CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr),
-                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(RTP_ECUDA, "epilogue map: cuTensorMapEncodeTiled failed (%d)", (int)r);
-    return RTP_OK;
+    return encode_out_map(m, ptr, rows, cols, cols, f32);
 }
 
 // Encodes a map, or copies the previous group's when it is of the same buffer
@@ -94,7 +83,7 @@ int launch_linear_gemm(const char* fn, const LinGemm& p, cudaStream_t stream)
 int take_linear_gemm_error(void* stream, uint32_t* code)
 {
     uint32_t split = 0;
-    int st = take_error(stream, code);
+    int st = take_tp_error(stream, code);
     if (st || (st = take_linear_split_error(stream, &split))) return st;
     if (!*code) *code = split;
     return RTP_OK;

@@ -73,33 +73,10 @@ constexpr int SPLIT_COST = 12;       // K blocks of time (0.28 us each) that a s
 // code costs an instruction fetch in every step of the epilogue)
 enum : int { CFG_A_T = 1, CFG_B_T = 2, CFG_F32 = 4, CFG_ACT = 8, CFG_EPI_SHIFT = 4 };
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-}
 // 16 or 32 accumulator columns of this warp's 32 lanes; the registers are valid
-// after tmem_wait (which takes them as operands, so that no use moves above it).
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
+// after tmem_wait.
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_16cols(taddr, r); }
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) { tmem_ld_wait(r); }
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32cols(taddr, r); }
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) { tmem_ld_wait(r); }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
@@ -115,14 +92,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(cluster_addr));
-    return v;
-}
 // The barrier at the same address in both CTAs of a pair (mask: their ranks in the cluster).
 __device__ __forceinline__ void mma_commit_both(uint32_t bar, uint16_t mask)
 {
@@ -856,19 +825,6 @@ int launch_cfg(const char* fn, int cfg, LinArgs& a, cudaStream_t stream)
     case CFG_B_T | CFG_F32: return launch_t<CFG_B_T | CFG_F32, SPLIT>(fn, a, stream);
     default: return fail(RTP_EUNSUPPORTED, "%s: no product for transposed operands of this kind", fn);
     }
-}
-
-// Reads and clears this translation unit's device error word.
-inline int take_error(void* stream, uint32_t* code)
-{
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_tp_error, sizeof v, 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_tp_error, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return fail(RTP_ECUDA, "rtp_device_error: %s", cudaGetErrorString(cudaGetLastError()));
-    *code = v;
-    return RTP_OK;
 }
 
 }  // namespace

@@ -9,6 +9,6 @@ int launch_linear_split(const char* fn, int cfg, LinArgs& a, cudaStream_t stream
     return launch_cfg<true>(fn, cfg, a, stream);
 }
 
-int take_linear_split_error(void* stream, uint32_t* code) { return take_error(stream, code); }
+int take_linear_split_error(void* stream, uint32_t* code) { return take_tp_error(stream, code); }
 
 }  // namespace rtp

@@ -111,6 +111,8 @@ int take_boxing_error(void* stream, uint32_t* code);
 // Launches the resharding kernel's bounded-wait self-test (a wait that never
 // completes, given up after limit_ns); out[0] = 1 when the block stopped on it.
 int bulk_wait_selftest(unsigned long long limit_ns, uint32_t* out, void* stream);
+// SMs of the current device; RTP_ECUDA without one (linear_few.cu).
+int device_sms(int* n);
 // The driver's cuTensorMapEncodeTiled (a PFN_cuTensorMapEncodeTiled_v12000), or NULL.
 void* tensor_map_encoder();
 
