@@ -352,11 +352,16 @@ def _exact_loss(case, s):
     return {"total": w.dot(loss), "loss": loss, "dX": dX, "dW": dW}
 
 
+def _pow64(e):
+    """2^e of an integer tensor in 64 bits, exactly."""
+    return ((e.to(I64) + 1023) << 52).view(torch.float64)
+
+
 def _held64(x, top, u, sign):
     """Values that blocks of 8-bit floats hold of x (rows), u their random numbers; `top`: exponent of a block's largest."""
     mag = x.abs()
     least = top[:, None] - (13 if sign else 29)  # exponent of the smallest normal value
-    step = torch.ldexp(torch.ones_like(mag), torch.maximum(torch.frexp(mag)[1] - 1, least) - 3)
+    step = _pow64(torch.maximum(torch.frexp(mag)[1] - 1, least) - 3)
     held = torch.floor(mag / step + u) * step
     if not sign:  # what is not zero stays so
         held = torch.where((mag > 0) & (held == 0), step, held)
@@ -376,7 +381,7 @@ def _exact_adam(case, s):
         got["master"] = w
     r = _noise(s, t) if case["states"] == 8 or case["param"] == "bf16" else None
     if case["param"] == "bf16":
-        ulp = torch.ldexp(torch.ones_like(w), torch.frexp(w)[1].clamp(min=-125) - 8)
+        ulp = _pow64(torch.frexp(w)[1].clamp(min=-125) - 8)
         up = torch.floor(w.abs() / ulp + (_pcg(r) % 65536).double() / 65536)
         got["p"] = up * ulp * torch.sign(w)
     for k, x, sign in (("m", m, True), ("v", v, False)):
