@@ -621,6 +621,124 @@ int rtp_clip_grad_norm(int n, const int32_t* dtypes, const int64_t* numels, cons
 int64_t rtp_grad_workspace_bytes(int n);
 
 /*
+ * Softmax cross entropy of an output layer whose vocabulary is split over P virtual
+ * ranks (the column-parallel layer of the ColossalAI "1D tensor parallelism" page,
+ * section 2; the pages stop before the loss), without the logits:
+ *   l = X [W_0 .. W_{P-1}], columns j < vocab   lse_r = log sum_j exp l_rj
+ *   loss_r = lse_r - l_{r,t_r}
+ *   X         bf16 [M, K];  W_shards: P bf16 [K, V/P]
+ *   vocab     columns from here on (counted over the ranks) are padding that takes no
+ *             part; in [1, V]
+ *   targets   [M] int64 (targets64 = 1) or int32 (0) on the device, counted over the ranks
+ *   ignore_index  rows with this target have a loss of 0. A target outside [0, vocab) that
+ *             is not ignore_index gives a NaN loss (the host does not see targets)
+ *   workspace rtp_tp_cross_entropy_workspace() bytes of device memory, 256-byte aligned;
+ *             needs no preparation; not shared by calls that may overlap
+ *   loss      float32 [M];  lse: float32 [M] (of every row), or NULL
+ * float32 accumulation and statistics; exponentials are within 2^-21 of themselves. Up to
+ * 128 rows run in the few-row kernel of rtp_tp_linear, more in its pair kernel.
+ * Requirements (RTP_ESHAPE): V % P == 0; K and V/P multiples of 8. Alignment (X, weights
+ * 16 bytes), errors, launches and M == 0 as in rtp_tp_linear; results do not change from
+ * run to run.
+ */
+int rtp_tp_cross_entropy(int P, int64_t M, int64_t K, int64_t V, int64_t vocab, const void* X, const void* const* W_shards,
+                         int targets64, const void* targets, int64_t ignore_index, void* workspace, int64_t workspace_bytes,
+                         float* loss, float* lse, rtp_stream stream);
+
+/*
+ * The loss with the gradients of scale * total, total = sum_r w_r loss_r / D:
+ *   d_rj = g_r (exp(l_rj - lse_r) - [j = t_r])   g_r = scale w_r / D
+ *   dX = sum_i d_i W_i^T   dW_i = X^T d_i
+ *   weights   w, float32 [M], or NULL (1). Ignored rows count for nothing, and rows of
+ *             weight 0 have no part in total and gradients
+ *   mean      1: D = sum of w over rows that are not ignored (0: total and gradients are
+ *             0); 0: D = 1
+ *   total     float32, device pointer (total itself is not scaled);  loss: float32 [M], not
+ *             weighted
+ *   dX        [M, K] by dx_dtype, or NULL;  dW: P [K, V/P] by dw_dtype, or NULL
+ *   accumulate 1: the products are added to the float32 dW that is there (several
+ *             micro-batches); subnormal values count as zero in such a sum
+ *   piece_rows rows that are taken at once (rounded up to 256): the workspace holds 2 V
+ *             bytes for each; 0: as many as keep that within the float32 sums of dW that
+ *             several pieces need, 2 K or 2048
+ * d is bf16: exp(l - largest of its tile) rounded once, d once more; both products read
+ * it. A row whose target is outside the vocabulary has NaN gradients. d of a row without
+ * a part is 0 whatever X holds there; dW still multiplies it with that X (0 * NaN).
+ * The rest as in rtp_tp_cross_entropy. M == 0 zeroes total and, unless accumulate, dW.
+ */
+int rtp_tp_cross_entropy_train(int P, int64_t M, int64_t K, int64_t V, int64_t vocab, const void* X,
+                               const void* const* W_shards, int targets64, const void* targets, int64_t ignore_index,
+                               const float* weights, int mean, float scale, int64_t piece_rows, void* workspace,
+                               int64_t workspace_bytes, float* total, float* loss, rtp_dtype dx_dtype, void* dX,
+                               rtp_dtype dw_dtype, void* const* dW, int accumulate, rtp_stream stream);
+
+/* Bytes of workspace of the two calls (train = 0 or 1; the forward call ignores piece_rows
+ * and dw_dtype; without dW, dw_dtype = RTP_F32 is enough). Host only. */
+int rtp_tp_cross_entropy_workspace(int P, int64_t M, int64_t K, int64_t V, int64_t piece_rows, int train, rtp_dtype dw_dtype,
+                                   int64_t* bytes);
+
+/*
+ * AdamW step over many tensors (the rank pieces whose gradients the backward calls
+ * write), no page counterpart:
+ *   g' = c g, c = min(1, max_norm / (norm + 1e-6))
+ *   m = b1 m + (1 - b1) g'   v = b2 v + (1 - b2) g'^2
+ *   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+ * One tensor:
+ *   param     float32 or bf16 by param_dtype
+ *   master    NULL, or the float32 copy of a bf16 param: it is updated, and param receives
+ *             it rounded. Without one a bf16 param is rounded at random, so that its mean
+ *             is right (to nearest, steps under half a spacing would be lost)
+ *   grad      float32 or bf16 by grad_dtype
+ *   exp_avg, exp_avg_sq  m and v: float32, or 8-bit codes with `scales`, two bytes (m's,
+ *             v's) for each RTP_ADAMW_BLOCK elements, 2-byte aligned; all bytes zero: m = v = 0
+ * Buffers are aligned to their elements; float32 ones that are 16-byte aligned, bf16 ones
+ * 8-byte and codes 4-byte go in vectors. Weights and their copies share no bytes with one
+ * another (RTP_EINVAL); other overlaps are not detected.
+ */
+typedef struct {
+    int64_t numel;
+    void* param;
+    const void* grad;
+    float* master;
+    void* exp_avg;
+    void* exp_avg_sq;
+    uint8_t* scales;
+    int32_t param_dtype, grad_dtype;
+    float weight_decay;
+    int32_t reserved;
+} rtp_adamw_tensor;
+
+enum { RTP_ADAMW_BLOCK = 128, RTP_ADAMW_CLOCK_BYTES = 128 };
+
+/*
+ *   bits      32, or 8: blocks of RTP_ADAMW_BLOCK elements share a power of two. m has 4
+ *             significant bits down to 2^-14 of its block's largest and is flat below; v 4
+ *             down to 2^-30 of it and never becomes zero. Both are rounded at random, which
+ *             keeps their means (to nearest, v would stand still). The block's exponent is
+ *             held to 2^-100 at least; a block with an infinity or a NaN becomes NaN
+ *   lr        the learning rate; lr_at: NULL, or a device pointer that it is read from
+ *   norm      NULL (no clipping), or the device pointer of a norm (rtp_grad_norm)
+ *   seed      of the random bits, a hash of seed, the tensor's place among the n, the step
+ *             and the element: a step is reproducible bit for bit
+ *   clock     RTP_ADAMW_CLOCK_BYTES of device memory, 16-byte aligned, set by
+ *             rtp_adamw_clock; its first 8 bytes are the steps done (int64). Every call
+ *             counts on by one, so that a captured step does so with each replay. Not shared
+ *             by calls that may overlap
+ * The quotient is within 2^-20 of itself. tensors[] is read before the call returns. lr,
+ * eps, max_norm and weight decays must be numbers >= 0 (RTP_EINVAL).
+ */
+int rtp_adamw_step(int n, const rtp_adamw_tensor* tensors, int bits, float lr, const float* lr_at, float eps, const float* norm,
+                   float max_norm, uint32_t seed, void* clock, rtp_stream stream);
+
+/* Sets a clock to `step` steps done, with the betas of the steps to come (each in [0, 1)). */
+int rtp_adamw_clock(void* clock, int64_t step, double beta1, double beta2, rtp_stream stream);
+
+/* The values of `blocks` blocks of 8-bit moments (buffers of whole blocks, 16-byte aligned)
+ * as float32 or bf16, which hold them exactly (bf16: 4 significant bits). */
+int rtp_adamw_values(int64_t blocks, const uint8_t* exp_avg, const uint8_t* exp_avg_sq, const uint8_t* scales, rtp_dtype dtype,
+                     void* m, void* v, rtp_stream stream);
+
+/*
  * Reads and clears the device words in which the tensor-core kernels of
  * rtp_tp_mlp, rtp_tp_linear and rtp_tp_glu record a wait that gave up (no progress for about 4 seconds; the
  * kernel then stops, frees its tensor memory and returns instead of hanging),

@@ -9,7 +9,8 @@ Names mirror the C ABI in ``include/rtp.h``:
   spec_from_dims_mapping, spec_from_onnx, spec_nd_sbp (the ND-SBP form filled
   directly), shard_shape, shard_box, shard, reshard, reshard_cost,
   infer_spmd, infer_reshape, tp_mlp, last_error; tp_linear, tp_glu and their
-  backward calls, grad_norm, clip_grad_norm (GradGroup keeps their tables).
+  backward calls, grad_norm, clip_grad_norm (GradGroup keeps their tables);
+  tp_cross_entropy, tp_cross_entropy_train; AdamWGroup (rtp_adamw_step).
 """
 from __future__ import annotations
 
@@ -69,6 +70,24 @@ class Spec(ctypes.Structure):
         return "Spec(mesh=%s, sbp=%s, ranks=%s)" % (mesh, ents, ranks)
 
 
+class AdamWTensor(ctypes.Structure):
+    """rtp_adamw_tensor: one weight, its gradient and its state."""
+
+    _fields_ = [
+        ("numel", ctypes.c_int64),
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("master", ctypes.c_void_p),
+        ("exp_avg", ctypes.c_void_p),
+        ("exp_avg_sq", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("param_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32),
+        ("weight_decay", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -108,6 +127,13 @@ def _load():
                                 c_int, vp, vp, vp, vp],
         "rtp_grad_norm": [c_int, i32p, i64p, vp, vp, vp, vp, vp],
         "rtp_clip_grad_norm": [c_int, i32p, i64p, vp, vp, ctypes.c_float, vp, vp, vp, vp],
+        "rtp_tp_cross_entropy": [c_int, i64, i64, i64, i64, vp, vp, c_int, vp, i64, vp, i64, vp, vp, vp],
+        "rtp_tp_cross_entropy_train": [c_int, i64, i64, i64, i64, vp, vp, c_int, vp, i64, vp, c_int, ctypes.c_float, i64,
+                                       vp, i64, vp, vp, c_int, vp, c_int, vp, c_int, vp],
+        "rtp_tp_cross_entropy_workspace": [c_int, i64, i64, i64, i64, c_int, c_int, i64p],
+        "rtp_adamw_step": [c_int, vp, c_int, ctypes.c_float, vp, ctypes.c_float, vp, ctypes.c_float, ctypes.c_uint32, vp, vp],
+        "rtp_adamw_clock": [vp, i64, ctypes.c_double, ctypes.c_double, vp],
+        "rtp_adamw_values": [i64, vp, vp, vp, c_int, vp, vp, vp],
         "rtp_device_error": [vp, u32p],
         "rtp_wait_selftest": [c_int, ctypes.c_ulonglong, vp, vp],
         "rtp_test_hook": [c_int, ctypes.c_int64],
@@ -909,6 +935,109 @@ def tp_glu_backward(X, Ag_shards, Au_shards, B_shards, Hg, Hu, Y, dZ, act: str =
     return (dX, *dw)
 
 
+# ---- cross entropy over a vocabulary split over the ranks ----------------------------------
+
+def _loss_arguments(fn: str, X, W, targets, vocab):
+    """(P, M, K, V, vocab, device, table of W, 1 for int64 targets) of the loss calls' arguments."""
+    torch = _torch()
+    P = len(W)
+    if not P:
+        raise RtpError(-1, "%s: no weight shards" % fn)
+    M, K = _matrix(fn, "X", X)
+    _, Vp = _matrix(fn, "W_shards[0]", W[0])
+    device = _device_of(X)
+    _table_of(fn, "X", [X], 1, (M, K), torch.bfloat16, device)
+    wp = _table_of(fn, "W_shards", W, P, (K, Vp), torch.bfloat16, device)
+    if not isinstance(targets, torch.Tensor) or targets.dtype not in (torch.int64, torch.int32):
+        raise RtpError(-1, "%s: targets must be an int64 or int32 tensor" % fn)
+    _check_vector(fn, "targets", targets, M, device)
+    return P, M, K, Vp * P, Vp * P if vocab is None else int(vocab), device, wp, int(targets.dtype == torch.int64)
+
+
+def _check_vector(fn: str, name: str, t, n: int, device: int, dtype=None):
+    """A contiguous vector of n elements on the device (and of a type), or RtpError."""
+    if dtype is not None and (not isinstance(t, _torch().Tensor) or t.dtype is not dtype):
+        raise RtpError(-1, "%s: %s must be a %s tensor" % (fn, name, str(dtype).replace("torch.", "")))
+    if tuple(t.shape) != (n,):
+        raise RtpError(-2, "%s: %s is %s, expected %s" % (fn, name, tuple(t.shape), (n,)))
+    if n and (not t.is_cuda or t.device.index != device or not t.is_contiguous()):
+        raise RtpError(-1, "%s: %s must be contiguous and on cuda:%d" % (fn, name, device))
+
+
+def _loss_workspace(P, M, K, V, piece_rows, train, dw_dtype, device, stream):
+    """(scratch for one call, owned by the stream it runs on; its bytes)"""
+    n = ctypes.c_int64()
+    _check(_load().rtp_tp_cross_entropy_workspace(P, M, K, V, piece_rows, train, dw_dtype, ctypes.byref(n)))
+    ws, = _new(1, ((n.value + 3) // 4,), _torch().float32, device, stream)
+    return ws, n.value
+
+
+def tp_cross_entropy(X, W_shards, targets, vocab: Optional[int] = None, ignore_index: int = -100, loss=None, lse=None,
+                     stream=None):
+    """Softmax cross entropy of the output layer X [W_0 .. W_{P-1}], whose vocabulary is split over P = len(W_shards)
+    virtual ranks (bf16 X [M, K], W_i [K, V/P]), without its logits. targets: [M] int64 or int32, counted over the ranks;
+    columns from `vocab` on (default: none) are padding. Returns (loss, lse), float32 [M]: lse - logit of the target (0
+    where the target is ignore_index, NaN where it is outside the vocabulary), and the logarithm of the sum of the
+    exponentials, so that -loss is the log probability of the target."""
+    fn = "tp_cross_entropy"
+    W = _listed(W_shards)
+    P, M, K, V, vocab, device, wp, wide = _loss_arguments(fn, X, W, targets, vocab)
+    f32 = _torch().float32
+    if loss is None:
+        loss, = _new(1, (M,), f32, device, stream)
+    if lse is None:
+        lse, = _new(1, (M,), f32, device, stream)
+    _check_vector(fn, "loss", loss, M, device, f32)
+    _check_vector(fn, "lse", lse, M, device, f32)
+    ws, n = _loss_workspace(P, M, K, V, 0, 0, F32, device, stream)
+    _check(_load().rtp_tp_cross_entropy(P, M, K, V, vocab, X.data_ptr(), wp, wide, targets.data_ptr(), int(ignore_index),
+                                        ws.data_ptr(), n, loss.data_ptr(), lse.data_ptr(), _stream_ptr(stream)))
+    return loss, lse
+
+
+def tp_cross_entropy_train(X, W_shards, targets, weights=None, vocab: Optional[int] = None, ignore_index: int = -100,
+                           reduction: str = "mean", scale: float = 1.0, dX=None, dW=None, loss=None, total=None,
+                           dx_dtype=None, dw_dtype=None, accumulate: bool = False, piece_rows: int = 0, stream=None):
+    """tp_cross_entropy with the gradients of scale * total, total = sum of weights * loss over the rows ("sum"), or that
+    divided by the sum of the weights of the rows that are not ignored ("mean"; 0 where that is 0). weights: float32 [M],
+    or None (1). Returns (total, loss, dX, dW): float32 scalar (not scaled) and [M], dX [M, K] and the list dW like
+    W_shards, bf16 or float32 (dx_dtype, dw_dtype, or by the buffers given). accumulate: dW (float32, given) += the
+    gradient. Rows are taken in pieces of piece_rows (0: as many as the scratch for the exponentials, 2 V bytes a row, is
+    worth); several pieces need 4 K V bytes more to sum a bf16 dW in float32."""
+    fn = "tp_cross_entropy_train"
+    torch = _torch()
+    W = _listed(W_shards)
+    if reduction != "mean" and reduction != "sum":
+        raise RtpError(-1, "%s: reduction %r is not 'mean' or 'sum'" % (fn, reduction))
+    P, M, K, V, vocab, device, wp, wide = _loss_arguments(fn, X, W, targets, vocab)
+    f32, bf16, shape = torch.float32, torch.bfloat16, (K, V // P)
+    if accumulate and dW is None:
+        raise RtpError(-1, "%s: accumulate needs the dW to add to" % fn)
+    if weights is not None:
+        _check_vector(fn, "weights", weights, M, device, f32)
+    dx_dtype = _out_dtype(dx_dtype, dX, bf16)
+    dw_dtype = _out_dtype(dw_dtype, None if dW is None else _listed(dW)[0], bf16)
+    if loss is None:
+        loss, = _new(1, (M,), f32, device, stream)
+    _check_vector(fn, "loss", loss, M, device, f32)
+    if total is None:
+        total, = _new(1, (), f32, device, stream)
+    _table_of(fn, "total", [total], 1, (), f32, device)
+    if dX is None:
+        dX, = _new(1, (M, K), dx_dtype, device, stream)
+    _table_of(fn, "dX", [dX], 1, (M, K), dx_dtype, device)
+    dW = _new(P, shape, dw_dtype, device, stream) if dW is None else _listed(dW)
+    dwp = _table_of(fn, "dW", dW, P, shape, dw_dtype, device)
+    code = _dtype_code(dW[0])
+    ws, n = _loss_workspace(P, M, K, V, int(piece_rows), 1, code, device, stream)
+    _check(_load().rtp_tp_cross_entropy_train(
+        P, M, K, V, vocab, X.data_ptr(), wp, wide, targets.data_ptr(), int(ignore_index),
+        None if weights is None else weights.data_ptr(), int(reduction == "mean"), float(scale), int(piece_rows),
+        ws.data_ptr(), n, total.data_ptr(), loss.data_ptr(), _dtype_code(dX), dX.data_ptr(), code, dwp, int(bool(accumulate)),
+        _stream_ptr(stream)))
+    return total, loss, dX, dW
+
+
 # ---- global gradient norm and clipping -----------------------------------------------------
 
 def counted_pieces(spec: Spec) -> List[bool]:
@@ -925,6 +1054,21 @@ def counted_pieces(spec: Spec) -> List[bool]:
             if c and spec.sbp_kind[d] == BROADCAST:
                 flags[spec.rank_ids[p]] = False
     return flags
+
+
+def _join_stream(device, handle, ready, tensors) -> bool:
+    """Lets a stream wait for what made a group's own tensors ready, and keep them until its work is done; False where it
+    is capturing and can do neither."""
+    torch = _torch()
+    s = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(s):
+        if torch.cuda.is_current_stream_capturing():
+            return False
+        if ready is not None:
+            s.wait_event(ready)
+    for t in tensors:
+        t.record_stream(s)
+    return True
 
 
 class GradGroup:
@@ -1001,15 +1145,8 @@ class GradGroup:
         """The first call on another stream than the workspace's own: that stream waits until the workspace is zero, and
         keeps it, should the group be dropped, until its work is done. A capturing stream can do neither: a capture
         begins with all earlier work complete, and its graph is replayed only as long as the group is kept."""
-        torch = _torch()
-        s = torch.cuda.ExternalStream(handle, self.device) if handle else torch.cuda.default_stream(self.device)
-        with torch.cuda.stream(s):
-            if torch.cuda.is_current_stream_capturing():
-                return
-            if self._zeroed is not None:
-                s.wait_event(self._zeroed)
-        self._ws.record_stream(s)
-        self._joined.add(handle)
+        if _join_stream(self.device, handle, self._zeroed, [self._ws]):
+            self._joined.add(handle)
 
     def _begin(self, stream):
         """(the norm's buffer, the handle of the stream to run on)"""
@@ -1066,6 +1203,197 @@ def grad_norm(grads, counted=None, stream=None):
 def clip_grad_norm(grads, max_norm: float, counted=None, out=None, stream=None):
     """Clips a list of gradients by their global norm (GradGroup.clip without keeping a group)."""
     return GradGroup._for_one_call(grads, counted, stream).clip(max_norm, out, stream)
+
+
+# ---- AdamW ---------------------------------------------------------------------------------
+
+ADAMW_BLOCK = 128  # elements of a block of 8-bit moments
+_ADAMW_CLOCK_BYTES = 128
+
+
+class AdamWGroup:
+    """AdamW over a program's weights (rank pieces, float32 and bf16 mixed), all of them in one pass.
+
+    weight_decay: one for all, or one per tensor. masters: float32 copies that bf16 weights are updated through, one per
+    tensor (None for a tensor without), or True for copies that the group makes; a bf16 weight without one is rounded at
+    random, so that small steps are not lost. states: bits of the moments, 32 or 8 (blocks of 128 elements share a power of
+    two, values are rounded at random; see rtp_adamw_step in rtp.h). seed: of the random bits.
+
+    The group keeps the tensors and, in one flat buffer each, the moments (exp_avg, exp_avg_sq: float32, or codes with
+    `scales`), tensor i in [offsets[i], offsets[i] + numel), a multiple of 128 from the start. The steps done are counted
+    on the GPU (`steps`, an int64 tensor), so a captured step counts on with each replay. Steps of one group that may
+    overlap on the GPU must be ordered by the caller. stream: where the state is allocated and zeroed (default: the current
+    stream)."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=1e-2, masters=None,
+                 states: int = 32, seed: int = 0, stream=None):
+        torch = _torch()
+        fn = "AdamWGroup"
+        self.params = list(params)
+        n = len(self.params)
+        if states not in (8, 32):
+            raise RtpError(-1, "%s: states of %r bits (8 or 32)" % (fn, states))
+        self.device = torch.device("cuda", _device_of(self.params[0]) if n else torch.cuda.current_device())
+        self._index, self.states, self.lr, self.eps = self.device.index, states, lr, float(eps)
+        self.betas = (float(betas[0]), float(betas[1]))
+        if not (0.0 <= self.betas[0] < 1.0 and 0.0 <= self.betas[1] < 1.0):
+            raise RtpError(-1, "%s: betas %r outside [0, 1)" % (fn, betas))
+        self.seed = int(seed) & 0xFFFFFFFF
+        decay = [weight_decay] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        if len(decay) != n:
+            raise RtpError(-1, "%s: %d weight decays for %d tensors" % (fn, len(decay), n))
+        self._decay = [float(d) for d in decay]
+        for i, p in enumerate(self.params):
+            self._check(fn, "params", i, p)
+        with _allocating_on(stream):
+            self.masters = self._masters(fn, masters)
+            self.offsets = [0]
+            for p in self.params:
+                self.offsets.append(self.offsets[-1] + (p.numel() + ADAMW_BLOCK - 1) // ADAMW_BLOCK * ADAMW_BLOCK)
+            total = self.offsets.pop()
+            flat = dict(dtype=torch.float32 if states == 32 else torch.uint8, device=self.device)
+            self.exp_avg, self.exp_avg_sq = torch.zeros(total, **flat), torch.zeros(total, **flat)
+            self.scales = torch.zeros((total // ADAMW_BLOCK, 2), **flat) if states == 8 else None
+            self._clock = torch.zeros(_ADAMW_CLOCK_BYTES // 8, dtype=torch.int64, device=self.device)
+            self.steps = self._clock[0]
+            self._set_clock(0, None)
+            self._own = [t for t in (self.exp_avg, self.exp_avg_sq, self.scales, self._clock) if t is not None]
+            # copies that the group made belong to it, as its state does
+            self._own += [m for m in self.masters if m is not None and masters is True]
+            self._joined = {torch._C._cuda_getCurrentRawStream(self._index) or None}
+            self._ready = None
+            if not torch.cuda.is_current_stream_capturing():
+                self._ready = torch.cuda.current_stream(self.device).record_event()
+        self._tabulate()
+
+    def _check(self, fn, name, i, t, like=None):
+        """A contiguous float32 or bf16 tensor of the group's device (a gradient: of its weight's shape)."""
+        if not isinstance(t, _torch().Tensor):
+            raise RtpError(-1, "%s: %s[%d] is no tensor" % (fn, name, i))
+        _dtype_code(t)
+        if like is not None and t.shape != like.shape:
+            raise RtpError(-2, "%s: %s[%d] is %s, expected %s" % (fn, name, i, tuple(t.shape), tuple(like.shape)))
+        if t.numel() and (t.device != self.device or not t.is_contiguous()):
+            raise RtpError(-1, "%s: %s[%d] must be contiguous and on %s" % (fn, name, i, self.device))
+
+    def _masters(self, fn, masters):
+        torch = _torch()
+        n = len(self.params)
+        if masters is None or masters is False:
+            return [None] * n
+        if masters is True:
+            return [p.detach().float() if p.dtype is torch.bfloat16 else None for p in self.params]
+        masters = list(masters)
+        if len(masters) != n:
+            raise RtpError(-1, "%s: %d masters for %d tensors" % (fn, len(masters), n))
+        for i, (m, p) in enumerate(zip(masters, self.params)):
+            if m is None:
+                continue
+            self._check(fn, "masters", i, m, p)
+            if m.dtype is not torch.float32 or p.dtype is not torch.bfloat16:
+                raise RtpError(-1, "%s: masters[%d] must be the float32 copy of a bf16 weight" % (fn, i))
+        return masters
+
+    def _set_clock(self, step: int, handle):
+        if handle is None:
+            handle = _torch()._C._cuda_getCurrentRawStream(self._index) or None
+        _check(_load().rtp_adamw_clock(self._clock.data_ptr(), step, *self.betas, handle))
+
+    def _tabulate(self):
+        """The table of the tensors as they are; the gradients are entered at each step."""
+        n = len(self.params)
+        self._table = (AdamWTensor * max(1, n))()
+        size = 4 if self.states == 32 else 1
+        for i, (t, p, m) in enumerate(zip(self._table, self.params, self.masters)):
+            at = self.offsets[i]
+            t.numel, t.param, t.param_dtype, t.weight_decay = p.numel(), p.data_ptr() or None, _dtype_code(p), self._decay[i]
+            t.master = None if m is None else m.data_ptr() or None
+            t.exp_avg, t.exp_avg_sq = self.exp_avg.data_ptr() + at * size, self.exp_avg_sq.data_ptr() + at * size
+            if self.states == 8:
+                t.scales = self.scales.data_ptr() + at // ADAMW_BLOCK * 2
+        self._numels = [p.numel() for p in self.params]
+
+    def _begin(self, stream):
+        torch = _torch()
+        if torch._C._cuda_getDevice() != self._index:
+            raise RtpError(-1, "AdamWGroup: tensors are on %s but the current CUDA device is %d" % (
+                self.device, torch.cuda.current_device()))
+        handle = _stream_ptr(stream)
+        if handle not in self._joined and _join_stream(self.device, handle, self._ready, self._own):
+            self._joined.add(handle)
+        return handle
+
+    def _scalar(self, name, t):
+        """A float32 scalar on the group's GPU, as its address."""
+        if t.dtype is not _torch().float32 or t.numel() != 1 or t.device != self.device:
+            raise RtpError(-1, "AdamWGroup: %s must be one float32 on %s" % (name, self.device))
+        return t.data_ptr()
+
+    def step(self, grads, lr=None, norm=None, max_norm: float = 1.0, stream=None):
+        """One step with the gradients of the weights (float32 or bf16, each like its weight). lr: instead of the group's;
+        a float, or a float32 scalar on the GPU (which a replayed step reads anew). norm: the global norm on the GPU
+        (GradGroup.norm): gradients count times min(1, max_norm / (norm + 1e-6)), and stay as they are."""
+        fn = "AdamWGroup.step"
+        handle = self._begin(stream)
+        grads = grads if type(grads) is list else list(grads)
+        if len(grads) != len(self.params):
+            raise RtpError(-1, "%s: %d gradients for %d tensors" % (fn, len(grads), len(self.params)))
+        for i, (t, p, m, g) in enumerate(zip(self._table, self.params, self.masters, grads)):
+            self._check(fn, "params", i, p)
+            if p.numel() != self._numels[i]:
+                raise RtpError(-2, "%s: params[%d] has %d elements, the group was built over %d" % (
+                    fn, i, p.numel(), self._numels[i]))
+            self._check(fn, "grads", i, g, p)
+            t.param, t.param_dtype = p.data_ptr() or None, _dtype_code(p)
+            if m is not None:
+                self._check(fn, "masters", i, m, p)
+                t.master = m.data_ptr() or None
+            t.grad, t.grad_dtype = g.data_ptr() or None, _dtype_code(g)
+        lr = self.lr if lr is None else lr
+        at = None
+        if isinstance(lr, _torch().Tensor):
+            at, lr = self._scalar("lr", lr), 0.0
+        _check(_load().rtp_adamw_step(len(grads), self._table, self.states, float(lr), at, self.eps,
+                                      None if norm is None else self._scalar("norm", norm), float(max_norm), self.seed,
+                                      self._clock.data_ptr(), handle))
+
+    def moments(self, dtype=None, stream=None):
+        """(m, v), flat as exp_avg: with 32-bit states these very buffers, with 8-bit ones the values that they hold, in
+        new tensors (bf16, which holds them exactly, or float32)."""
+        if self.states == 32:
+            return self.exp_avg, self.exp_avg_sq
+        handle = self._begin(stream)
+        dtype = _out_dtype(dtype, None, _torch().bfloat16)
+        m, v = _new(2, tuple(self.exp_avg.shape), dtype, self._index, stream)
+        _check(_load().rtp_adamw_values(self.exp_avg.numel() // ADAMW_BLOCK, self.exp_avg.data_ptr(),
+                                        self.exp_avg_sq.data_ptr(), self.scales.data_ptr(), _dtype_code(m), m.data_ptr(),
+                                        v.data_ptr(), handle))
+        return m, v
+
+    def state_dict(self) -> dict:
+        """The state, for load_state_dict: "step" (an int: waits for the GPU), "exp_avg", "exp_avg_sq" and, of 8-bit states,
+        "scales": the group's own buffers, not copies."""
+        got = {"step": int(self.steps), "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq}
+        return got if self.scales is None else {**got, "scales": self.scales}
+
+    def load_state_dict(self, state: dict) -> None:
+        """Copies a state_dict of a group over tensors of the same sizes into this one's buffers, on the current stream."""
+        fn = "AdamWGroup.load_state_dict"
+        names = ["exp_avg", "exp_avg_sq"] + (["scales"] if self.states == 8 else [])
+        if set(state) != set(names + ["step"]):
+            raise RtpError(-1, "%s: keys %s, expected %s" % (fn, sorted(state), sorted(names + ["step"])))
+        for name in names:
+            own, t = getattr(self, name), state[name]
+            if t.shape != own.shape or t.dtype is not own.dtype:
+                raise RtpError(-2, "%s: %s is %s %s, expected %s %s" % (fn, name, t.dtype, tuple(t.shape), own.dtype,
+                                                                      tuple(own.shape)))
+        step = int(state["step"])
+        if step < 0:
+            raise RtpError(-1, "%s: step %d" % (fn, step))
+        handle = self._begin(None)
+        for name in names:
+            getattr(self, name).copy_(state[name])
+        self._set_clock(step, handle)
 
 
 def device_error(stream=None) -> int:

@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "librtp.so")
 TABLE = os.path.join(HERE, "_table.so")  # Python extension: pointer tables of checked tensors
 
 HOST_SOURCES = ["spec.cpp", "plan.cpp", "infer.cpp"]
-CUDA_SOURCES = ["boxing.cu", "tp_mlp.cu", "tp_mlp_static.cu", "linear.cu", "linear_gemm.cu", "linear_gemm_split.cu", "linear_few.cu", "grad_norm.cu"]
+CUDA_SOURCES = ["boxing.cu", "tp_mlp.cu", "tp_mlp_static.cu", "linear.cu", "linear_gemm.cu", "linear_gemm_split.cu", "linear_few.cu", "grad_norm.cu", "cross_entropy.cu",
+                "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,515 @@
+// Softmax cross entropy of an output layer whose vocabulary is split over P virtual
+// ranks, without the logits: W_i [K, V/P] are the column-parallel shards.
+//
+//   l = X [W_0 .. W_{P-1}]        lse_r = log sum_j exp l_rj       loss_r = lse_r - l_{r,t_r}
+//   d_rj = g_r (exp(l_rj - lse_r) - [j = t_r])     dX = sum_i d_i W_i^T     dW_i = X^T d_i
+//
+// Forward: the product's epilogue leaves, for each row and tile, the largest logit and
+// the sum of the exponentials relative to it (softmax.cuh); loss_rows_kernel joins them.
+// Training, 6 M K V operations: the same product also writes the exponentials e in bf16,
+// relative to their tile's largest logit (so each holds its value to half a bf16 step,
+// whatever the logits' size, which rounded logits would not); loss_rows_kernel, with the
+// row's sum at hand, turns them in place into d, rounded once more; two products read d.
+// Recomputing the logits instead would cost a third more operations and save that one
+// pass over 2 M V bytes.
+//
+// The exponentials of all rows take 2 M V bytes. Rows are taken in pieces, so that they
+// take no more than the float32 sums of dW that pieces need (4 K V): 2 K rows at most.
+// With several pieces dW is summed in float32, by adds in the output's TMA stores.
+#include <algorithm>
+#include <cstring>
+
+#include "linear.h"
+#include "softmax.cuh"
+#include "tcgen05.cuh"
+
+namespace rtp {
+
+namespace {
+
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+
+// Sums and counters of one call, at the start of its workspace.
+struct Shared {
+    double weight;      // of the counted rows
+    float scale;        // of a row's gradient, before its own weight
+    unsigned finished;  // blocks of the last piece
+};
+constexpr int64_t SHARED_BYTES = 256;
+
+struct RowsArgs {
+    SoftmaxArgs softmax;  // of the piece's rows
+    int64_t ignore;
+    const float* weights;  // of the piece's rows, or NULL
+    float* loss;           // of the piece's rows
+    float* lse;            // or NULL
+    // training
+    __nv_bfloat16* e[LIN_MAX_RANKS];
+    Shared* shared;
+    float* total;              // or NULL: not the last piece
+    const float* all_loss;     // of every row, with their weights and targets
+    const float* all_weights;
+    const void* all_targets;
+    int64_t all_rows;
+    int32_t mean;
+    int32_t P, cols, part_cols, parts_of_rank;
+};
+
+template <class T, class F>
+__device__ __forceinline__ T block_reduce(T v, T* scratch, F&& f)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    __syncthreads();  // a previous result has been read
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = scratch[0];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) v = f(v, scratch[w]);
+    return v;
+}
+
+// d of 8 neighbouring columns from their exponentials; `at`: the target among them, or not.
+__device__ __forceinline__ uint4 gradients(const uint4& e, float factor, float g, int at)
+{
+    float d[8] = {bf16_lo(e.x), bf16_hi(e.x), bf16_lo(e.y), bf16_hi(e.y), bf16_lo(e.z), bf16_hi(e.z), bf16_lo(e.w), bf16_hi(e.w)};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j] = j == at ? fmaf(d[j], factor, -g) : d[j] * factor;
+    return make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
+}
+
+// Sum over every row of weight * loss, in a fixed order.
+__device__ __forceinline__ float total_loss(const RowsArgs& a, double* scratch)
+{
+    double s = 0.0;
+    for (int64_t r = threadIdx.x; r < a.all_rows; r += THREADS) {
+        const float w = a.all_weights ? __ldcg(a.all_weights + r) : 1.0f;
+        if (w != 0.0f) s += (double)w * (double)__ldcg(a.all_loss + r);  // ignored rows: 0
+    }
+    s = block_reduce(s, scratch, [](double x, double y) { return x + y; });
+    if (a.mean) s = a.shared->weight != 0.0 ? s / a.shared->weight : 0.0;
+    return (float)s;
+}
+
+// One row a block (blockIdx.x; gridDim.y blocks share its columns): joins the row's
+// statistics into lse and loss and, TRAIN, turns its exponentials into d.
+template <bool TRAIN>
+__global__ void __launch_bounds__(THREADS) loss_rows_kernel(const __grid_constant__ RowsArgs a)
+{
+    __shared__ double scratch[WARPS];
+    float* scratch_f = reinterpret_cast<float*>(scratch);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t row = blockIdx.x;
+    const float2* stats = a.softmax.stats + row * a.softmax.parts;
+    const int64_t t = target_at(a.softmax.targets, a.softmax.targets64, row);
+    const bool ignored = t == a.ignore, known = t >= 0 && t < a.softmax.vocab;
+    float top = minus_infinity(), sum = 0.0f;
+    for (int i = threadIdx.x; i < a.softmax.parts; i += THREADS) {
+        const float2 s = __ldcg(stats + i);
+        const float now = fmaxf(top, s.x), r = finite_ref(now);
+        sum = sum * exp2_fast(top - r) + s.y * exp2_fast(s.x - r);
+        top = now;
+    }
+    const float mine = top;
+    top = block_reduce(top, scratch_f, [](float x, float y) { return fmaxf(x, y); });
+    const float ref = finite_ref(top);
+    sum = block_reduce(sum * exp2_fast(mine - ref), scratch_f, [](float x, float y) { return x + y; });
+    if (threadIdx.x == 0 && blockIdx.y == 0) {
+        const float lse = (ref + log2f(sum)) * LN2;
+        if (a.lse) a.lse[row] = lse;
+        float loss = ignored ? 0.0f : __int_as_float(0x7FC00000);
+        if (!ignored && known) loss = lse - __ldcg(a.softmax.target_logit + row);
+        a.loss[row] = loss;
+    }
+    if constexpr (TRAIN) {
+        const float w = a.weights ? __ldcg(a.weights + row) : 1.0f;
+        float g = ignored || w == 0.0f ? 0.0f : a.shared->scale * w;
+        if (!ignored && !known && g != 0.0f) g = __int_as_float(0x7FC00000);  // a target outside the vocabulary shows
+        const int vectors = a.cols / 8, stride = (int)gridDim.y * THREADS;
+        const float scaled = g / sum;
+        for (int i = 0; i < a.P; ++i) {
+            uint4* e = reinterpret_cast<uint4*>(a.e[i] + row * a.cols);
+            const float2* s = stats + i * a.parts_of_rank;
+            const int64_t first = t - (int64_t)i * a.cols;
+            const int at = known && first >= 0 && first < a.cols ? (int)first : -8;
+            if (g == 0.0f) {  // whatever the row holds
+                for (int v = (int)blockIdx.y * THREADS + threadIdx.x; v < vectors; v += stride) e[v] = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+            }
+#pragma unroll 4
+            for (int v = (int)blockIdx.y * THREADS + threadIdx.x; v < vectors; v += stride) {
+                const float factor = scaled * exp2_fast(__ldcg(s + 8 * v / a.part_cols).x - ref);
+                e[v] = gradients(__ldcs(e + v), factor, g, at - 8 * v);
+            }
+        }
+        if (!a.total) return;
+        __shared__ bool closing;
+        if (threadIdx.x == 0) {
+            __threadfence();
+            closing = atomicAdd(&a.shared->finished, 1u) == gridDim.x * gridDim.y - 1;
+        }
+        __syncthreads();
+        if (!closing) return;
+        __threadfence();
+        const float total = total_loss(a, scratch);
+        if (threadIdx.x == 0) *a.total = total;
+    }
+}
+
+// The weight of the counted rows, from which the gradients' scale follows. One block:
+// 8192 rows take 3 us.
+__global__ void __launch_bounds__(1024) loss_scale_kernel(const void* targets, int targets64, const float* weights, int64_t rows,
+                                                          int64_t ignore, int mean, float scale, Shared* sh, float* total)
+{
+    __shared__ double sums[32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    double s = 0.0;
+    if (mean)
+        for (int64_t r = threadIdx.x; r < rows; r += 1024)
+            if (target_at(targets, targets64, r) != ignore) s += weights ? (double)__ldcg(weights + r) : 1.0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x) return;
+    s = 0.0;
+    for (int w = 0; w < 32; ++w) s += sums[w];
+    sh->weight = s;
+    sh->scale = !mean ? scale : s != 0.0 ? (float)((double)scale / s) : 0.0f;
+    sh->finished = 0u;
+    if (rows == 0) *total = 0.0f;
+}
+
+// float32 sums to bf16 gradients.
+struct RoundArgs {
+    const float4* from[LIN_MAX_RANKS];
+    uint2* to[LIN_MAX_RANKS];
+    int64_t quads;
+};
+__global__ void __launch_bounds__(THREADS) round_kernel(const __grid_constant__ RoundArgs a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const float4* from = a.from[blockIdx.y];
+    uint2* to = a.to[blockIdx.y];
+    const int64_t stride = (int64_t)gridDim.x * THREADS;
+#pragma unroll 4
+    for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < a.quads; i += stride) {
+        const float4 v = __ldcs(from + i);
+        to[i] = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+    }
+}
+
+// ---- host side --------------------------------------------------------------------
+
+#define TRY(call)          \
+    do {                   \
+        int st_ = (call);  \
+        if (st_) return st_; \
+    } while (0)
+
+// A launch that may be set up while the stream's previous kernel still runs (every
+// kernel here waits for it before it touches memory).
+template <class... A, class... B>
+int launch(const char* fn, void (*kernel)(A...), dim3 grid, int threads, cudaStream_t stream, B... args)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? RTP_OK : fail(RTP_ECUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+}
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+struct Shape {
+    int P;
+    int64_t M, K, V, vocab, Vp;
+    int64_t piece;  // rows of a piece
+    int pieces;
+};
+
+// part_cols of the product that a piece of `rows` rows takes
+int part_cols(int64_t rows) { return rows <= LIN_FEW_ROWS ? LIN_FEW_COLS : LIN_TILE_COLS; }
+int64_t parts(const Shape& s, int64_t rows) { return s.P * ((s.Vp + part_cols(rows) - 1) / part_cols(rows)); }
+
+int check_shape(const char* fn, int P, int64_t M, int64_t K, int64_t V, int64_t vocab, int64_t piece_rows, bool train, Shape* s)
+{
+    if (P < 1 || P > LIN_MAX_RANKS) return fail(RTP_EUNSUPPORTED, "%s: P = %d outside [1, %d]", fn, P, LIN_MAX_RANKS);
+    const int64_t lim = (int64_t)1 << 31;
+    if (M < 0 || M >= lim || K < 1 || K >= lim || V < 1 || V >= lim)
+        return fail(RTP_ESHAPE, "%s: sizes M=%lld, K=%lld, V=%lld outside [0 or 1, 2^31)", fn, (long long)M, (long long)K, (long long)V);
+    if (V % P || K % 8 || (V / P) % 8)
+        return fail(RTP_ESHAPE, "%s: K=%lld and a rank's columns (V=%lld over P=%d) must be multiples of 8 (16-byte rows)", fn,
+                    (long long)K, (long long)V, P);
+    if (vocab < 1 || vocab > V) return fail(RTP_ESHAPE, "%s: vocab=%lld outside [1, V=%lld]", fn, (long long)vocab, (long long)V);
+    if (piece_rows < 0) return fail(RTP_EINVAL, "%s: piece_rows=%lld", fn, (long long)piece_rows);
+    s->P = P, s->M = M, s->K = K, s->V = V, s->vocab = vocab, s->Vp = V / P;
+    // As many rows as the head of this file allows, in pieces of about the same size;
+    // whole row tiles, so that only the last piece ends inside one.
+    const int64_t most = piece_rows ? up(piece_rows, LIN_TILE_ROWS) : up(std::max<int64_t>(2 * K, 2048), LIN_TILE_ROWS);
+    s->pieces = train && M > most ? (int)((M + most - 1) / most) : 1;
+    s->piece = s->pieces > 1 ? up((M + s->pieces - 1) / s->pieces, LIN_TILE_ROWS) : M;
+    if (s->pieces > 1) s->pieces = (int)((M + s->piece - 1) / s->piece);
+    return RTP_OK;
+}
+
+// Where things are in a workspace; sum: float32 sums of dW.
+struct Space {
+    int64_t logit, stats, e, sum, bytes;
+};
+Space space_of(const Shape& s, bool train, bool sum)
+{
+    // the last piece may be of few rows, with narrower parts than the others
+    const int64_t last = s.M - (s.pieces - 1) * s.piece;
+    const int64_t most = std::max(s.piece * parts(s, s.piece), last * parts(s, last));
+    Space w;
+    w.logit = SHARED_BYTES;
+    w.stats = w.logit + up(s.piece * 4, 256);
+    w.e = w.stats + up(most * 8, 256);
+    w.sum = w.e + (train ? up(s.piece * s.V * 2, 256) : 0);
+    w.bytes = w.sum + (sum ? s.K * s.V * 4 : 0);
+    return w;
+}
+
+int check_ptr(const char* fn, const char* name, const void* p, uintptr_t align, bool needed)
+{
+    if (needed && !p) return fail(RTP_EINVAL, "%s: NULL %s", fn, name);
+    if ((uintptr_t)p & (align - 1)) return fail(RTP_EINVAL, "%s: %s must be %d-byte aligned", fn, name, (int)align);
+    return RTP_OK;
+}
+int check_ptrs(const char* fn, const char* name, const void* const* p, int n)
+{
+    if (!p) return fail(RTP_EINVAL, "%s: NULL %s", fn, name);
+    for (int i = 0; i < n; ++i) TRY(check_ptr(fn, name, p[i], 16, true));
+    return RTP_OK;
+}
+
+struct Call {
+    const char* fn;
+    Shape s;
+    const void* X;
+    const void* const* W;
+    const void* targets;
+    int targets64;
+    int64_t ignore;
+    char* ws;
+    Space space;
+};
+
+int check_call(Call& c, int targets64, int64_t workspace_bytes, const float* loss)
+{
+    const char* fn = c.fn;
+    const bool some = c.s.M > 0;
+    if (targets64 != 0 && targets64 != 1) return fail(RTP_EINVAL, "%s: targets64 = %d", fn, targets64);
+    TRY(check_ptrs(fn, "weight", c.W, c.s.P));
+    TRY(check_ptr(fn, "X", c.X, 16, some));
+    TRY(check_ptr(fn, "targets", c.targets, targets64 ? 8 : 4, some));
+    TRY(check_ptr(fn, "loss", loss, 4, some));
+    TRY(check_ptr(fn, "workspace", c.ws, 256, true));
+    if (workspace_bytes < c.space.bytes)
+        return fail(RTP_EINVAL, "%s: a workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes, (long long)c.space.bytes);
+    return RTP_OK;
+}
+
+const void* rows_of(const void* p, int64_t first, int64_t row_bytes)
+{
+    return p ? static_cast<const char*>(p) + first * row_bytes : nullptr;
+}
+
+// The product with its statistics for `rows` rows from `first`, and the rows' arguments.
+int softmax_product(const Call& c, LinEpi epi, int64_t first, int64_t rows, RowsArgs* a, cudaStream_t stream)
+{
+    LinGemm g;
+    g.epi = epi;
+    g.groups = c.s.P;
+    g.a_shared = true;
+    g.rows = rows;
+    g.cols = c.s.Vp;
+    g.kdim = c.s.K;
+    for (int i = 0; i < c.s.P; ++i) {
+        g.A[i] = rows_of(c.X, first, c.s.K * 2);
+        g.B[i] = c.W[i];
+        if (epi == LIN_EXP) {
+            g.out[i] = c.ws + c.space.e + i * rows * c.s.Vp * 2;
+            a->e[i] = static_cast<__nv_bfloat16*>(g.out[i]);
+        }
+    }
+    g.softmax.stats = reinterpret_cast<float2*>(c.ws + c.space.stats);
+    g.softmax.target_logit = reinterpret_cast<float*>(c.ws + c.space.logit);
+    g.softmax.targets = rows_of(c.targets, first, c.targets64 ? 8 : 4);
+    g.softmax.targets64 = c.targets64;
+    g.softmax.vocab = c.s.vocab;
+    a->softmax = softmax_args(g.softmax, (int)parts(c.s, rows));
+    a->ignore = c.ignore;
+    a->P = c.s.P;
+    a->cols = (int)c.s.Vp;
+    a->part_cols = part_cols(rows);
+    a->parts_of_rank = a->softmax.parts / c.s.P;
+    return rows <= LIN_FEW_ROWS ? launch_linear_few(c.fn, g, false, stream) : launch_linear_gemm(c.fn, g, stream);
+}
+
+int forward_impl(Call& c, int targets64, int64_t workspace_bytes, float* loss, float* lse, cudaStream_t stream)
+{
+    c.space = space_of(c.s, false, false);
+    TRY(check_call(c, targets64, workspace_bytes, loss));
+    TRY(check_ptr(c.fn, "lse", lse, 4, false));
+    if (c.s.M == 0) return RTP_OK;
+    RowsArgs a = {};
+    TRY(softmax_product(c, LIN_LSE, 0, c.s.M, &a, stream));
+    a.loss = loss;
+    a.lse = lse;
+    return launch(c.fn, loss_rows_kernel<false>, dim3((unsigned)c.s.M), THREADS, stream, a);
+}
+
+int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* weights, int mean, float scale, float* total,
+               float* loss, int dx_dtype, void* dX, int dw_dtype, void* const* dW, int accumulate, cudaStream_t stream)
+{
+    const char* fn = c.fn;
+    const Shape& s = c.s;
+    const bool some = s.M > 0;
+    if ((dx_dtype != RTP_F32 && dx_dtype != RTP_BF16) || (dw_dtype != RTP_F32 && dw_dtype != RTP_BF16))
+        return fail(RTP_EINVAL, "%s: a gradient is of unknown type", fn);
+    if (mean != 0 && mean != 1) return fail(RTP_EINVAL, "%s: mean = %d", fn, mean);
+    if (accumulate != 0 && accumulate != 1) return fail(RTP_EINVAL, "%s: accumulate = %d", fn, accumulate);
+    if (accumulate && (!dW || dw_dtype != RTP_F32)) return fail(RTP_EINVAL, "%s: only float32 weight gradients accumulate", fn);
+    const bool sums = dW && dw_dtype == RTP_BF16 && s.pieces > 1;
+    c.space = space_of(s, true, sums);
+    TRY(check_call(c, targets64, workspace_bytes, loss));
+    TRY(check_ptr(fn, "weights", weights, 4, false));
+    TRY(check_ptr(fn, "total", total, 4, true));
+    TRY(check_ptr(fn, "dX", dX, 16, false));
+    if (dW) TRY(check_ptrs(fn, "dW", const_cast<const void* const*>(dW), s.P));
+    int sms = 0;
+    if (device_sms(&sms)) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
+    const int64_t dx_size = dx_dtype == RTP_F32 ? 4 : 2, dw_size = dw_dtype == RTP_F32 ? 4 : 2;
+    Shared* sh = reinterpret_cast<Shared*>(c.ws);
+    TRY(launch(fn, loss_scale_kernel, dim3(1), 1024, stream, c.targets, c.targets64, weights, s.M, c.ignore, mean, scale, sh, total));
+    if (!some) {
+        for (int i = 0; dW && !accumulate && i < s.P; ++i)
+            if (cudaMemsetAsync(dW[i], 0, (size_t)(s.K * s.Vp * dw_size), stream) != cudaSuccess)
+                return fail(RTP_ECUDA, "%s: cudaMemsetAsync failed", fn);
+        return RTP_OK;
+    }
+    for (int p = 0; p < s.pieces; ++p) {
+        const int64_t first = p * s.piece, rows = std::min(s.piece, s.M - first);
+        RowsArgs a = {};
+        TRY(softmax_product(c, LIN_EXP, first, rows, &a, stream));
+        a.weights = weights ? weights + first : nullptr;
+        a.loss = loss + first;
+        a.shared = sh;
+        a.mean = mean;
+        if (p == s.pieces - 1) {
+            a.total = total;
+            a.all_loss = loss;
+            a.all_weights = weights;
+            a.all_targets = c.targets;
+            a.all_rows = s.M;
+        }
+        // Blocks that share a row, where the rows alone would not fill the GPU: each with
+        // at least 2 vectors of a rank's columns for every thread.
+        unsigned split = 1;
+        while (rows * split < 2 * sms && split < 16 && s.Vp / 8 >= 2 * 2 * split * THREADS) split *= 2;
+        TRY(launch(fn, loss_rows_kernel<true>, dim3((unsigned)rows, split), THREADS, stream, a));
+        if (dX) {
+            LinGemm g;
+            g.groups = s.P;
+            g.fused = true;
+            g.b_t = true;
+            g.out_f32 = dx_dtype == RTP_F32;
+            g.rows = rows;
+            g.cols = s.K;
+            g.kdim = s.Vp;
+            for (int i = 0; i < s.P; ++i) {
+                g.A[i] = a.e[i];
+                g.B[i] = c.W[i];
+            }
+            g.out[0] = static_cast<char*>(dX) + first * s.K * dx_size;
+            TRY(launch_linear_gemm(fn, g, stream));
+        }
+        if (dW) {
+            LinGemm g;
+            g.groups = s.P;
+            g.a_t = true;
+            g.a_shared = true;
+            g.out_f32 = sums || dw_dtype == RTP_F32;
+            g.accumulate = accumulate || p > 0;
+            g.rows = s.K;
+            g.cols = s.Vp;
+            g.kdim = rows;
+            for (int i = 0; i < s.P; ++i) {
+                g.A[i] = rows_of(c.X, first, s.K * 2);
+                g.B[i] = a.e[i];
+                g.out[i] = sums ? c.ws + c.space.sum + i * s.K * s.Vp * 4 : dW[i];
+            }
+            TRY(launch_linear_gemm(fn, g, stream));
+        }
+    }
+    if (sums) {
+        RoundArgs a = {};
+        for (int i = 0; i < s.P; ++i) {
+            a.from[i] = reinterpret_cast<const float4*>(c.ws + c.space.sum + i * s.K * s.Vp * 4);
+            a.to[i] = static_cast<uint2*>(dW[i]);
+        }
+        a.quads = s.K * s.Vp / 4;
+        const int64_t blocks = std::min<int64_t>((a.quads + THREADS - 1) / THREADS, (int64_t)8 * sms);
+        TRY(launch(fn, round_kernel, dim3((unsigned)blocks, (unsigned)s.P), THREADS, stream, a));
+    }
+    return RTP_OK;
+}
+
+}  // namespace
+
+}  // namespace rtp
+
+using namespace rtp;
+
+extern "C" {
+
+int rtp_tp_cross_entropy_workspace(int P, int64_t M, int64_t K, int64_t V, int64_t piece_rows, int train, rtp_dtype dw_dtype,
+                                   int64_t* bytes)
+{
+    const char* fn = "rtp_tp_cross_entropy_workspace";
+    if (!bytes) return fail(RTP_EINVAL, "%s: NULL argument", fn);
+    Shape s;
+    TRY(check_shape(fn, P, M, K, V, V, piece_rows, train != 0, &s));
+    *bytes = space_of(s, train != 0, train && dw_dtype == RTP_BF16 && s.pieces > 1).bytes;
+    return RTP_OK;
+}
+
+int rtp_tp_cross_entropy(int P, int64_t M, int64_t K, int64_t V, int64_t vocab, const void* X, const void* const* W_shards,
+                         int targets64, const void* targets, int64_t ignore_index, void* workspace, int64_t workspace_bytes,
+                         float* loss, float* lse, rtp_stream stream)
+{
+    const char* fn = "rtp_tp_cross_entropy";
+    return guarded(fn, [&] {
+        Call c = {fn, {}, X, W_shards, targets, targets64, ignore_index, static_cast<char*>(workspace), {}};
+        TRY(check_shape(fn, P, M, K, V, vocab, 0, false, &c.s));
+        return forward_impl(c, targets64, workspace_bytes, loss, lse, static_cast<cudaStream_t>(stream));
+    });
+}
+
+int rtp_tp_cross_entropy_train(int P, int64_t M, int64_t K, int64_t V, int64_t vocab, const void* X,
+                               const void* const* W_shards, int targets64, const void* targets, int64_t ignore_index,
+                               const float* weights, int mean, float scale, int64_t piece_rows, void* workspace,
+                               int64_t workspace_bytes, float* total, float* loss, rtp_dtype dx_dtype, void* dX,
+                               rtp_dtype dw_dtype, void* const* dW, int accumulate, rtp_stream stream)
+{
+    const char* fn = "rtp_tp_cross_entropy_train";
+    return guarded(fn, [&] {
+        Call c = {fn, {}, X, W_shards, targets, targets64, ignore_index, static_cast<char*>(workspace), {}};
+        TRY(check_shape(fn, P, M, K, V, vocab, piece_rows, true, &c.s));
+        return train_impl(c, targets64, workspace_bytes, weights, mean, scale, total, loss, dx_dtype, dX, dw_dtype, dW, accumulate,
+                          static_cast<cudaStream_t>(stream));
+    });
+}
+
+}  // extern "C"

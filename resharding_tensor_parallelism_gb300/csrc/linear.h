@@ -15,6 +15,19 @@ enum LinEpi : int {
     LIN_OUT = 0,   // out = act(acc + bias) + residual; optionally h = acc + bias
     LIN_GLU = 1,   // out = act(gate) * up, from B (gate) and B2 (up); optionally out2 = gate, out3 = up
     LIN_DGLU = 2,  // acc = dY: out = acc * up * act'(gate), out2 = acc * act(gate); gate = aux, up = aux2
+    LIN_LSE = 3,   // acc = logits: softmax statistics of each row's part of a tile, and the target's logit
+    LIN_EXP = 4,   // LIN_LSE, and out = the exponentials that the statistics sum up
+};
+
+// Softmax statistics (LIN_LSE, LIN_EXP): for a row and a part (the columns of one tile)
+// x = ref, y = sum over the part's columns j of 2^(l_j log2(e) - ref), ref = the part's
+// largest l_j log2(e); (-inf, 0) where a part has no column of the vocabulary.
+struct LinSoftmax {
+    float2* stats = nullptr;        // [rows][groups * parts of a group]
+    float* target_logit = nullptr;  // [rows]; not written where the target is in no column
+    const void* targets = nullptr;  // [rows], int64 or int32: column counted over the groups
+    int targets64 = 1;
+    int64_t vocab = 0;              // columns from here on (counted over the groups) take no part
 };
 
 // A [rows, kdim] times B [kdim, cols], bf16 row-major, float32 accumulation.
@@ -26,6 +39,7 @@ enum LinEpi : int {
 struct LinGemm {
     int groups = 1;
     bool fused = false, a_t = false, b_t = false, a_shared = false, out_f32 = false;
+    bool accumulate = false;  // gradients in float32: out += product
     LinEpi epi = LIN_OUT;
     int act = RTP_ACT_NONE;
     int64_t rows = 0, cols = 0, kdim = 0;
@@ -39,13 +53,16 @@ struct LinGemm {
     const void* residual[LIN_MAX_RANKS] = {};
     const void* aux[LIN_MAX_RANKS] = {};
     const void* aux2[LIN_MAX_RANKS] = {};
+    LinSoftmax softmax;
 };
 
 // The 2-SM pair kernel (linear_gemm.cu): any LinGemm, in tiles of 256 x 256 (LIN_GLU:
 // 128 columns of the output).
 constexpr int LIN_TILE_ROWS = 256, LIN_TILE_COLS = 256;
+// Columns of the few-row kernel's tiles.
+constexpr int LIN_FEW_COLS = 128;
 int launch_linear_gemm(const char* fn, const LinGemm& g, cudaStream_t stream);
-// The few-row kernel (linear_few.cu): LIN_OUT and LIN_GLU, at most
+// The few-row kernel (linear_few.cu): all but LIN_DGLU, at most
 // LIN_FEW_ROWS rows, no transposed operands. weights_ready: nothing queued on the
 // stream since a kernel that waited for its own predecessor writes B, so B may be
 // read before the previous kernel has finished.

@@ -2,6 +2,7 @@
 // transposed, out^T = B^T A^T: 128 output columns ("features") of a CTA are the M
 // operand of the MMA, the rows ("tokens"), up to 128 in steps of 16, its N operand.
 // For LIN_GLU a CTA's 128 features are 64 gate and the same 64 up columns.
+// LIN_LSE and LIN_EXP leave softmax statistics of 128 columns (softmax.cuh).
 //
 // With few tokens every weight is used a handful of times, so the weights' bytes
 // over the HBM rate bound the time, and the tiles of the pair kernel would leave
@@ -19,13 +20,14 @@
 
 #include "activation.cuh"
 #include "linear.h"
+#include "softmax.cuh"
 #include "tcgen05.cuh"
 
 namespace rtp {
 
 namespace {
 
-constexpr int FEAT = 128;                      // features of a CTA's tile
+constexpr int FEAT = LIN_FEW_COLS;             // features of a CTA's tile
 constexpr uint32_t SUB = 64 * BK * 2;          // one 64 x 64 box, 8 KB
 constexpr uint32_t W_BYTES = FEAT * BK * 2;    // 16 KB
 constexpr int THREADS = 256;                   // warps w and w + 4 read the same quarter of the tensor memory's lanes
@@ -48,6 +50,7 @@ struct Args {
     int32_t split, stages;
     int32_t act, keep, weights_ready;
     unsigned long long wait_ns;  // limit of a wait for this kernel's own progress
+    SoftmaxArgs softmax;
 };
 
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -279,7 +282,40 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
         for (int r = 1; r < a.split; ++r) v = add4(v, ld_cluster_f4(map_to_rank(addr, (uint32_t)r)));
         return v;
     };
-    while (i0 < items) {
+    if constexpr (EPI == LIN_LSE || EPI == LIN_EXP) {
+        // A warp takes a token at a time, a lane 4 of its 128 features.
+        const int f = 4 * lane, cols = min(FEAT, a.cols - f0);
+        const int64_t first = (int64_t)g * a.cols + f0;
+        const int valid = min(valid_columns(a.softmax, first, FEAT), cols);
+#pragma unroll 2
+        for (int t = part * (THREADS / 32) + warp; t < a.rows; t += a.split * (THREADS / 32)) {
+            const float4 w = sum4(t, f);
+            float v[4] = {w.x, w.y, w.z, w.w}, top = minus_infinity(), sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (f + j >= valid) v[j] = minus_infinity();
+                top = fmaxf(top, v[j]);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top *= LOG2E;
+            const float ref = finite_ref(top);
+            const int target = target_in(a.softmax, t, first, valid) - f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (target == j) a.softmax.target_logit[t] = v[j];
+                v[j] = exp2_fast(fmaf(v[j], LOG2E, -ref));
+                sum += v[j];
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) a.softmax.stats[(int64_t)t * a.softmax.parts + tile] = make_float2(top, sum);
+            if (EPI == LIN_EXP && f < cols)
+                store_bf16x4(static_cast<__nv_bfloat16*>(a.out[g]) + (int64_t)t * a.cols + f0 + f,
+                             make_float4(v[0], v[1], v[2], v[3]));
+        }
+    }
+    while (EPI != LIN_LSE && EPI != LIN_EXP && i0 < items) {
         float4 v[UNROLL];
 #pragma unroll
         for (int j = 0; j < UNROLL; ++j) {
@@ -407,6 +443,7 @@ int launch_linear_few(const char* fn, const LinGemm& p, bool weights_ready, cuda
     a.rows = (int)p.rows;
     a.cols = (int)p.cols;
     a.act = p.act;
+    a.softmax = softmax_args(p.softmax, outs * a.tiles);
     a.weights_ready = weights_ready;
     int64_t wait_ns = (int64_t)WAIT_LIMIT_NS;
     take_hook(RTP_HOOK_WAIT_LIMIT, &wait_ns);
@@ -422,6 +459,8 @@ int launch_linear_few(const char* fn, const LinGemm& p, bool weights_ready, cuda
            a.kbs >= 2 * a.split * (tiles * a.split * 2 <= sms ? 4 : 8))
         a.split *= 2;
     const size_t smem = (size_t)a.stages * stage + SMEM_EXTRA;
+    if (p.epi == LIN_LSE) return launch_t<LIN_LSE, false>(fn, a, (unsigned)tiles, smem, stream);
+    if (p.epi == LIN_EXP) return launch_t<LIN_EXP, false>(fn, a, (unsigned)tiles, smem, stream);
     if (p.epi == LIN_GLU) return launch_t<LIN_GLU, false>(fn, a, (unsigned)tiles, smem, stream);
     return p.out_f32 ? launch_t<LIN_OUT, true>(fn, a, (unsigned)tiles, smem, stream)
                      : launch_t<LIN_OUT, false>(fn, a, (unsigned)tiles, smem, stream);

@@ -43,7 +43,7 @@ int launch_linear_gemm(const char* fn, const LinGemm& p, cudaStream_t stream)
     const int outs = p.fused ? 1 : p.groups;
     a.keep = p.epi == LIN_DGLU || p.out2[0] != nullptr;
     for (int g = 0; g < outs; ++g) {
-        if ((st = epi_map(&a.to[g], p.out[g], p.rows, p.cols, p.out_f32))) return st;
+        if (p.epi != LIN_LSE && (st = epi_map(&a.to[g], p.out[g], p.rows, p.cols, p.out_f32))) return st;
         if (a.keep && (st = epi_map(&a.to2[g], p.out2[g], p.rows, p.cols, false))) return st;
         if (a.keep && p.epi == LIN_GLU && (st = epi_map(&a.to3[g], p.out3[g], p.rows, p.cols, false))) return st;
         const void* in = p.epi == LIN_DGLU ? p.aux[g] : g < LIN_MAX_RANKS ? p.residual[g] : nullptr;
@@ -58,6 +58,7 @@ int launch_linear_gemm(const char* fn, const LinGemm& p, cudaStream_t stream)
     a.has_bias = p.bias[0] != nullptr;
     a.has_residual = p.residual[0] != nullptr;
     a.act = p.act;
+    a.accumulate = p.accumulate;
     a.ld = p.cols;
     a.groups = p.groups;
     a.fused = p.fused;
@@ -68,6 +69,7 @@ int launch_linear_gemm(const char* fn, const LinGemm& p, cudaStream_t stream)
     a.n_tiles = (int)((p.cols + tile_cols - 1) / tile_cols);
     a.kb_per_group = (int)((p.kdim + BK - 1) / BK);
     a.total_tiles = outs * a.m_tiles * a.n_tiles;
+    a.softmax = softmax_args(p.softmax, outs * a.n_tiles);
     // Short K: tall blocks of M tiles, whose A rows stay in L2 while the B columns
     // stream past; long K: near-square waves, which read the fewest panels (as
     // measured for the plain tensor-parallel MLP's products).

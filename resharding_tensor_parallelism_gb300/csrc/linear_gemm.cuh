@@ -6,6 +6,10 @@
 //   LIN_GLU    y = act(X Ag) * (X Au): both projections and their product in one
 //              kernel, and optionally the two pre-activations
 //   LIN_DGLU   acc = dY = dZ B^T: dHg = dY * Hu * act'(Hg), dHu = dY * act(Hg)
+//   LIN_LSE    acc = logits: of each row's 256 columns the largest and the sum of the
+//              exponentials relative to it, and the logit of the row's target
+//   LIN_EXP    the same, and the exponentials in bf16 (two passes over the tensor memory:
+//              they are relative to the largest one of the whole tile)
 //
 // The tensor pipe bounds them: 2 rows cols kdim operations. A cluster of 2 CTAs
 // (2 SMs) computes one 256 x 256 accumulator tile per step, as in the plain
@@ -39,6 +43,7 @@
 
 #include "activation.cuh"
 #include "linear.h"
+#include "softmax.cuh"
 #include "tcgen05.cuh"
 
 namespace rtp {
@@ -56,6 +61,8 @@ struct LinArgs {
     int32_t act, has_bias, has_residual, keep;
     int32_t kbs;    // K blocks of a tile (of all operand pairs when fused)
     int32_t split;  // SPLIT kernels: K parts of a tile, over a cluster of `split` pairs
+    int32_t accumulate;  // float32 gradients are added to what is there
+    SoftmaxArgs softmax;
 };
 
 namespace {
@@ -163,6 +170,7 @@ __global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_ke
     constexpr int EPI = CFG >> CFG_EPI_SHIFT;
     constexpr bool PLAIN = EPI == LIN_OUT && (A_T || B_T);  // gradients: the accumulator alone
     constexpr bool ACT = EPI != LIN_OUT || (CFG & CFG_ACT) != 0;
+    constexpr bool SOFTMAX = EPI == LIN_LSE || EPI == LIN_EXP;
     constexpr int TILE_COLS = EPI == LIN_GLU ? BN / 2 : BN;
     using L = Layout<CFG, SPLIT>;
     constexpr int STAGES = L::stages, SLOTS = L::slots, EPI_WARPS = L::epi_warps;
@@ -212,7 +220,7 @@ __global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_ke
             prefetch_map(&a.tb[EPI == LIN_GLU ? (int)cta * LIN_MAX_RANKS + g : g]);
         }
     }
-    if (warp == 2 && lane == 0) {
+    if (EPI != LIN_LSE && warp == 2 && lane == 0) {
         for (int g = 0; g < (a.fused ? 1 : a.groups); ++g) prefetch_map(&a.to[g]);
     }
     if (warp == 1) {
@@ -400,6 +408,12 @@ __global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_ke
                 if (has_bias && (lane >> 2) < CHUNKS && at < TILE_COLS && tile_col + at < a.cols)
                     bias = __ldg(reinterpret_cast<const uint4*>(a.bias[g] + tile_col + at));
             }
+            int valid = 0, target = -1;  // columns of the tile in the vocabulary; the row's target among them
+            if constexpr (SOFTMAX) {
+                const int64_t first_col = (int64_t)g * a.cols + tile_col;
+                valid = min(valid_columns(a.softmax, first_col, TILE_COLS), a.cols - tile_col);
+                if (row < a.rows) target = target_in(a.softmax, row, first_col, valid);
+            }
             int ok = 1;
             if (lane == 0) ok = wait_bar(acc_full(acc), acc_phase, abort_flag, ERR_EPILOGUE) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -462,7 +476,8 @@ __global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_ke
             };
             auto store = [&](const CUtensorMap* map, uint32_t s, int c0) {
                 if (lane == 0) {
-                    tma_store_2d(map, slot_addr(s), c0, row0);
+                    if (F32 && PLAIN && a.accumulate) tma_add_2d(map, slot_addr(s), c0, row0);
+                    else tma_store_2d(map, slot_addr(s), c0, row0);
                     bulk_commit();
                 }
             };
@@ -548,7 +563,78 @@ __global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_ke
                 }
                 cluster_sync();
             }
-            if constexpr (EPI == LIN_OUT) {
+            if constexpr (SOFTMAX) {
+                // logits of step c, -inf outside the vocabulary; the next step's are on their way
+                float top = minus_infinity(), sum = 0.0f, logit = 0.0f;
+                auto logits = [&](int c, float (&v)[STEP]) {
+                    take(c, 0, ra, v);
+                    if (c + 1 < steps) start(c + 1, 0, ra);
+                    const int col = column(c);
+                    if (col + STEP > valid) {
+#pragma unroll
+                        for (int j = 0; j < STEP; ++j)
+                            if (col + j >= valid) v[j] = minus_infinity();
+                    }
+                };
+                auto largest = [](const float (&v)[STEP]) {
+                    float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                    for (int j = 4; j < STEP; ++j) m[j & 3] = fmaxf(m[j & 3], v[j]);
+                    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                };
+                auto find_target = [&](int c, const float (&v)[STEP]) {
+                    const int at = target - column(c);
+                    if (__any_sync(0xffffffffu, at >= 0 && at < STEP)) {
+#pragma unroll
+                        for (int j = 0; j < STEP; ++j)
+                            if (at == j) logit = v[j];
+                    }
+                };
+                // v becomes its exponentials, relative to ref; returns their sum
+                auto exponentials = [](float (&v)[STEP], float ref) {
+                    float s[4] = {};
+#pragma unroll
+                    for (int j = 0; j < STEP; ++j) {
+                        v[j] = exp2_fast(fmaf(v[j], LOG2E, -ref));
+                        s[j & 3] += v[j];
+                    }
+                    return (s[0] + s[1]) + (s[2] + s[3]);
+                };
+                if constexpr (EPI == LIN_EXP) {
+                    if (steps > 0) start(0, 0, ra);
+#pragma unroll 1
+                    for (int c = 0; c < steps; ++c) {
+                        float v[STEP];
+                        logits(c, v);
+                        top = fmaxf(top, largest(v));
+                    }
+                    top *= LOG2E;
+                }
+                const float ref = finite_ref(top);
+                if (steps > 0) start(0, 0, ra);
+#pragma unroll 1
+                for (int c = 0; c < steps; ++c) {
+                    const uint32_t s = slot + (uint32_t)c;
+                    float v[STEP];
+                    logits(c, v);
+                    find_target(c, v);
+                    if constexpr (EPI == LIN_EXP) {
+                        sum += exponentials(v, ref);
+                        acquire();
+                        put_bf16(s, c, v);
+                        flush();
+                        store(&a.to[g], s, tile_col + chunk_at(c));
+                    } else {
+                        const float now = fmaxf(top, largest(v) * LOG2E), r = finite_ref(now);
+                        sum = sum * exp2_fast(top - r) + exponentials(v, r);
+                        top = now;
+                    }
+                }
+                if (row < a.rows && steps > 0) {
+                    a.softmax.stats[row * a.softmax.parts + g * a.n_tiles + nt] = make_float2(top, sum);
+                    if (target >= 0) a.softmax.target_logit[row] = logit;
+                }
+            } else if constexpr (EPI == LIN_OUT) {
                 if (steps > 0) start(0, 0, ra);
 #pragma unroll 1
                 for (int c = 0; c < steps; ++c) {
@@ -823,6 +909,12 @@ int launch_cfg(const char* fn, int cfg, LinArgs& a, cudaStream_t stream)
     case CFG_A_T | CFG_F32: return launch_t<CFG_A_T | CFG_F32, SPLIT>(fn, a, stream);
     case CFG_B_T: return launch_t<CFG_B_T, SPLIT>(fn, a, stream);
     case CFG_B_T | CFG_F32: return launch_t<CFG_B_T | CFG_F32, SPLIT>(fn, a, stream);
+    case LIN_LSE << CFG_EPI_SHIFT:
+        if constexpr (!SPLIT) return launch_t<LIN_LSE << CFG_EPI_SHIFT, SPLIT>(fn, a, stream);
+        return LIN_NOT_SPLIT;
+    case LIN_EXP << CFG_EPI_SHIFT:
+        if constexpr (!SPLIT) return launch_t<LIN_EXP << CFG_EPI_SHIFT, SPLIT>(fn, a, stream);
+        return LIN_NOT_SPLIT;
     default: return fail(RTP_EUNSUPPORTED, "%s: no product for transposed operands of this kind", fn);
     }
 }
