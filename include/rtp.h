@@ -660,10 +660,11 @@ int rtp_tp_cross_entropy(int P, int64_t M, int64_t K, int64_t V, int64_t vocab, 
  *             micro-batches); subnormal values count as zero in such a sum
  *   piece_rows rows that are taken at once (rounded up to 256): the workspace holds 2 V
  *             bytes for each; 0: as many as keep that within the float32 sums of dW that
- *             several pieces need, 2 K or 2048
- * d is bf16: exp(l - largest of its tile) rounded once, d once more; both products read
- * it. A row whose target is outside the vocabulary has NaN gradients. d of a row without
- * a part is 0 whatever X holds there; dW still multiplies it with that X (0 * NaN).
+ *             several pieces need (2 K rows, at least 2048), or within 1 GiB
+ * The products read bf16: the exponentials, of a row relative to the same number (at the
+ * target less the row's sum), and for dW the rows of X times g_r over the row's sum. A row
+ * whose target is outside the vocabulary has NaN gradients; a row without a part gives
+ * none, whatever X holds there.
  * The rest as in rtp_tp_cross_entropy. M == 0 zeroes total and, unless accumulate, dW.
  */
 int rtp_tp_cross_entropy_train(int P, int64_t M, int64_t K, int64_t V, int64_t vocab, const void* X,

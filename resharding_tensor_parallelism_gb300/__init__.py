@@ -1002,8 +1002,8 @@ def tp_cross_entropy_train(X, W_shards, targets, weights=None, vocab: Optional[i
     divided by the sum of the weights of the rows that are not ignored ("mean"; 0 where that is 0). weights: float32 [M],
     or None (1). Returns (total, loss, dX, dW): float32 scalar (not scaled) and [M], dX [M, K] and the list dW like
     W_shards, bf16 or float32 (dx_dtype, dw_dtype, or by the buffers given). accumulate: dW (float32, given) += the
-    gradient. Rows are taken in pieces of piece_rows (0: as many as the scratch for the exponentials, 2 V bytes a row, is
-    worth); several pieces need 4 K V bytes more to sum a bf16 dW in float32."""
+    gradient. Rows are taken in pieces of piece_rows (0: 2 K rows, at least 2048, or as many as take 1 GiB of scratch for the
+    exponentials, 2 V bytes a row); several pieces need 4 K V bytes more to sum a bf16 dW in float32."""
     fn = "tp_cross_entropy_train"
     torch = _torch()
     W = _listed(W_shards)

@@ -4,17 +4,21 @@
 //   l = X [W_0 .. W_{P-1}]        lse_r = log sum_j exp l_rj       loss_r = lse_r - l_{r,t_r}
 //   d_rj = g_r (exp(l_rj - lse_r) - [j = t_r])     dX = sum_i d_i W_i^T     dW_i = X^T d_i
 //
-// Forward: the product's epilogue leaves, for each row and tile, the largest logit and
-// the sum of the exponentials relative to it (softmax.cuh); loss_rows_kernel joins them.
+// Forward: the product's epilogue leaves, for each row and tile, the sum of the
+// exponentials (softmax.cuh); loss_rows_kernel joins them.
 // Training, 6 M K V operations: the same product also writes the exponentials e in bf16,
-// relative to their tile's largest logit (so each holds its value to half a bf16 step,
-// whatever the logits' size, which rounded logits would not); loss_rows_kernel, with the
-// row's sum at hand, turns them in place into d, rounded once more; two products read d.
-// Recomputing the logits instead would cost a third more operations and save that one
-// pass over 2 M V bytes.
+// all of a row relative to the same number. With s_r the row's sum,
+//   d_rj = (g_r / s_r) (e_rj - s_r [j = t_r])
+// so the second factor is e but for one element of a row, and the first one is applied to
+// the rows of what d multiplies: dX_r = (g_r / s_r) sum_j (..)_rj W_j in that product's
+// epilogue, dW = X'^T (..) with X'_r = (g_r / s_r) X_r. loss_rows_kernel writes that element,
+// the factor and X'; e is never read but by the two products. (Turning e into d in a pass of
+// its own took 0.63 ms of the 16.3 of 8192 x 4096 x 131072, and one more rounding.) Rows with
+// logits beyond what exponentials hold relative to 0 are brought to one reference there.
+// Recomputing the logits instead of keeping e would cost a third more operations.
 //
-// The exponentials of all rows take 2 M V bytes. Rows are taken in pieces, so that they
-// take no more than the float32 sums of dW that pieces need (4 K V): 2 K rows at most.
+// The exponentials take 2 V bytes a row. Rows are taken in pieces, so that they take no
+// more than the float32 sums of dW that several pieces need (4 K V: 2 K rows), or 1 GiB.
 // With several pieces dW is summed in float32, by adds in the output's TMA stores.
 #include <algorithm>
 #include <cstring>
@@ -39,20 +43,20 @@ constexpr int64_t SHARED_BYTES = 256;
 
 struct RowsArgs {
     SoftmaxArgs softmax;  // of the piece's rows
-    int64_t ignore;
-    const float* weights;  // of the piece's rows, or NULL
-    float* loss;           // of the piece's rows
-    float* lse;            // or NULL
+    float* loss;          // of the piece's rows
+    float* lse;           // or NULL
     // training
     __nv_bfloat16* e[LIN_MAX_RANKS];
+    const uint4* x;  // [rows, K]
+    uint4* scaled;   // x times the row's factor
+    float* factor;
     Shared* shared;
     float* total;              // or NULL: not the last piece
-    const float* all_loss;     // of every row, with their weights and targets
+    const float* all_loss;     // of every row, with their weights
     const float* all_weights;
-    const void* all_targets;
     int64_t all_rows;
     int32_t mean;
-    int32_t P, cols, part_cols, parts_of_rank;
+    int32_t P, cols, part_cols, parts_of_rank, x_vectors;
 };
 
 template <class T, class F>
@@ -69,13 +73,10 @@ __device__ __forceinline__ T block_reduce(T v, T* scratch, F&& f)
     return v;
 }
 
-// d of 8 neighbouring columns from their exponentials; `at`: the target among them, or not.
-__device__ __forceinline__ uint4 gradients(const uint4& e, float factor, float g, int at)
+__device__ __forceinline__ uint4 times(const uint4& v, float f)
 {
-    float d[8] = {bf16_lo(e.x), bf16_hi(e.x), bf16_lo(e.y), bf16_hi(e.y), bf16_lo(e.z), bf16_hi(e.z), bf16_lo(e.w), bf16_hi(e.w)};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) d[j] = j == at ? fmaf(d[j], factor, -g) : d[j] * factor;
-    return make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
+    return make_uint4(pack_bf16(bf16_lo(v.x) * f, bf16_hi(v.x) * f), pack_bf16(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
+                      pack_bf16(bf16_lo(v.z) * f, bf16_hi(v.z) * f), pack_bf16(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
 }
 
 // Sum over every row of weight * loss, in a fixed order.
@@ -91,8 +92,8 @@ __device__ __forceinline__ float total_loss(const RowsArgs& a, double* scratch)
     return (float)s;
 }
 
-// One row a block (blockIdx.x; gridDim.y blocks share its columns): joins the row's
-// statistics into lse and loss and, TRAIN, turns its exponentials into d.
+// One row a block: joins the row's statistics into lse and loss and, TRAIN, does what the
+// head of this file says. Latency bound: 2 KB of statistics and K elements a row.
 template <bool TRAIN>
 __global__ void __launch_bounds__(THREADS) loss_rows_kernel(const __grid_constant__ RowsArgs a)
 {
@@ -103,51 +104,55 @@ __global__ void __launch_bounds__(THREADS) loss_rows_kernel(const __grid_constan
     const int64_t row = blockIdx.x;
     const float2* stats = a.softmax.stats + row * a.softmax.parts;
     const int64_t t = target_at(a.softmax.targets, a.softmax.targets64, row);
-    const bool ignored = t == a.ignore, known = t >= 0 && t < a.softmax.vocab;
-    float top = minus_infinity(), sum = 0.0f;
+    const bool ignored = t == a.softmax.ignore, known = t >= 0 && t < a.softmax.vocab;
+    const float w = !TRAIN ? 0.0f : a.softmax.weights ? __ldcg(a.softmax.weights + row) : 1.0f;
+    // The row's reference is the largest of its parts': 0, unless a part has one above, or all below.
+    float top = minus_infinity(), low = -minus_infinity(), sum = 0.0f;
     for (int i = threadIdx.x; i < a.softmax.parts; i += THREADS) {
         const float2 s = __ldcg(stats + i);
         const float now = fmaxf(top, s.x), r = finite_ref(now);
         sum = sum * exp2_fast(top - r) + s.y * exp2_fast(s.x - r);
         top = now;
+        if (s.x > minus_infinity()) low = fminf(low, s.x);
     }
     const float mine = top;
     top = block_reduce(top, scratch_f, [](float x, float y) { return fmaxf(x, y); });
     const float ref = finite_ref(top);
     sum = block_reduce(sum * exp2_fast(mine - ref), scratch_f, [](float x, float y) { return x + y; });
-    if (threadIdx.x == 0 && blockIdx.y == 0) {
+    const float logit = known ? __ldcg(a.softmax.target_logit + row) : 0.0f;
+    if (threadIdx.x == 0) {
         const float lse = (ref + log2f(sum)) * LN2;
         if (a.lse) a.lse[row] = lse;
-        float loss = ignored ? 0.0f : __int_as_float(0x7FC00000);
-        if (!ignored && known) loss = lse - __ldcg(a.softmax.target_logit + row);
-        a.loss[row] = loss;
+        a.loss[row] = ignored ? 0.0f : known ? lse - logit : __int_as_float(0x7FC00000);
     }
     if constexpr (TRAIN) {
-        const float w = a.weights ? __ldcg(a.weights + row) : 1.0f;
-        float g = ignored || w == 0.0f ? 0.0f : a.shared->scale * w;
-        if (!ignored && !known && g != 0.0f) g = __int_as_float(0x7FC00000);  // a target outside the vocabulary shows
-        const int vectors = a.cols / 8, stride = (int)gridDim.y * THREADS;
-        const float scaled = g / sum;
-        for (int i = 0; i < a.P; ++i) {
-            uint4* e = reinterpret_cast<uint4*>(a.e[i] + row * a.cols);
-            const float2* s = stats + i * a.parts_of_rank;
-            const int64_t first = t - (int64_t)i * a.cols;
-            const int at = known && first >= 0 && first < a.cols ? (int)first : -8;
-            if (g == 0.0f) {  // whatever the row holds
-                for (int v = (int)blockIdx.y * THREADS + threadIdx.x; v < vectors; v += stride) e[v] = make_uint4(0u, 0u, 0u, 0u);
-                continue;
+        const bool part = !ignored && w != 0.0f;
+        if (__syncthreads_or(low < top) && part) {
+            for (int i = 0; i < a.P; ++i) {
+                uint4* e = reinterpret_cast<uint4*>(a.e[i] + row * a.cols);
+                for (int v = threadIdx.x; v < a.cols / 8; v += THREADS) {
+                    const float r = __ldcg(stats + i * a.parts_of_rank + 8 * v / a.part_cols).x;
+                    if (r != ref) e[v] = times(e[v], exp2_fast(r - ref));
+                }
             }
-#pragma unroll 4
-            for (int v = (int)blockIdx.y * THREADS + threadIdx.x; v < vectors; v += stride) {
-                const float factor = scaled * exp2_fast(__ldcg(s + 8 * v / a.part_cols).x - ref);
-                e[v] = gradients(__ldcs(e + v), factor, g, at - 8 * v);
-            }
+            __syncthreads();
         }
+        // a target outside the vocabulary shows
+        const float factor = !part ? 0.0f : known ? a.shared->scale * w / sum : __int_as_float(0x7FC00000);
+        if (threadIdx.x == 0) {
+            a.factor[row] = factor;
+            if (part && known)
+                a.e[t / a.cols][row * a.cols + t % a.cols] = __float2bfloat16_rn(exp2_fast(fmaf(logit, LOG2E, -ref)) - sum);
+        }
+        const uint4* x = a.x + row * a.x_vectors;
+        uint4* scaled = a.scaled + row * a.x_vectors;
+        for (int v = threadIdx.x; v < a.x_vectors; v += THREADS)  // a row without a part is 0 whatever it holds
+            scaled[v] = part ? times(__ldcg(x + v), factor) : make_uint4(0u, 0u, 0u, 0u);
         if (!a.total) return;
         __shared__ bool closing;
         if (threadIdx.x == 0) {
             __threadfence();
-            closing = atomicAdd(&a.shared->finished, 1u) == gridDim.x * gridDim.y - 1;
+            closing = atomicAdd(&a.shared->finished, 1u) == gridDim.x - 1;
         }
         __syncthreads();
         if (!closing) return;
@@ -157,13 +162,15 @@ __global__ void __launch_bounds__(THREADS) loss_rows_kernel(const __grid_constan
     }
 }
 
-// The weight of the counted rows, from which the gradients' scale follows. One block:
-// 8192 rows take 3 us.
+// The weight of the counted rows, from which the gradients' scale follows. One block, which
+// runs beside the product before it: that one has waited for all earlier work, and neither
+// touches what the other writes. It ends after the product all the same, so that the kernel
+// behind it need wait for this one only. alone: there is no product (no rows).
 __global__ void __launch_bounds__(1024) loss_scale_kernel(const void* targets, int targets64, const float* weights, int64_t rows,
-                                                          int64_t ignore, int mean, float scale, Shared* sh, float* total)
+                                                          int64_t ignore, int mean, float scale, Shared* sh, float* total, int alone)
 {
     __shared__ double sums[32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (alone) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     double s = 0.0;
     if (mean)
@@ -173,13 +180,15 @@ __global__ void __launch_bounds__(1024) loss_scale_kernel(const void* targets, i
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
     __syncthreads();
-    if (threadIdx.x) return;
-    s = 0.0;
-    for (int w = 0; w < 32; ++w) s += sums[w];
-    sh->weight = s;
-    sh->scale = !mean ? scale : s != 0.0 ? (float)((double)scale / s) : 0.0f;
-    sh->finished = 0u;
-    if (rows == 0) *total = 0.0f;
+    if (threadIdx.x == 0) {
+        s = 0.0;
+        for (int w = 0; w < 32; ++w) s += sums[w];
+        sh->weight = s;
+        sh->scale = !mean ? scale : s != 0.0 ? (float)((double)scale / s) : 0.0f;
+        sh->finished = 0u;
+        if (rows == 0) *total = 0.0f;
+    }
+    if (!alone) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // float32 sums to bf16 gradients.
@@ -255,7 +264,7 @@ int check_shape(const char* fn, int P, int64_t M, int64_t K, int64_t V, int64_t 
     s->P = P, s->M = M, s->K = K, s->V = V, s->vocab = vocab, s->Vp = V / P;
     // As many rows as the head of this file allows, in pieces of about the same size;
     // whole row tiles, so that only the last piece ends inside one.
-    const int64_t most = piece_rows ? up(piece_rows, LIN_TILE_ROWS) : up(std::max<int64_t>(2 * K, 2048), LIN_TILE_ROWS);
+    const int64_t most = up(piece_rows ? piece_rows : std::max({2 * K, (int64_t)2048, ((int64_t)1 << 29) / V}), LIN_TILE_ROWS);
     s->pieces = train && M > most ? (int)((M + most - 1) / most) : 1;
     s->piece = s->pieces > 1 ? up((M + s->pieces - 1) / s->pieces, LIN_TILE_ROWS) : M;
     if (s->pieces > 1) s->pieces = (int)((M + s->piece - 1) / s->piece);
@@ -264,7 +273,7 @@ int check_shape(const char* fn, int P, int64_t M, int64_t K, int64_t V, int64_t 
 
 // Where things are in a workspace; sum: float32 sums of dW.
 struct Space {
-    int64_t logit, stats, e, sum, bytes;
+    int64_t logit, factor, stats, x, e, sum, bytes;
 };
 Space space_of(const Shape& s, bool train, bool sum)
 {
@@ -273,8 +282,10 @@ Space space_of(const Shape& s, bool train, bool sum)
     const int64_t most = std::max(s.piece * parts(s, s.piece), last * parts(s, last));
     Space w;
     w.logit = SHARED_BYTES;
-    w.stats = w.logit + up(s.piece * 4, 256);
-    w.e = w.stats + up(most * 8, 256);
+    w.factor = w.logit + up(s.piece * 4, 256);
+    w.stats = w.factor + (train ? up(s.piece * 4, 256) : 0);
+    w.x = w.stats + up(most * 8, 256);
+    w.e = w.x + (train ? up(s.piece * s.K * 2, 256) : 0);
     w.sum = w.e + (train ? up(s.piece * s.V * 2, 256) : 0);
     w.bytes = w.sum + (sum ? s.K * s.V * 4 : 0);
     return w;
@@ -326,7 +337,7 @@ const void* rows_of(const void* p, int64_t first, int64_t row_bytes)
 }
 
 // The product with its statistics for `rows` rows from `first`, and the rows' arguments.
-int softmax_product(const Call& c, LinEpi epi, int64_t first, int64_t rows, RowsArgs* a, cudaStream_t stream)
+int softmax_product(const Call& c, LinEpi epi, const float* weights, int64_t first, int64_t rows, RowsArgs* a, cudaStream_t stream)
 {
     LinGemm g;
     g.epi = epi;
@@ -348,8 +359,9 @@ int softmax_product(const Call& c, LinEpi epi, int64_t first, int64_t rows, Rows
     g.softmax.targets = rows_of(c.targets, first, c.targets64 ? 8 : 4);
     g.softmax.targets64 = c.targets64;
     g.softmax.vocab = c.s.vocab;
+    g.softmax.ignore = c.ignore;
+    g.softmax.weights = weights ? weights + first : nullptr;
     a->softmax = softmax_args(g.softmax, (int)parts(c.s, rows));
-    a->ignore = c.ignore;
     a->P = c.s.P;
     a->cols = (int)c.s.Vp;
     a->part_cols = part_cols(rows);
@@ -364,7 +376,7 @@ int forward_impl(Call& c, int targets64, int64_t workspace_bytes, float* loss, f
     TRY(check_ptr(c.fn, "lse", lse, 4, false));
     if (c.s.M == 0) return RTP_OK;
     RowsArgs a = {};
-    TRY(softmax_product(c, LIN_LSE, 0, c.s.M, &a, stream));
+    TRY(softmax_product(c, LIN_LSE, nullptr, 0, c.s.M, &a, stream));
     a.loss = loss;
     a.lse = lse;
     return launch(c.fn, loss_rows_kernel<false>, dim3((unsigned)c.s.M), THREADS, stream, a);
@@ -392,8 +404,12 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
     if (device_sms(&sms)) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
     const int64_t dx_size = dx_dtype == RTP_F32 ? 4 : 2, dw_size = dw_dtype == RTP_F32 ? 4 : 2;
     Shared* sh = reinterpret_cast<Shared*>(c.ws);
-    TRY(launch(fn, loss_scale_kernel, dim3(1), 1024, stream, c.targets, c.targets64, weights, s.M, c.ignore, mean, scale, sh, total));
+    auto set_scale = [&] {
+        return launch(fn, loss_scale_kernel, dim3(1), 1024, stream, c.targets, c.targets64, weights, s.M, c.ignore, mean, scale, sh,
+                      total, some ? 0 : 1);
+    };
     if (!some) {
+        TRY(set_scale());
         for (int i = 0; dW && !accumulate && i < s.P; ++i)
             if (cudaMemsetAsync(dW[i], 0, (size_t)(s.K * s.Vp * dw_size), stream) != cudaSuccess)
                 return fail(RTP_ECUDA, "%s: cudaMemsetAsync failed", fn);
@@ -402,8 +418,12 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
     for (int p = 0; p < s.pieces; ++p) {
         const int64_t first = p * s.piece, rows = std::min(s.piece, s.M - first);
         RowsArgs a = {};
-        TRY(softmax_product(c, LIN_EXP, first, rows, &a, stream));
-        a.weights = weights ? weights + first : nullptr;
+        TRY(softmax_product(c, LIN_EXP, weights, first, rows, &a, stream));
+        if (p == 0) TRY(set_scale());
+        a.x = static_cast<const uint4*>(rows_of(c.X, first, s.K * 2));
+        a.scaled = reinterpret_cast<uint4*>(c.ws + c.space.x);
+        a.x_vectors = (int)(s.K / 8);
+        a.factor = reinterpret_cast<float*>(c.ws + c.space.factor);
         a.loss = loss + first;
         a.shared = sh;
         a.mean = mean;
@@ -411,14 +431,9 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
             a.total = total;
             a.all_loss = loss;
             a.all_weights = weights;
-            a.all_targets = c.targets;
             a.all_rows = s.M;
         }
-        // Blocks that share a row, where the rows alone would not fill the GPU: each with
-        // at least 2 vectors of a rank's columns for every thread.
-        unsigned split = 1;
-        while (rows * split < 2 * sms && split < 16 && s.Vp / 8 >= 2 * 2 * split * THREADS) split *= 2;
-        TRY(launch(fn, loss_rows_kernel<true>, dim3((unsigned)rows, split), THREADS, stream, a));
+        TRY(launch(fn, loss_rows_kernel<true>, dim3((unsigned)rows), THREADS, stream, a));
         if (dX) {
             LinGemm g;
             g.groups = s.P;
@@ -432,6 +447,7 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
                 g.A[i] = a.e[i];
                 g.B[i] = c.W[i];
             }
+            g.row_scale = a.factor;
             g.out[0] = static_cast<char*>(dX) + first * s.K * dx_size;
             TRY(launch_linear_gemm(fn, g, stream));
         }
@@ -446,7 +462,7 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
             g.cols = s.Vp;
             g.kdim = rows;
             for (int i = 0; i < s.P; ++i) {
-                g.A[i] = rows_of(c.X, first, s.K * 2);
+                g.A[i] = a.scaled;
                 g.B[i] = a.e[i];
                 g.out[i] = sums ? c.ws + c.space.sum + i * s.K * s.Vp * 4 : dW[i];
             }

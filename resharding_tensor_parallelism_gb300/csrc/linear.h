@@ -20,14 +20,18 @@ enum LinEpi : int {
 };
 
 // Softmax statistics (LIN_LSE, LIN_EXP): for a row and a part (the columns of one tile)
-// x = ref, y = sum over the part's columns j of 2^(l_j log2(e) - ref), ref = the part's
-// largest l_j log2(e); (-inf, 0) where a part has no column of the vocabulary.
+// x = ref, y = sum over the part's columns j of 2^(l_j log2(e) - ref). ref is 0, or,
+// where that sum is not in [2^-64, 2^64], the part's largest l_j log2(e); -inf with a sum
+// of 0. LIN_EXP writes the terms of the sums, in the rows that take part in gradients
+// (target other than `ignore`, weight other than 0), and 0 in the others.
 struct LinSoftmax {
     float2* stats = nullptr;        // [rows][groups * parts of a group]
     float* target_logit = nullptr;  // [rows]; not written where the target is in no column
     const void* targets = nullptr;  // [rows], int64 or int32: column counted over the groups
     int targets64 = 1;
     int64_t vocab = 0;              // columns from here on (counted over the groups) take no part
+    int64_t ignore = 0;
+    const float* weights = nullptr;  // [rows], or NULL: 1
 };
 
 // A [rows, kdim] times B [kdim, cols], bf16 row-major, float32 accumulation.
@@ -39,7 +43,8 @@ struct LinSoftmax {
 struct LinGemm {
     int groups = 1;
     bool fused = false, a_t = false, b_t = false, a_shared = false, out_f32 = false;
-    bool accumulate = false;  // gradients in float32: out += product
+    bool accumulate = false;           // gradients in float32: out += product
+    const float* row_scale = nullptr;  // b_t gradients: row r of the product times row_scale[r]
     LinEpi epi = LIN_OUT;
     int act = RTP_ACT_NONE;
     int64_t rows = 0, cols = 0, kdim = 0;

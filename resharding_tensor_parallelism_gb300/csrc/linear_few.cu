@@ -290,29 +290,33 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
 #pragma unroll 2
         for (int t = part * (THREADS / 32) + warp; t < a.rows; t += a.split * (THREADS / 32)) {
             const float4 w = sum4(t, f);
-            float v[4] = {w.x, w.y, w.z, w.w}, top = minus_infinity(), sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (f + j >= valid) v[j] = minus_infinity();
-                top = fmaxf(top, v[j]);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            top *= LOG2E;
-            const float ref = finite_ref(top);
+            float v[4] = {w.x, w.y, w.z, w.w}, e[4], ref = 0.0f, sum;
             const int target = target_in(a.softmax, t, first, valid) - f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                if (f + j >= valid) v[j] = minus_infinity();
                 if (target == j) a.softmax.target_logit[t] = v[j];
-                v[j] = exp2_fast(fmaf(v[j], LOG2E, -ref));
-                sum += v[j];
             }
+            auto terms = [&]() {
+                sum = 0.0f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0) a.softmax.stats[(int64_t)t * a.softmax.parts + tile] = make_float2(top, sum);
+                for (int j = 0; j < 4; ++j) sum += e[j] = exp2_fast(fmaf(v[j], LOG2E, -ref));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            };
+            terms();
+            if (valid > 0 && !in_range(sum)) {
+                float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                ref = finite_ref(top * LOG2E);
+                terms();
+            }
+            if (sum == 0.0f) ref = minus_infinity();
+            if (lane == 0) a.softmax.stats[(int64_t)t * a.softmax.parts + tile] = make_float2(ref, sum);
             if (EPI == LIN_EXP && f < cols)
                 store_bf16x4(static_cast<__nv_bfloat16*>(a.out[g]) + (int64_t)t * a.cols + f0 + f,
-                             make_float4(v[0], v[1], v[2], v[3]));
+                             takes_part(a.softmax, t) ? make_float4(e[0], e[1], e[2], e[3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f));
         }
     }
     while (EPI != LIN_LSE && EPI != LIN_EXP && i0 < items) {

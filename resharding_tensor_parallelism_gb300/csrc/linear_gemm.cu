@@ -59,6 +59,7 @@ int launch_linear_gemm(const char* fn, const LinGemm& p, cudaStream_t stream)
     a.has_residual = p.residual[0] != nullptr;
     a.act = p.act;
     a.accumulate = p.accumulate;
+    a.row_scale = p.row_scale;
     a.ld = p.cols;
     a.groups = p.groups;
     a.fused = p.fused;

@@ -6,10 +6,9 @@
 //   LIN_GLU    y = act(X Ag) * (X Au): both projections and their product in one
 //              kernel, and optionally the two pre-activations
 //   LIN_DGLU   acc = dY = dZ B^T: dHg = dY * Hu * act'(Hg), dHu = dY * act(Hg)
-//   LIN_LSE    acc = logits: of each row's 256 columns the largest and the sum of the
-//              exponentials relative to it, and the logit of the row's target
-//   LIN_EXP    the same, and the exponentials in bf16 (two passes over the tensor memory:
-//              they are relative to the largest one of the whole tile)
+//   LIN_LSE    acc = logits: of each row's 256 columns the sum of the exponentials, and
+//              the logit of the row's target (softmax.cuh)
+//   LIN_EXP    the same, and the exponentials in bf16
 //
 // The tensor pipe bounds them: 2 rows cols kdim operations. A cluster of 2 CTAs
 // (2 SMs) computes one 256 x 256 accumulator tile per step, as in the plain
@@ -61,7 +60,8 @@ struct LinArgs {
     int32_t act, has_bias, has_residual, keep;
     int32_t kbs;    // K blocks of a tile (of all operand pairs when fused)
     int32_t split;  // SPLIT kernels: K parts of a tile, over a cluster of `split` pairs
-    int32_t accumulate;  // float32 gradients are added to what is there
+    int32_t accumulate;      // float32 gradients are added to what is there
+    const float* row_scale;  // CFG_B_T gradients: of each row, or NULL
     SoftmaxArgs softmax;
 };
 
@@ -409,11 +409,18 @@ __global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_ke
                     bias = __ldg(reinterpret_cast<const uint4*>(a.bias[g] + tile_col + at));
             }
             int valid = 0, target = -1;  // columns of the tile in the vocabulary; the row's target among them
+            uint32_t live = 0u;          // all bits: the row has a part in the gradients
             if constexpr (SOFTMAX) {
                 const int64_t first_col = (int64_t)g * a.cols + tile_col;
                 valid = min(valid_columns(a.softmax, first_col, TILE_COLS), a.cols - tile_col);
-                if (row < a.rows) target = target_in(a.softmax, row, first_col, valid);
+                if (row < a.rows) {
+                    target = target_in(a.softmax, row, first_col, valid);
+                    if (EPI == LIN_EXP && takes_part(a.softmax, row)) live = ~0u;
+                }
             }
+            float row_scale = 1.0f;
+            if constexpr (PLAIN && B_T)
+                if (a.row_scale && row < a.rows) row_scale = __ldcg(a.row_scale + row);
             int ok = 1;
             if (lane == 0) ok = wait_bar(acc_full(acc), acc_phase, abort_flag, ERR_EPILOGUE) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -565,7 +572,6 @@ __global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_ke
             }
             if constexpr (SOFTMAX) {
                 // logits of step c, -inf outside the vocabulary; the next step's are on their way
-                float top = minus_infinity(), sum = 0.0f, logit = 0.0f;
                 auto logits = [&](int c, float (&v)[STEP]) {
                     take(c, 0, ra, v);
                     if (c + 1 < steps) start(c + 1, 0, ra);
@@ -576,62 +582,56 @@ __global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_ke
                             if (col + j >= valid) v[j] = minus_infinity();
                     }
                 };
-                auto largest = [](const float (&v)[STEP]) {
-                    float m[4] = {v[0], v[1], v[2], v[3]};
+                // First relative to 0; once more relative to the largest logit where the sum
+                // shows that these exponentials are too large or too small to be kept.
+                float ref = 0.0f, sum = 0.0f, logit = 0.0f;
+                for (bool again = false; steps > 0; again = true) {
+                    sum = 0.0f;
+                    start(0, 0, ra);
+#pragma unroll 1
+                    for (int c = 0; c < steps; ++c) {
+                        float v[STEP], part[4] = {};
+                        logits(c, v);
+                        const int at = target - column(c);
+                        if (__any_sync(0xffffffffu, at >= 0 && at < STEP)) {
 #pragma unroll
-                    for (int j = 4; j < STEP; ++j) m[j & 3] = fmaxf(m[j & 3], v[j]);
-                    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-                };
-                auto find_target = [&](int c, const float (&v)[STEP]) {
-                    const int at = target - column(c);
-                    if (__any_sync(0xffffffffu, at >= 0 && at < STEP)) {
+                            for (int j = 0; j < STEP; ++j)
+                                if (at == j) logit = v[j];
+                        }
 #pragma unroll
-                        for (int j = 0; j < STEP; ++j)
-                            if (at == j) logit = v[j];
+                        for (int j = 0; j < STEP; ++j) {
+                            v[j] = exp2_fast(fmaf(v[j], LOG2E, -ref));
+                            part[j & 3] += v[j];
+                        }
+                        sum += (part[0] + part[1]) + (part[2] + part[3]);
+                        if constexpr (EPI == LIN_EXP) {
+                            const uint32_t s = slot + (uint32_t)c;
+                            acquire();
+#pragma unroll
+                            for (int q = 0; q < STEP / 8; ++q)
+                                st_shared_v4(unit(s, q), bf16x2(v[8 * q], v[8 * q + 1]) & live, bf16x2(v[8 * q + 2], v[8 * q + 3]) & live,
+                                             bf16x2(v[8 * q + 4], v[8 * q + 5]) & live, bf16x2(v[8 * q + 6], v[8 * q + 7]) & live);
+                            flush();
+                            store(&a.to[g], s, tile_col + chunk_at(c));
+                        }
                     }
-                };
-                // v becomes its exponentials, relative to ref; returns their sum
-                auto exponentials = [](float (&v)[STEP], float ref) {
-                    float s[4] = {};
-#pragma unroll
-                    for (int j = 0; j < STEP; ++j) {
-                        v[j] = exp2_fast(fmaf(v[j], LOG2E, -ref));
-                        s[j & 3] += v[j];
-                    }
-                    return (s[0] + s[1]) + (s[2] + s[3]);
-                };
-                if constexpr (EPI == LIN_EXP) {
-                    if (steps > 0) start(0, 0, ra);
+                    const bool far = valid > 0 && !in_range(sum);
+                    if (again || !__any_sync(0xffffffffu, far)) break;
+                    float top = minus_infinity();
+                    start(0, 0, ra);
 #pragma unroll 1
                     for (int c = 0; c < steps; ++c) {
                         float v[STEP];
                         logits(c, v);
-                        top = fmaxf(top, largest(v));
+#pragma unroll
+                        for (int j = 0; j < STEP; ++j) top = fmaxf(top, v[j]);
                     }
-                    top *= LOG2E;
-                }
-                const float ref = finite_ref(top);
-                if (steps > 0) start(0, 0, ra);
-#pragma unroll 1
-                for (int c = 0; c < steps; ++c) {
-                    const uint32_t s = slot + (uint32_t)c;
-                    float v[STEP];
-                    logits(c, v);
-                    find_target(c, v);
-                    if constexpr (EPI == LIN_EXP) {
-                        sum += exponentials(v, ref);
-                        acquire();
-                        put_bf16(s, c, v);
-                        flush();
-                        store(&a.to[g], s, tile_col + chunk_at(c));
-                    } else {
-                        const float now = fmaxf(top, largest(v) * LOG2E), r = finite_ref(now);
-                        sum = sum * exp2_fast(top - r) + exponentials(v, r);
-                        top = now;
-                    }
+                    if (far) ref = finite_ref(top * LOG2E);
+                    if (lane == 0) bulk_wait_all();  // what is stored is stored again
+                    __syncwarp();
                 }
                 if (row < a.rows && steps > 0) {
-                    a.softmax.stats[row * a.softmax.parts + g * a.n_tiles + nt] = make_float2(top, sum);
+                    a.softmax.stats[row * a.softmax.parts + g * a.n_tiles + nt] = make_float2(sum == 0.0f ? minus_infinity() : ref, sum);
                     if (target >= 0) a.softmax.target_logit[row] = logit;
                 }
             } else if constexpr (EPI == LIN_OUT) {
@@ -645,6 +645,12 @@ __global__ void __launch_bounds__(Layout<CFG, SPLIT>::threads, 1) linear_gemm_ke
                     if (c % PER == 0) {
                         if (!has_in) acquire();  // else the slots were free when the operands were fetched
                         else if (!(good = wait_in(s))) break;
+                    }
+                    if constexpr (PLAIN && B_T) {
+                        if (a.row_scale) {
+#pragma unroll
+                            for (int j = 0; j < STEP; ++j) v[j] *= row_scale;
+                        }
                     }
                     if constexpr (!PLAIN) {
                         if (has_bias) {

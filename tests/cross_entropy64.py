@@ -42,12 +42,15 @@ def gradients(X, W, targets, vocab, ignore, weights=None, mean=True, scale=1.0):
     d = p.clone()
     rows = torch.nonzero(counted & (targets >= 0) & (targets < vocab))[:, 0]
     d[rows, targets.long()[rows]] -= g[rows]
-    # an exponential is rounded to bf16, times a factor that is off by the row's error, and d is rounded once more
-    err = BF16 * (p.abs() + d.abs()) * 1.01 + p.abs() * lse_bound(X, W, vocab, lse, logits)[:, None] * 2
+    # Both products read d's exponentials (at the target: less the row's sum) rounded to bf16, half a step of d itself; dW
+    # reads rows of X that were multiplied by a factor and rounded, half a step more of every term. The exponentials and
+    # the factor are off by the row's error (each once).
+    row = p.abs() * lse_bound(X, W, vocab, lse, logits)[:, None] * 2
+    ex, ew = BF16 * d.abs() * 1.01 + row, 2 * BF16 * d.abs() * 1.01 + row
     pad = W.shape[1] - vocab
-    d, err = (torch.nn.functional.pad(t, (0, pad)) for t in (d, err))
+    d, ex, ew = (torch.nn.functional.pad(t, (0, pad)) for t in (d, ex, ew))
     Xd, Wd = X.double(), W.double()
     dX, dW = d @ Wd.t(), Xd.t() @ d
-    bx = err @ Wd.abs().t() + 1.2 * W.shape[1] * EPS * (d.abs() @ Wd.abs().t())
-    bw = Xd.abs().t() @ err + 1.2 * X.shape[0] * EPS * (Xd.abs().t() @ d.abs())
+    bx = ex @ Wd.abs().t() + 1.2 * W.shape[1] * EPS * (d.abs() @ Wd.abs().t())
+    bw = Xd.abs().t() @ ew + 1.2 * X.shape[0] * EPS * (Xd.abs().t() @ d.abs())
     return total, loss, dX, dW, bx, bw

@@ -112,9 +112,9 @@ def test_pieces_of_rows(M, piece, P, dtype):
 
 
 def test_pieces_by_default():
-    """2048 rows a piece for a narrow model."""
-    X, W, shards, t = _inputs(2304, 64, 512, 2, 512, seed=4)
-    _check_train(X, W, t, 512, rtp.tp_cross_entropy_train(X, shards, t, ignore_index=IGNORE))
+    """2048 rows a piece for a narrow model with a vocabulary of which they take 1 GiB."""
+    X, W, shards, t = _inputs(2304, 64, 262144, 2, 262144, seed=4)
+    _check_train(X, W, t, 262144, rtp.tp_cross_entropy_train(X, shards, t, ignore_index=IGNORE))
 
 
 @pytest.mark.parametrize("M,piece", [(100, 0), (300, 0), (600, 256)])
@@ -134,8 +134,7 @@ def test_nothing_to_learn_from(M):
     X[1] = float("nan")
     total, loss, dX, dW = rtp.tp_cross_entropy_train(X, shards, t, ignore_index=IGNORE)
     assert float(total) == 0 and not loss.any() and not dX.any()
-    X[1] = 0
-    assert not any(d.any() for d in rtp.tp_cross_entropy_train(X, shards, t, ignore_index=IGNORE)[3])
+    assert not any(d.any() for d in dW)
 
 
 @pytest.mark.parametrize("M", [4, 300])
@@ -148,8 +147,9 @@ def test_rows_without_a_part_hold_anything(M):
     want = rtp.tp_cross_entropy_train(X, shards, t, weights=w, ignore_index=IGNORE)
     Y = X.clone()
     Y[0], Y[2] = float("nan"), float("inf")
-    total, loss, dX, _ = rtp.tp_cross_entropy_train(Y, shards, t, weights=w, ignore_index=IGNORE)
+    total, loss, dX, dW = rtp.tp_cross_entropy_train(Y, shards, t, weights=w, ignore_index=IGNORE)
     assert torch.equal(total, want[0]) and not dX[0].any() and not dX[2].any() and float(loss[0]) == 0
+    assert all(torch.equal(a, b) for a, b in zip(dW, want[3]))
     keep = [i for i in range(M) if i not in (0, 2)]
     assert torch.equal(loss[keep], want[1][keep]) and torch.equal(dX[keep], want[2][keep])
 
@@ -167,9 +167,19 @@ def test_targets_outside_the_vocabulary_show(M):
 
 
 @pytest.mark.parametrize("M", [3, 260])
-def test_far_logits(M):
-    """Logits of some thousands: far beyond what an exponential holds, in tiles that differ by more than that."""
-    X, W, shards, t = _inputs(M, 64, 1024, 2, 1020, spread=1000.0, seed=7)
+@pytest.mark.parametrize("how", ["all", "some rows", "one rank", "all low", "one rank low"])
+def test_far_logits(M, how):
+    """Logits of some thousands: far beyond what an exponential holds, in tiles that differ by more than that; in some rows
+    only, in one rank's tiles only, and far below zero, beside ordinary ones or not."""
+    X, W, shards, t = _inputs(M, 64, 1024, 2, 1020, spread=1000.0 if how == "all" else 1.0, seed=7)
+    if how == "some rows":
+        X[::3] *= 300
+    if how == "one rank":
+        W[:, 600:] *= 200
+    if how.endswith("low"):
+        X[:, 0] = 16.0
+        W[0, 512 if how.startswith("one") else 0:] = -20.0
+    shards = [w.contiguous() for w in W.chunk(2, 1)]
     loss, lse = rtp.tp_cross_entropy(X, shards, t, vocab=1020, ignore_index=IGNORE)
     _check_forward(X, W, t, 1020, loss, lse)
     _check_train(X, W, t, 1020, rtp.tp_cross_entropy_train(X, shards, t, vocab=1020, ignore_index=IGNORE))
