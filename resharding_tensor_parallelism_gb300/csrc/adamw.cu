@@ -215,121 +215,210 @@ __device__ __forceinline__ float sqrt_fast(float x)
     return r;
 }
 
-// Rows of a thread in flight: ROWS; a chunk is what a block takes at once.
-template <int ROWS>
-constexpr int CHUNK = ROWS * WARPS * ROW;
+// What a step has read from the device, and its launch's arguments.
+struct Rates {
+    float beta1, beta2, rest1, rest2, correct2, lr, rate, clip, eps;
+    uint32_t seed, step;
+};
 
-template <bool BITS8, int ROWS, int N>
-__global__ void __launch_bounds__(THREADS, 2) adamw_kernel(const __grid_constant__ Table<N> t, const __grid_constant__ Step s)
+// One row of any types, alignment and length.
+template <bool BITS8>
+__device__ __noinline__ void any_row(const Item& it, int64_t row, const Rates& s)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const float beta1 = s.clock->keep1, beta2 = s.clock->keep2, rest1 = s.clock->rest1, rest2 = s.clock->rest2;
-    const float correct2 = s.clock->correct2, lr = s.lr_at ? __ldcg(s.lr_at) : s.lr, rate = lr * s.clock->correct1;
-    const uint32_t step = (uint32_t)(s.clock->step + 1);
-    float clip = 1.0f;
-    if (s.norm) {
-        clip = s.max_norm / (__ldcg(s.norm) + 1e-6f);
-        if (clip > 1.0f) clip = 1.0f;  // a NaN stays one
-    }
-    int item = 0;
-    for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-        for (int half = N / 2; half > 0; half /= 2)
-            if (item + half < t.n && t.items[item + half].chunk0 <= c) item += half;
-        const Item& it = t.items[item];
-        const bool pb = it.param_bf16, gb = it.grad_bf16, vec = it.vectors;
-        const int64_t e0 = (int64_t)(c - it.chunk0) * CHUNK<ROWS> + warp * ROW;  // row i: WARPS * ROW further on
-        Raw p[ROWS], g[ROWS], m[ROWS], v[ROWS];
-        uchar2 scales[ROWS];
+    const int lane = threadIdx.x & 31;
+    const bool pb = it.param_bf16, gb = it.grad_bf16, vec = it.vectors;
+    const int64_t at = row + 4 * lane;
+    const int n = (int)min((int64_t)4, it.numel - at);
+    const uint32_t key = pcg(pcg(pcg(s.seed) + it.id) + s.step);
+    const float keep = 1.0f - s.lr * it.decay;
+    float x[4], dx[4], m[4], v[4];
+    floats(it.master ? load4(it.master, false, at, n, vec) : load4(it.param, pb, at, n, vec), pb && !it.master, x);
+    floats(load4(it.grad, gb, at, n, vec), gb, dx);
+    if constexpr (BITS8) {
+        const uint32_t mw = load_codes(it.m, at, n, vec), vw = load_codes(it.v, at, n, vec);
+        const uchar2 scales = __ldcs(it.scales + row / ROW);
+        const float ms = block_scale(scales.x, 134), vs = block_scale(scales.y, 142);
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            const int64_t row = e0 + i * (WARPS * ROW), at = row + 4 * lane;
-            const int n = (int)min((int64_t)4, it.numel - at);
-            p[i] = it.master ? load4(it.master, false, at, n, vec) : load4(it.param, pb, at, n, vec);
-            g[i] = load4(it.grad, gb, at, n, vec);
-            if constexpr (BITS8) {
-                m[i].w.x = load_codes(it.m, at, n, vec);
-                v[i].w.x = load_codes(it.v, at, n, vec);
-                scales[i] = row < it.numel ? __ldcs(it.scales + row / ROW) : make_uchar2(0, 0);
-            } else {
-                m[i] = load4(it.m, false, at, n, vec);
-                v[i] = load4(it.v, false, at, n, vec);
-            }
+        for (int j = 0; j < 4; ++j) {
+            m[j] = decode_m(mw >> 8 * j & 255u, ms);
+            v[j] = decode_v(vw >> 8 * j & 255u, vs);
         }
-        const uint32_t key = pcg(pcg(pcg(s.seed) + it.id) + step);
-        const float keep = 1.0f - lr * it.decay;
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            const int64_t row = e0 + i * (WARPS * ROW), at = row + 4 * lane;
-            if (row >= it.numel) break;  // the warp's
-            const int n = (int)min((int64_t)4, it.numel - at);
-            float x[4], dx[4], m1[4], v1[4];
-            floats(p[i], pb && !it.master, x);
-            floats(g[i], gb, dx);
-            if constexpr (BITS8) {
-                const float ms = block_scale(scales[i].x, 134), vs = block_scale(scales[i].y, 142);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    m1[j] = decode_m(m[i].w.x >> 8 * j & 255u, ms);
-                    v1[j] = decode_v(v[i].w.x >> 8 * j & 255u, vs);
-                }
-            } else {
-                floats(m[i], false, m1);
-                floats(v[i], false, v1);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float d = dx[j] * clip;
-                m1[j] = fmaf(beta1, m1[j], rest1 * d);
-                v1[j] = fmaf(beta2, v1[j], rest2 * d * d);
-                x[j] = fmaf(x[j], keep, -rate * __fdividef(m1[j], sqrt_fast(v1[j] * correct2) + s.eps));
-            }
-            uint32_t noise[4];
-            if (BITS8 || (pb && !it.master)) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) noise[j] = pcg((uint32_t)at + (uint32_t)j + key);
-            }
-            if (it.master) store_f32(it.master, at, n, vec, x);
-            if (!pb) {
-                store_f32(it.param, at, n, vec, x);
-            } else {
-                uint32_t b[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = it.master ? round_bf16(x[j]) : round_bf16_at_random(x[j], pcg(noise[j]) & 0xFFFFu);
-                store_16(it.param, at, n, vec, b);
-            }
-            if constexpr (BITS8) {
-                uint32_t mt = 0u, vt = 0u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {  // elements behind the end count as 0
-                    mt = max(mt, j < n ? __float_as_uint(fabsf(m1[j])) : 0u);
-                    vt = max(vt, j < n ? __float_as_uint(fabsf(v1[j])) : 0u);
-                }
-                const int me = max((int)(__reduce_max_sync(0xffffffffu, mt) >> 23), LEAST_EXPONENT);
-                const int ve = max((int)(__reduce_max_sync(0xffffffffu, vt) >> 23), LEAST_EXPONENT);
-                const float ms = power_of_two(261 - me), vs = power_of_two(269 - ve);  // 2^(134 - E), 2^(142 - E)
-                uint32_t mc = 0u, vc = 0u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t a = encode<7>(fabsf(m1[j]) * ms, (noise[j] & 0xFFFFu) << 4 | 8u) & 127u;
-                    const uint32_t b = max(encode<15>(v1[j] * vs, noise[j] >> 16 << 4 | 8u) & 255u, v1[j] > 0.0f ? 1u : 0u);
-                    mc |= (a | (__float_as_uint(m1[j]) >> 31 << 7)) << 8 * j;
-                    vc |= b << 8 * j;
-                }
-                store_codes(it.m, at, n, vec, mc);
-                store_codes(it.v, at, n, vec, vc);
-                if (lane == 0) it.scales[row / ROW] = make_uchar2((unsigned char)me, (unsigned char)ve);
-            } else {
-                store_f32(it.m, at, n, vec, m1);
-                store_f32(it.v, at, n, vec, v1);
-            }
-        }
+        __syncwarp();  // the block's exponents have been read
+    } else {
+        floats(load4(it.m, false, at, n, vec), false, m);
+        floats(load4(it.v, false, at, n, vec), false, v);
     }
-    if (!s.last) return;
+    uint32_t noise[4], b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float d = dx[j] * s.clip;
+        m[j] = fmaf(s.beta1, m[j], s.rest1 * d);
+        v[j] = fmaf(s.beta2, v[j], s.rest2 * d * d);
+        x[j] = fmaf(x[j], keep, -s.rate * __fdividef(m[j], sqrt_fast(v[j] * s.correct2) + s.eps));
+        noise[j] = pcg((uint32_t)at + (uint32_t)j + key);
+        b[j] = it.master ? round_bf16(x[j]) : round_bf16_at_random(x[j], pcg(noise[j]) & 0xFFFFu);
+    }
+    if (it.master) store_f32(it.master, at, n, vec, x);
+    if (pb) store_16(it.param, at, n, vec, b);
+    else store_f32(it.param, at, n, vec, x);
+    if constexpr (BITS8) {
+        uint32_t mt = 0u, vt = 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // elements behind the end count as 0
+            mt = max(mt, j < n ? __float_as_uint(fabsf(m[j])) : 0u);
+            vt = max(vt, j < n ? __float_as_uint(fabsf(v[j])) : 0u);
+        }
+        const int me = max((int)(__reduce_max_sync(0xffffffffu, mt) >> 23), LEAST_EXPONENT);
+        const int ve = max((int)(__reduce_max_sync(0xffffffffu, vt) >> 23), LEAST_EXPONENT);
+        const float ms = power_of_two(261 - me), vs = power_of_two(269 - ve);  // 2^(134 - E), 2^(142 - E)
+        uint32_t mc = 0u, vc = 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t a = encode<7>(fabsf(m[j]) * ms, (noise[j] & 0xFFFFu) << 4 | 8u) & 127u;
+            const uint32_t c = max(encode<15>(v[j] * vs, noise[j] >> 16 << 4 | 8u) & 255u, v[j] > 0.0f ? 1u : 0u);
+            mc |= (a | (__float_as_uint(m[j]) >> 31 << 7)) << 8 * j;
+            vc |= c << 8 * j;
+        }
+        store_codes(it.m, at, n, vec, mc);
+        store_codes(it.v, at, n, vec, vc);
+        if (lane == 0) it.scales[row / ROW] = make_uchar2((unsigned char)me, (unsigned char)ve);
+    } else {
+        store_f32(it.m, at, n, vec, m);
+        store_f32(it.v, at, n, vec, v);
+    }
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float sqrt_ftz(float x)
+{
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Whole, aligned rows of 8-bit moments: the row's update in as few instructions as the
+// format allows (in the form of any_row, 200 an element, the arithmetic took 2.3 times as
+// long as the memory). A code shifted to the bits that a float32's exponent and mantissa
+// end in, subnormal ones too, is the value it stands for times a power of two, which goes
+// into beta's factor; a value times a power of two has its code in those bits, with the
+// lost part below. Both hold for block exponents that such powers of two fit; other
+// rows (and NaN) return false with nothing written. The denominator is formed times 2^32,
+// so that no v but 0 counts as zero.
+constexpr int MOST_M = 140, MOST_V = 156;
+template <bool PB, bool MASTER, bool GB>
+__device__ __forceinline__ bool row_of_8_bits(const Item& it, int64_t at, const Raw& p, const Raw& g, uint32_t mw, uint32_t vw,
+                                              uchar2 scales, const Rates& s, float keep, uint32_t key)
+{
+    const int em = max((int)scales.x, LEAST_EXPONENT), ev = max((int)scales.y, LEAST_EXPONENT);
+    if (em > MOST_M || ev > MOST_V) return false;
+    const float fm = s.beta1 * power_of_two(em - 14 + 127), fv = s.beta2 * power_of_two(ev - 30 + 127);
+    const float root = s.correct2 * 0x1p64f, eps = s.eps * 0x1p32f, rate = s.rate * -0x1p32f;
+    float x[4], dx[4], m[4], v[4];
+    floats(p, PB && !MASTER, x);
+    floats(g, GB, dx);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float d = dx[j] * s.clip;
+        const float mo = __int_as_float((int)(mw << (24 - 8 * j)) >> 4 & (int)0x87F00000);
+        const float vo = __uint_as_float((j < 3 ? vw << (20 - 8 * j) : vw >> 4) & 0x0FF00000u);
+        m[j] = fmaf(mo, fm, s.rest1 * d);
+        v[j] = fmaf(vo, fv, s.rest2 * d * d);
+        x[j] = fmaf(x[j], keep, rate * m[j] * rcp_ftz(sqrt_ftz(v[j] * root) + eps));
+    }
+    const float mt = max_nan(max_nan(fabsf(m[0]), fabsf(m[1])), max_nan(fabsf(m[2]), fabsf(m[3])));
+    const float vt = max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3]));
+    // exponents where a float32 has them
+    constexpr uint32_t EXPONENT = 0x7F800000u, LEAST = (uint32_t)LEAST_EXPONENT << 23;
+    const uint32_t me = max(__reduce_max_sync(0xffffffffu, __float_as_uint(mt)) & EXPONENT, LEAST);
+    const uint32_t ve = max(__reduce_max_sync(0xffffffffu, __float_as_uint(vt)) & EXPONENT, LEAST);
+    if (me > (uint32_t)MOST_M << 23 || ve > (uint32_t)MOST_V << 23) return false;
+    const float sm = __uint_as_float(((14u + 127u) << 23) - me), sv = __uint_as_float(((30u + 127u) << 23) - ve);
+    const uint32_t x0 = ((uint32_t)at + key) * 747796405u + 2891336453u;
+    uint32_t mc[4], vc[4], b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t h = x0 + (uint32_t)j * 747796405u;
+        const uint32_t w = ((h >> ((h >> 28) + 4u)) ^ h) * 277803737u, noise = (w >> 22) ^ w;
+        // the random 16 bits, and half of the next one, 4 bits up as the codes
+        const uint32_t rm = __byte_perm(noise, 0x80u, 0x5104), rv = __byte_perm(noise, 0x80u, 0x5324);
+        // (A funnel shift: CUDA 13.0's assembler takes a plain shift of these bits, or 16 times them, for 0.)
+        mc[j] = (__funnelshift_l(0u, __float_as_uint(fabsf(m[j]) * sm), 4) + rm) | (__float_as_uint(m[j]) & 0x80000000u);
+        vc[j] = __funnelshift_l(0u, __float_as_uint(v[j] * sv), 4) + rv;
+        if (v[j] > 0.0f) vc[j] = max(vc[j], 1u << 24);
+        if (PB) b[j] = MASTER ? round_bf16(x[j]) : round_bf16_at_random(x[j], pcg(noise) & 0xFFFFu);
+    }
+    if (MASTER) store_f32(it.master, at, 4, true, x);
+    if (PB) store_16(it.param, at, 4, true, b);
+    else store_f32(it.param, at, 4, true, x);
+    auto top_bytes = [](const uint32_t (&c)[4]) { return __byte_perm(__byte_perm(c[0], c[1], 0x73), __byte_perm(c[2], c[3], 0x73), 0x5410); };
+    store_codes(it.m, at, 4, true, top_bytes(mc));
+    store_codes(it.v, at, 4, true, top_bytes(vc));
+    if ((threadIdx.x & 31) == 0) it.scales[at / ROW] = make_uchar2((unsigned char)(me >> 23), (unsigned char)(ve >> 23));
+    return true;
+}
+
+// The same for float32 moments.
+template <bool PB, bool MASTER, bool GB>
+__device__ __forceinline__ void row_of_32_bits(const Item& it, int64_t at, const Raw& p, const Raw& g, const Raw& mw, const Raw& vw,
+                                               const Rates& s, float keep, uint32_t key)
+{
+    float x[4], dx[4], m[4], v[4];
+    floats(p, PB && !MASTER, x);
+    floats(g, GB, dx);
+    floats(mw, false, m);
+    floats(vw, false, v);
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float d = dx[j] * s.clip;
+        m[j] = fmaf(s.beta1, m[j], s.rest1 * d);
+        v[j] = fmaf(s.beta2, v[j], s.rest2 * d * d);
+        x[j] = fmaf(x[j], keep, -s.rate * __fdividef(m[j], sqrt_fast(v[j] * s.correct2) + s.eps));
+        if (PB) b[j] = MASTER ? round_bf16(x[j]) : round_bf16_at_random(x[j], pcg(pcg((uint32_t)at + (uint32_t)j + key)) & 0xFFFFu);
+    }
+    if (MASTER) store_f32(it.master, at, 4, true, x);
+    if (PB) store_16(it.param, at, 4, true, b);
+    else store_f32(it.param, at, 4, true, x);
+    store_f32(it.m, at, 4, true, m);
+    store_f32(it.v, at, 4, true, v);
+}
+
+__device__ __forceinline__ Rates rates_of(const Step& a)
+{
+    const Clock& k = *a.clock;
+    Rates s;
+    s.beta1 = k.keep1, s.beta2 = k.keep2, s.rest1 = k.rest1, s.rest2 = k.rest2, s.correct2 = k.correct2;
+    s.lr = a.lr_at ? __ldcg(a.lr_at) : a.lr;
+    s.rate = s.lr * k.correct1;
+    s.step = (uint32_t)(k.step + 1);
+    s.clip = 1.0f;
+    if (a.norm) {
+        s.clip = a.max_norm / (__ldcg(a.norm) + 1e-6f);
+        if (s.clip > 1.0f) s.clip = 1.0f;  // a NaN stays one
+    }
+    s.eps = a.eps;
+    s.seed = a.seed;
+    return s;
+}
+
+// The last block to finish a step moves its clock on.
+__device__ __forceinline__ void advance(const Step& a)
+{
+    if (!a.last) return;
     __syncthreads();  // every thread has read the clock
-    if (threadIdx.x == 0 && atomicAdd(&s.clock->finished, 1u) == gridDim.x - 1) {
-        Clock& k = *s.clock;
+    if (threadIdx.x == 0 && atomicAdd(&a.clock->finished, 1u) == gridDim.x - 1) {
+        Clock& k = *a.clock;
         k.finished = 0u;
         k.step += 1;
         k.power1 *= k.beta1;
@@ -337,6 +426,170 @@ __global__ void __launch_bounds__(THREADS, 2) adamw_kernel(const __grid_constant
         k.correct1 = (float)(1.0 / (1.0 - k.power1));
         k.correct2 = (float)(1.0 / (1.0 - k.power2));
     }
+}
+
+// The item of chunk c, from one that begins no later on.
+template <int N>
+__device__ __forceinline__ int item_of(const Table<N>& t, uint32_t c, int item)
+{
+    for (int half = N / 2; half > 0; half /= 2)
+        if (item + half < t.n && t.items[item + half].chunk0 <= c) item += half;
+    return item;
+}
+
+// A tensor's types, known where the code is compiled: f is called with one of these.
+template <bool PB, bool MASTER, bool GB>
+struct Types {
+    static constexpr bool param_bf16 = PB, master = MASTER, grad_bf16 = GB;
+};
+template <class F>
+__device__ __forceinline__ void by_types(const Item& it, F&& f)
+{
+    if (!it.param_bf16) it.grad_bf16 ? f(Types<false, false, true>()) : f(Types<false, false, false>());
+    else if (it.master) it.grad_bf16 ? f(Types<true, true, true>()) : f(Types<true, true, false>());
+    else it.grad_bf16 ? f(Types<true, false, true>()) : f(Types<true, false, false>());
+}
+
+// ---- float32 moments: a warp's ROWS rows of a chunk at once, every load first ----
+
+constexpr int ROWS32 = 4, BLOCKS32 = 2;
+template <int ROWS>
+constexpr int CHUNK = ROWS * WARPS * ROW;
+
+template <int ROWS, bool PB, bool MASTER, bool GB>
+__device__ __forceinline__ void whole_rows(const Item& it, int64_t e0, const Rates& s)
+{
+    const uint32_t key = pcg(pcg(pcg(s.seed) + it.id) + s.step);
+    const float keep = 1.0f - s.lr * it.decay;
+    Raw p[ROWS], g[ROWS], m[ROWS], v[ROWS];
+    const int64_t at0 = e0 + 4 * (threadIdx.x & 31);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t at = at0 + i * (WARPS * ROW);
+        p[i] = load4(MASTER ? it.master : it.param, PB && !MASTER, at, 4, true);
+        g[i] = load4(it.grad, GB, at, 4, true);
+        m[i] = load4(it.m, false, at, 4, true);
+        v[i] = load4(it.v, false, at, 4, true);
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+        row_of_32_bits<PB, MASTER, GB>(it, at0 + i * (WARPS * ROW), p[i], g[i], m[i], v[i], s, keep, key);
+}
+
+template <int ROWS, int N>
+__global__ void __launch_bounds__(THREADS, BLOCKS32) adamw_kernel(const __grid_constant__ Table<N> t, const __grid_constant__ Step a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x >> 5;
+    const Rates s = rates_of(a);
+    int item = 0;
+    for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+        item = item_of(t, c, item);
+        const Item& it = t.items[item];
+        const int64_t first = (int64_t)(c - it.chunk0) * CHUNK<ROWS>, e0 = first + warp * ROW;  // row i: WARPS * ROW further on
+        if (it.vectors && first + CHUNK<ROWS> <= it.numel) {
+            by_types(it, [&](auto types) {
+                using T = decltype(types);
+                whole_rows<ROWS, T::param_bf16, T::master, T::grad_bf16>(it, e0, s);
+            });
+        } else {
+            for (int64_t row = e0; row < min(first + CHUNK<ROWS>, it.numel); row += WARPS * ROW) any_row<false>(it, row, s);
+        }
+    }
+    advance(a);
+}
+
+// ---- 8-bit moments ----
+// A warp takes strips of STRIP rows in turn, and the next strip's values come into shared
+// memory (cp.async) while it computes one: the arithmetic, 74 instructions an element,
+// leaves no registers for loads that far ahead, and without them a warp waited 2.7 us for
+// its rows (50 M elements: 188 us, issue slots 53 % busy). A lane copies and reads its own
+// elements only, so nothing is synchronised.
+
+constexpr int STRIP8 = 4, THREADS8 = 128, WARPS8 = THREADS8 / 32, BLOCKS8 = 5;
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* shared, const void* global)
+{
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(shared);
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(global) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(global), "n"(BYTES) : "memory");
+}
+// 4 elements of float32 or bf16
+__device__ __forceinline__ void copy_async4(void* shared, const void* global, bool bf16, int64_t at)
+{
+    if (bf16) copy_async<8>(shared, static_cast<const char*>(global) + 2 * at);
+    else copy_async<16>(shared, static_cast<const char*>(global) + 4 * at);
+}
+
+template <int STRIP, int N>
+__global__ void __launch_bounds__(THREADS8, BLOCKS8) adamw8_kernel(const __grid_constant__ Table<N> t, const __grid_constant__ Step a)
+{
+    __shared__ uint4 sp[2][STRIP][THREADS8], sg[2][STRIP][THREADS8];
+    __shared__ uint32_t sm[2][STRIP][THREADS8], sv[2][STRIP][THREADS8];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int me = (int)threadIdx.x, lane = me & 31;
+    const Rates s = rates_of(a);
+    struct Strip {
+        int item, rows;    // rows that are whole and aligned
+        int64_t e0;        // first element
+        uint32_t scales;   // lane i: the exponents of row i
+    };
+    auto fetch = [&](uint32_t c, int item, int buf) {
+        Strip n;
+        n.item = item_of(t, c, item);
+        const Item& it = t.items[n.item];
+        n.e0 = (int64_t)(c - it.chunk0) * (STRIP * ROW);
+        n.rows = it.vectors ? (int)min((it.numel - n.e0) / ROW, (int64_t)STRIP) : 0;
+        n.scales = 0u;
+        if (lane < n.rows) {
+            const uchar2 e = __ldcs(it.scales + n.e0 / ROW + lane);
+            n.scales = (uint32_t)e.x | (uint32_t)e.y << 8;
+        }
+#pragma unroll
+        for (int i = 0; i < STRIP; ++i) {
+            if (i >= n.rows) break;
+            const int64_t at = n.e0 + i * ROW + 4 * lane;
+            if (it.master) copy_async4(&sp[buf][i][me], it.master, false, at);
+            else copy_async4(&sp[buf][i][me], it.param, it.param_bf16, at);
+            copy_async4(&sg[buf][i][me], it.grad, it.grad_bf16, at);
+            copy_async<4>(&sm[buf][i][me], static_cast<const char*>(it.m) + at);
+            copy_async<4>(&sv[buf][i][me], static_cast<const char*>(it.v) + at);
+        }
+        return n;
+    };
+    const uint32_t stride = gridDim.x * WARPS8;
+    uint32_t c = blockIdx.x * WARPS8 + (uint32_t)(me >> 5);
+    int buf = 0;
+    Strip now = {0, 0, 0, 0u}, next = now;
+    if (c < t.chunks) now = fetch(c, 0, 0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    for (; c < t.chunks; c += stride) {
+        if (c + stride < t.chunks) next = fetch(c + stride, now.item, buf ^ 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const Item& it = t.items[now.item];
+        by_types(it, [&](auto types) {
+            using T = decltype(types);
+            const uint32_t key = pcg(pcg(pcg(s.seed) + it.id) + s.step);
+            const float keep = 1.0f - s.lr * it.decay;
+#pragma unroll 1
+            for (int i = 0; i < now.rows; ++i) {
+                const uint32_t e = __shfl_sync(0xffffffffu, now.scales, i);
+                const int64_t row = now.e0 + i * ROW;
+                if (!row_of_8_bits<T::param_bf16, T::master, T::grad_bf16>(it, row + 4 * lane, Raw{sp[buf][i][me]},
+                                                                           Raw{sg[buf][i][me]}, sm[buf][i][me], sv[buf][i][me],
+                                                                           make_uchar2(e & 255u, e >> 8), s, keep, key))
+                    any_row<true>(it, row, s);
+            }
+        });
+        for (int64_t row = now.e0 + now.rows * ROW; row < min(now.e0 + STRIP * ROW, it.numel); row += ROW) any_row<true>(it, row, s);
+        now = next;
+        buf ^= 1;
+    }
+    advance(a);
 }
 
 __global__ void adamw_clock_kernel(Clock* k, long long step, double beta1, double beta2)
@@ -356,42 +609,41 @@ __global__ void adamw_clock_kernel(Clock* k, long long step, double beta1, doubl
     k->finished = 0u;
 }
 
-// Values of 8-bit moments: 16 elements a thread, 8 threads a block of the format.
+// Values of 8-bit moments: 8 elements a thread, 16 threads a block of the format (16 a
+// thread left half of every sector to another store: 61 us for 50 M elements).
 template <bool F32>
-__global__ void __launch_bounds__(THREADS) adamw_values_kernel(const uint4* m8, const uint4* v8, const uchar2* scales, void* m,
+__global__ void __launch_bounds__(THREADS) adamw_values_kernel(const uint2* m8, const uint2* v8, const uchar2* scales, void* m,
                                                                void* v, int64_t units)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t stride = (int64_t)gridDim.x * THREADS;
+#pragma unroll 4
     for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < units; i += stride) {
-        const uchar2 sc = scales[i / (ROW / 16)];
+        const uchar2 sc = scales[i / (ROW / 8)];
         const float ms = block_scale(sc.x, 134), vs = block_scale(sc.y, 142);
-        const uint4 a = __ldcs(m8 + i), b = __ldcs(v8 + i);
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-        float x[16], y[16];
+        const uint2 a = __ldcs(m8 + i), b = __ldcs(v8 + i);
+        float x[8], y[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            x[j] = decode_m(aw[j / 4] >> 8 * (j % 4) & 255u, ms);
-            y[j] = decode_v(bw[j / 4] >> 8 * (j % 4) & 255u, vs);
+        for (int j = 0; j < 8; ++j) {
+            x[j] = decode_m((j < 4 ? a.x : a.y) >> 8 * (j % 4) & 255u, ms);
+            y[j] = decode_v((j < 4 ? b.x : b.y) >> 8 * (j % 4) & 255u, vs);
         }
         if constexpr (F32) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                static_cast<float4*>(m)[4 * i + q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-                static_cast<float4*>(v)[4 * i + q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+            for (int q = 0; q < 2; ++q) {
+                __stcs(static_cast<float4*>(m) + 2 * i + q, make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]));
+                __stcs(static_cast<float4*>(v) + 2 * i + q, make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]));
             }
         } else {
-            uint32_t p[8], q[8];
+            uint32_t p[4], q[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 p[j] = round_bf16(x[2 * j]) | round_bf16(x[2 * j + 1]) << 16;
                 q[j] = round_bf16(y[2 * j]) | round_bf16(y[2 * j + 1]) << 16;
             }
-            static_cast<uint4*>(m)[2 * i] = make_uint4(p[0], p[1], p[2], p[3]);
-            static_cast<uint4*>(m)[2 * i + 1] = make_uint4(p[4], p[5], p[6], p[7]);
-            static_cast<uint4*>(v)[2 * i] = make_uint4(q[0], q[1], q[2], q[3]);
-            static_cast<uint4*>(v)[2 * i + 1] = make_uint4(q[4], q[5], q[6], q[7]);
+            __stcs(static_cast<uint4*>(m) + i, make_uint4(p[0], p[1], p[2], p[3]));
+            __stcs(static_cast<uint4*>(v) + i, make_uint4(q[0], q[1], q[2], q[3]));
         }
     }
 }
@@ -414,10 +666,11 @@ int launch(const char* fn, void (*kernel)(A...), unsigned grid, int threads, cud
     return e == cudaSuccess ? RTP_OK : fail(RTP_ECUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
 }
 
-// Table by table, in chunks of ROWS rows a warp. The step's clock moves on with the last
+// Table by table, in chunks of `chunk` elements. The step's clock moves on with the last
 // one, which runs (on one block) even when there is nothing to update.
-template <bool BITS8, int ROWS, int N>
-int run(const char* fn, std::vector<Item>& items, Step s, int blocks, cudaStream_t stream)
+template <int N>
+int run(const char* fn, std::vector<Item>& items, Step s, void (*kernel)(Table<N>, Step), int64_t chunk, int threads,
+        int chunks_of_block, int blocks, cudaStream_t stream)
 {
     static thread_local Table<N> t;
     size_t i = 0;
@@ -425,7 +678,7 @@ int run(const char* fn, std::vector<Item>& items, Step s, int blocks, cudaStream
         t.n = 0;
         uint64_t chunks = 0;
         for (; i < items.size() && t.n < N; ++i) {
-            const uint64_t add = ((uint64_t)items[i].numel + CHUNK<ROWS> - 1) / CHUNK<ROWS>;
+            const uint64_t add = ((uint64_t)items[i].numel + chunk - 1) / chunk;
             if (t.n > 0 && chunks + add > 0x7fffffffu) break;
             items[i].chunk0 = (uint32_t)chunks;
             t.items[t.n++] = items[i];
@@ -433,11 +686,28 @@ int run(const char* fn, std::vector<Item>& items, Step s, int blocks, cudaStream
         }
         t.chunks = (uint32_t)chunks;
         s.last = i >= items.size();
-        const unsigned grid = (unsigned)std::max<uint64_t>(1, std::min<uint64_t>(chunks, (uint64_t)blocks));
-        const int st = launch(fn, adamw_kernel<BITS8, ROWS, N>, grid, THREADS, stream, t, s);
+        const uint64_t wanted = (chunks + chunks_of_block - 1) / chunks_of_block;
+        const int st = launch(fn, kernel, (unsigned)std::max<uint64_t>(1, std::min<uint64_t>(wanted, (uint64_t)blocks)), threads,
+                              stream, t, s);
         if (st) return st;
     } while (i < items.size());
     return RTP_OK;
+}
+
+// One row a warp and chunk where more would leave warps without any.
+template <int N>
+int run_sized(const char* fn, std::vector<Item>& items, uint64_t elements, int bits, const Step& s, int sms, cudaStream_t stream)
+{
+    if (bits == 8) {
+        const int blocks = sms * BLOCKS8;
+        if (elements < (uint64_t)blocks * WARPS8 * STRIP8 * ROW)
+            return run<N>(fn, items, s, adamw8_kernel<1, N>, ROW, THREADS8, WARPS8, blocks, stream);
+        return run<N>(fn, items, s, adamw8_kernel<STRIP8, N>, STRIP8 * ROW, THREADS8, WARPS8, blocks, stream);
+    }
+    const int blocks = sms * BLOCKS32;
+    if (elements < (uint64_t)blocks * CHUNK<ROWS32>)
+        return run<N>(fn, items, s, adamw_kernel<1, N>, CHUNK<1>, THREADS, 1, blocks, stream);
+    return run<N>(fn, items, s, adamw_kernel<ROWS32, N>, CHUNK<ROWS32>, THREADS, 1, blocks, stream);
 }
 
 int step_impl(const char* fn, int n, const rtp_adamw_tensor* tensors, int bits, float lr, const float* lr_at, float eps,
@@ -459,7 +729,7 @@ int step_impl(const char* fn, int n, const rtp_adamw_tensor* tensors, int bits, 
         const rtp_adamw_tensor& w = tensors[i];
         if ((w.param_dtype != RTP_F32 && w.param_dtype != RTP_BF16) || (w.grad_dtype != RTP_F32 && w.grad_dtype != RTP_BF16))
             return fail(RTP_EINVAL, "%s: tensor %d is of an unknown type", fn, i);
-        if (w.numel < 0 || w.numel >= (int64_t)1 << 42) return fail(RTP_ESHAPE, "%s: tensor %d has %lld elements", fn, i, (long long)w.numel);
+        if (w.numel < 0 || w.numel >= (int64_t)1 << 39) return fail(RTP_ESHAPE, "%s: tensor %d has %lld elements", fn, i, (long long)w.numel);
         if (!(w.weight_decay >= 0.0f)) return fail(RTP_EINVAL, "%s: weight decay %g of tensor %d is not a number >= 0", fn, (double)w.weight_decay, i);
         if (w.numel == 0) continue;
         const bool pb = w.param_dtype == RTP_BF16, gb = w.grad_dtype == RTP_BF16;
@@ -486,15 +756,8 @@ int step_impl(const char* fn, int n, const rtp_adamw_tensor* tensors, int bits, 
     int sms = 0;
     if (device_sms(&sms)) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
     const Step s = {static_cast<Clock*>(clock), lr_at, norm, lr, max_norm, eps, seed, 0};
-    const int blocks = sms * 2;
-    const bool fine = elements < (uint64_t)blocks * CHUNK<4>;  // one row a warp spreads them over the GPU
-    auto go = [&](auto wide) {
-        constexpr bool B8 = decltype(wide)::value;
-        if (items.size() <= SMALL)
-            return fine ? run<B8, 1, SMALL>(fn, items, s, blocks, stream) : run<B8, 4, SMALL>(fn, items, s, blocks, stream);
-        return fine ? run<B8, 1, LARGE>(fn, items, s, blocks, stream) : run<B8, 4, LARGE>(fn, items, s, blocks, stream);
-    };
-    return bits == 8 ? go(std::true_type{}) : go(std::false_type{});
+    return items.size() <= SMALL ? run_sized<SMALL>(fn, items, elements, bits, s, sms, stream)
+                                 : run_sized<LARGE>(fn, items, elements, bits, s, sms, stream);
 }
 
 }  // namespace
@@ -537,11 +800,11 @@ int rtp_adamw_values(int64_t blocks, const uint8_t* exp_avg, const uint8_t* exp_
         return fail(RTP_EINVAL, "%s: a buffer is not 16-byte aligned", fn);
     int sms = 0;
     if (device_sms(&sms)) return fail(RTP_ECUDA, "%s: no CUDA device", fn);
-    const int64_t units = blocks * (ROW / 16);
+    const int64_t units = blocks * (ROW / 8);
     const unsigned grid = (unsigned)std::min<int64_t>((units + THREADS - 1) / THREADS, (int64_t)sms * 8);
     return launch(fn, dtype == RTP_F32 ? adamw_values_kernel<true> : adamw_values_kernel<false>, grid, THREADS,
-                  static_cast<cudaStream_t>(stream), reinterpret_cast<const uint4*>(exp_avg),
-                  reinterpret_cast<const uint4*>(exp_avg_sq), reinterpret_cast<const uchar2*>(scales), m, v, units);
+                  static_cast<cudaStream_t>(stream), reinterpret_cast<const uint2*>(exp_avg),
+                  reinterpret_cast<const uint2*>(exp_avg_sq), reinterpret_cast<const uchar2*>(scales), m, v, units);
 }
 
 }  // extern "C"
