@@ -664,8 +664,9 @@ def _tables():
         except ImportError as e:
             raise ImportError("_table.so is not built (%s); run `python -c \"import __graft_entry__ as g; g.build()\"`"
                               % e) from e
-        _table.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.rtp_tp_linear, _lib.rtp_tp_glu,
-                                                                          _lib.rtp_clip_grad_norm)])
+        _table.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+            _lib.rtp_tp_linear, _lib.rtp_tp_glu, _lib.rtp_clip_grad_norm, _lib.rtp_tp_cross_entropy,
+            _lib.rtp_tp_cross_entropy_train, _lib.rtp_tp_cross_entropy_workspace, _lib.rtp_adamw_step)])
         _ext = _table
     return _ext
 
@@ -980,6 +981,11 @@ def tp_cross_entropy(X, W_shards, targets, vocab: Optional[int] = None, ignore_i
     where the target is ignore_index, NaN where it is outside the vocabulary), and the logarithm of the sum of the
     exponentials, so that -loss is the log probability of the target."""
     fn = "tp_cross_entropy"
+    if loss is None and lse is None and stream is None and type(W_shards) is list and _on_gpu(X):
+        got = _called((_ext or _tables()).loss(X, W_shards, targets, -1 if vocab is None else max(0, int(vocab)),
+                                               int(ignore_index), _torch()._C._cuda_getDevice(), _stream_ptr(None) or 0))
+        if got is not None:
+            return got
     W = _listed(W_shards)
     P, M, K, V, vocab, device, wp, wide = _loss_arguments(fn, X, W, targets, vocab)
     f32 = _torch().float32
@@ -1009,6 +1015,13 @@ def tp_cross_entropy_train(X, W_shards, targets, weights=None, vocab: Optional[i
     W = _listed(W_shards)
     if reduction != "mean" and reduction != "sum":
         raise RtpError(-1, "%s: reduction %r is not 'mean' or 'sum'" % (fn, reduction))
+    if (dX is None and dW is None and loss is None and total is None and dx_dtype is None and dw_dtype is None and
+            not accumulate and not piece_rows and stream is None and type(W_shards) is list and _on_gpu(X)):
+        got = _called((_ext or _tables()).loss_train(
+            X, W, targets, weights, -1 if vocab is None else max(0, int(vocab)), int(ignore_index), reduction == "mean",
+            float(scale), _torch()._C._cuda_getDevice(), _stream_ptr(None) or 0))
+        if got is not None:
+            return got
     P, M, K, V, vocab, device, wp, wide = _loss_arguments(fn, X, W, targets, vocab)
     f32, bf16, shape = torch.float32, torch.bfloat16, (K, V // P)
     if accumulate and dW is None:
@@ -1312,6 +1325,7 @@ class AdamWGroup:
             if self.states == 8:
                 t.scales = self.scales.data_ptr() + at // ADAMW_BLOCK * 2
         self._numels = [p.numel() for p in self.params]
+        self._table_at, self._clock_at = ctypes.addressof(self._table), self._clock.data_ptr()
 
     def _begin(self, stream):
         torch = _torch()
@@ -1336,6 +1350,13 @@ class AdamWGroup:
         fn = "AdamWGroup.step"
         handle = self._begin(stream)
         grads = grads if type(grads) is list else list(grads)
+        lr = self.lr if lr is None else lr
+        if type(lr) is int:
+            lr = float(lr)
+        if _called((_ext or _tables()).adamw(self._table_at, len(self.params), self.params, self.masters, grads, self.states,
+                                             lr, self.eps, norm, float(max_norm), self.seed, self._clock_at, self._index,
+                                             handle or 0)):
+            return
         if len(grads) != len(self.params):
             raise RtpError(-1, "%s: %d gradients for %d tensors" % (fn, len(grads), len(self.params)))
         for i, (t, p, m, g) in enumerate(zip(self._table, self.params, self.masters, grads)):
@@ -1349,7 +1370,6 @@ class AdamWGroup:
                 self._check(fn, "masters", i, m, p)
                 t.master = m.data_ptr() or None
             t.grad, t.grad_dtype = g.data_ptr() or None, _dtype_code(g)
-        lr = self.lr if lr is None else lr
         at = None
         if isinstance(lr, _torch().Tensor):
             at, lr = self._scalar("lr", lr), 0.0

@@ -50,7 +50,7 @@ def _table_command(target: str) -> list:
     from torch.utils import cpp_extension as ext
 
     inc = [a for p in ext.include_paths() + [sysconfig.get_paths()["include"]] for a in ("-isystem", p)]
-    return ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared", *inc,
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared", *inc, "-I", INCLUDE,
             "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, os.path.join(CSRC, "table.cpp"), "-o", target,
             "-L", ext.library_paths()[0], "-lc10", "-ltorch_cpu", "-ltorch_python"]
 

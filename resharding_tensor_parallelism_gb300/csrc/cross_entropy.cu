@@ -33,11 +33,10 @@ namespace {
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
 
-// Sums and counters of one call, at the start of its workspace.
+// Sums of one call, at the start of its workspace.
 struct Shared {
-    double weight;      // of the counted rows
-    float scale;        // of a row's gradient, before its own weight
-    unsigned finished;  // blocks of the last piece
+    double weight;  // of the counted rows
+    float scale;    // of a row's gradient, before its own weight
 };
 constexpr int64_t SHARED_BYTES = 256;
 
@@ -47,16 +46,12 @@ struct RowsArgs {
     float* lse;           // or NULL
     // training
     __nv_bfloat16* e[LIN_MAX_RANKS];
-    const uint4* x;  // [rows, K]
+    const uint4* x;  // [rows, K], or its copy at `scaled`
     uint4* scaled;   // x times the row's factor
     float* factor;
     Shared* shared;
-    float* total;              // or NULL: not the last piece
-    const float* all_loss;     // of every row, with their weights
-    const float* all_weights;
-    int64_t all_rows;
-    int32_t mean;
-    int32_t P, cols, part_cols, parts_of_rank, x_vectors;
+    int64_t ld;  // of e
+    int32_t P, cols, part_cols, parts_of_rank, x_vectors, x_stride, scaled_stride;
 };
 
 template <class T, class F>
@@ -79,21 +74,11 @@ __device__ __forceinline__ uint4 times(const uint4& v, float f)
                       pack_bf16(bf16_lo(v.z) * f, bf16_hi(v.z) * f), pack_bf16(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
 }
 
-// Sum over every row of weight * loss, in a fixed order.
-__device__ __forceinline__ float total_loss(const RowsArgs& a, double* scratch)
-{
-    double s = 0.0;
-    for (int64_t r = threadIdx.x; r < a.all_rows; r += THREADS) {
-        const float w = a.all_weights ? __ldcg(a.all_weights + r) : 1.0f;
-        if (w != 0.0f) s += (double)w * (double)__ldcg(a.all_loss + r);  // ignored rows: 0
-    }
-    s = block_reduce(s, scratch, [](double x, double y) { return x + y; });
-    if (a.mean) s = a.shared->weight != 0.0 ? s / a.shared->weight : 0.0;
-    return (float)s;
-}
-
 // One row a block: joins the row's statistics into lse and loss and, TRAIN, does what the
-// head of this file says. Latency bound: 2 KB of statistics and K elements a row.
+// head of this file says. Latency bound (1 to 8 KB of statistics and K elements a row), so
+// every load goes out first, and a row whose parts all refer to 0 takes one barrier
+// (8192 rows of 512 parts, K = 4096: 60 us with loads where they are used and two
+// reductions; a warp a row 54, but 18 instead of 13 for 777 rows of 196).
 template <bool TRAIN>
 __global__ void __launch_bounds__(THREADS) loss_rows_kernel(const __grid_constant__ RowsArgs a)
 {
@@ -101,94 +86,149 @@ __global__ void __launch_bounds__(THREADS) loss_rows_kernel(const __grid_constan
     float* scratch_f = reinterpret_cast<float*>(scratch);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int me = (int)threadIdx.x;
     const int64_t row = blockIdx.x;
     const float2* stats = a.softmax.stats + row * a.softmax.parts;
     const int64_t t = target_at(a.softmax.targets, a.softmax.targets64, row);
-    const bool ignored = t == a.softmax.ignore, known = t >= 0 && t < a.softmax.vocab;
+    const float logit = __ldcg(a.softmax.target_logit + row);  // nothing where the target is not known
     const float w = !TRAIN ? 0.0f : a.softmax.weights ? __ldcg(a.softmax.weights + row) : 1.0f;
-    // The row's reference is the largest of its parts': 0, unless a part has one above, or all below.
-    float top = minus_infinity(), low = -minus_infinity(), sum = 0.0f;
-    for (int i = threadIdx.x; i < a.softmax.parts; i += THREADS) {
-        const float2 s = __ldcg(stats + i);
-        const float now = fmaxf(top, s.x), r = finite_ref(now);
-        sum = sum * exp2_fast(top - r) + s.y * exp2_fast(s.x - r);
-        top = now;
-        if (s.x > minus_infinity()) low = fminf(low, s.x);
-    }
-    const float mine = top;
-    top = block_reduce(top, scratch_f, [](float x, float y) { return fmaxf(x, y); });
-    const float ref = finite_ref(top);
-    sum = block_reduce(sum * exp2_fast(mine - ref), scratch_f, [](float x, float y) { return x + y; });
-    const float logit = known ? __ldcg(a.softmax.target_logit + row) : 0.0f;
-    if (threadIdx.x == 0) {
-        const float lse = (ref + log2f(sum)) * LN2;
-        if (a.lse) a.lse[row] = lse;
-        a.loss[row] = ignored ? 0.0f : known ? lse - logit : __int_as_float(0x7FC00000);
-    }
+    const float scale = TRAIN ? __ldcg(&a.shared->scale) : 0.0f;
+    constexpr int AHEAD = 2;  // vectors of X a thread holds: 4096 elements a block
+    uint4 x[AHEAD];
     if constexpr (TRAIN) {
-        const bool part = !ignored && w != 0.0f;
-        if (__syncthreads_or(low < top) && part) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (me + k * THREADS < a.x_vectors) x[k] = __ldcg(a.x + row * a.x_stride + me + k * THREADS);
+    }
+    float sum = 0.0f;
+    bool other = false;  // a part that refers to something else
+#pragma unroll 4
+    for (int i = me; i < a.softmax.parts; i += THREADS) {
+        const float2 s = __ldcg(stats + i);
+        if (s.x == 0.0f) sum += s.y;
+        else if (s.x != minus_infinity()) other = true;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((me & 31) == 0) scratch_f[me >> 5] = sum;
+    other = __syncthreads_or(other);
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) sum += scratch_f[k];
+    const bool ignored = t == a.softmax.ignore, known = t >= 0 && t < a.softmax.vocab, part = !ignored && w != 0.0f;
+    float ref = 0.0f;
+    if (other) {  // the row's reference is the largest of its parts'
+        float top = minus_infinity();
+        for (int i = me; i < a.softmax.parts; i += THREADS) top = fmaxf(top, __ldcg(stats + i).x);
+        ref = finite_ref(block_reduce(top, scratch_f, [](float x, float y) { return fmaxf(x, y); }));
+        sum = 0.0f;
+        for (int i = me; i < a.softmax.parts; i += THREADS) {
+            const float2 s = __ldcg(stats + i);
+            if (s.x != minus_infinity()) sum += s.y * exp2_fast(s.x - ref);
+        }
+        sum = block_reduce(sum, scratch_f, [](float x, float y) { return x + y; });
+        if (TRAIN && part) {
             for (int i = 0; i < a.P; ++i) {
-                uint4* e = reinterpret_cast<uint4*>(a.e[i] + row * a.cols);
-                for (int v = threadIdx.x; v < a.cols / 8; v += THREADS) {
+                uint4* e = reinterpret_cast<uint4*>(a.e[i] + row * a.ld);
+                for (int v = me; v < a.cols / 8; v += THREADS) {
                     const float r = __ldcg(stats + i * a.parts_of_rank + 8 * v / a.part_cols).x;
                     if (r != ref) e[v] = times(e[v], exp2_fast(r - ref));
                 }
             }
             __syncthreads();
         }
+    }
+    if (me == 0) {
+        const float lse = (ref + log2f(sum)) * LN2;
+        if (a.lse) a.lse[row] = lse;
+        a.loss[row] = ignored ? 0.0f : known ? lse - logit : __int_as_float(0x7FC00000);
+    }
+    if constexpr (TRAIN) {
         // a target outside the vocabulary shows
-        const float factor = !part ? 0.0f : known ? a.shared->scale * w / sum : __int_as_float(0x7FC00000);
-        if (threadIdx.x == 0) {
+        const float factor = !part ? 0.0f : known ? scale * w / sum : __int_as_float(0x7FC00000);
+        if (me == 0) {
             a.factor[row] = factor;
             if (part && known)
-                a.e[t / a.cols][row * a.cols + t % a.cols] = __float2bfloat16_rn(exp2_fast(fmaf(logit, LOG2E, -ref)) - sum);
+                a.e[t / a.cols][row * a.ld + t % a.cols] = __float2bfloat16_rn(exp2_fast(fmaf(logit, LOG2E, -ref)) - sum);
         }
-        const uint4* x = a.x + row * a.x_vectors;
-        uint4* scaled = a.scaled + row * a.x_vectors;
-        for (int v = threadIdx.x; v < a.x_vectors; v += THREADS)  // a row without a part is 0 whatever it holds
-            scaled[v] = part ? times(__ldcg(x + v), factor) : make_uint4(0u, 0u, 0u, 0u);
-        if (!a.total) return;
-        __shared__ bool closing;
-        if (threadIdx.x == 0) {
-            __threadfence();
-            closing = atomicAdd(&a.shared->finished, 1u) == gridDim.x - 1;
-        }
-        __syncthreads();
-        if (!closing) return;
-        __threadfence();
-        const float total = total_loss(a, scratch);
-        if (threadIdx.x == 0) *a.total = total;
+        uint4* scaled = a.scaled + row * a.scaled_stride;
+        auto put = [&](int v, const uint4& x) {  // a row without a part is 0 whatever it holds
+            scaled[v] = part ? times(x, factor) : make_uint4(0u, 0u, 0u, 0u);
+        };
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (me + k * THREADS < a.x_vectors) put(me + k * THREADS, x[k]);
+        for (int v = me + AHEAD * THREADS; v < a.x_vectors; v += THREADS) put(v, __ldcg(a.x + row * a.x_stride + v));
     }
 }
 
-// The weight of the counted rows, from which the gradients' scale follows. One block, which
-// runs beside the product before it: that one has waited for all earlier work, and neither
-// touches what the other writes. It ends after the product all the same, so that the kernel
-// behind it need wait for this one only. alone: there is no product (no rows).
+// Sum over 1024 threads, in the first warp (64-bit adds are slow here: by every thread, 8 us).
+__device__ __forceinline__ double block_sum_1024(double s)
+{
+    __shared__ double sums[32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x >= 32) return 0.0;
+    s = sums[threadIdx.x];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+// The weight of the counted rows, from which the gradients' scale follows, and at the end
+// the total. One block each, which run beside the product in front of them: that one has
+// waited for all earlier work, and neither touches what the other writes. They end after
+// the product all the same, so that the kernel behind need wait for them only. alone: there
+// is no such product. (The total by the last block of loss_rows_kernel to finish: a counter
+// that 16384 blocks count on took 80 us.)
 __global__ void __launch_bounds__(1024) loss_scale_kernel(const void* targets, int targets64, const float* weights, int64_t rows,
                                                           int64_t ignore, int mean, float scale, Shared* sh, float* total, int alone)
 {
-    __shared__ double sums[32];
     if (alone) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     double s = 0.0;
     if (mean)
         for (int64_t r = threadIdx.x; r < rows; r += 1024)
             if (target_at(targets, targets64, r) != ignore) s += weights ? (double)__ldcg(weights + r) : 1.0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
-    __syncthreads();
+    s = block_sum_1024(s);
     if (threadIdx.x == 0) {
-        s = 0.0;
-        for (int w = 0; w < 32; ++w) s += sums[w];
         sh->weight = s;
         sh->scale = !mean ? scale : s != 0.0 ? (float)((double)scale / s) : 0.0f;
-        sh->finished = 0u;
         if (rows == 0) *total = 0.0f;
     }
     if (!alone) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(1024) loss_total_kernel(const float* loss, const float* weights, int64_t rows, int mean,
+                                                          const Shared* sh, float* total, int alone)
+{
+    if (alone) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    double s = 0.0;
+    for (int64_t r = threadIdx.x; r < rows; r += 1024) {
+        const float w = weights ? __ldcg(weights + r) : 1.0f;
+        if (w != 0.0f) s += (double)w * (double)__ldcg(loss + r);  // ignored rows: 0
+    }
+    s = block_sum_1024(s);
+    if (threadIdx.x == 0) {
+        const double weight = __ldcg(&sh->weight);
+        *total = (float)(!mean ? s : weight != 0.0 ? s / weight : 0.0);
+    }
+    if (!alone) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Rows of X to rows that begin on a 128-byte line: the product reads 128 bytes of a row at
+// a time, and where those lie across two lines its operands come at two thirds of the rate.
+__global__ void __launch_bounds__(THREADS) align_rows_kernel(const uint4* x, uint4* to, int64_t rows, int vectors, int stride)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t n = rows * vectors;
+#pragma unroll 2
+    for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * THREADS)
+        to[i / vectors * stride + i % vectors] = __ldcg(x + i);
 }
 
 // float32 sums to bf16 gradients.
@@ -242,6 +282,7 @@ int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 struct Shape {
     int P;
     int64_t M, K, V, vocab, Vp;
+    int64_t lde, ldx;  // row strides of the exponentials and the scaled X: whole lines, which a product reads 128 bytes of
     int64_t piece;  // rows of a piece
     int pieces;
 };
@@ -249,6 +290,13 @@ struct Shape {
 // part_cols of the product that a piece of `rows` rows takes
 int part_cols(int64_t rows) { return rows <= LIN_FEW_ROWS ? LIN_FEW_COLS : LIN_TILE_COLS; }
 int64_t parts(const Shape& s, int64_t rows) { return s.P * ((s.Vp + part_cols(rows) - 1) / part_cols(rows)); }
+
+// Whether the product reads a copy of X with aligned rows: where its gain, an eighth of the
+// product's time, is more than the copy's 3 us.
+bool aligns_x(const Shape& s, int64_t rows)
+{
+    return s.K % 64 && rows > LIN_FEW_ROWS && (double)rows * (double)s.K * (double)s.V >= 2e10;
+}
 
 int check_shape(const char* fn, int P, int64_t M, int64_t K, int64_t V, int64_t vocab, int64_t piece_rows, bool train, Shape* s)
 {
@@ -262,6 +310,7 @@ int check_shape(const char* fn, int P, int64_t M, int64_t K, int64_t V, int64_t 
     if (vocab < 1 || vocab > V) return fail(RTP_ESHAPE, "%s: vocab=%lld outside [1, V=%lld]", fn, (long long)vocab, (long long)V);
     if (piece_rows < 0) return fail(RTP_EINVAL, "%s: piece_rows=%lld", fn, (long long)piece_rows);
     s->P = P, s->M = M, s->K = K, s->V = V, s->vocab = vocab, s->Vp = V / P;
+    s->lde = up(s->Vp, 64), s->ldx = up(K, 64);
     // As many rows as the head of this file allows, in pieces of about the same size;
     // whole row tiles, so that only the last piece ends inside one.
     const int64_t most = up(piece_rows ? piece_rows : std::max({2 * K, (int64_t)2048, ((int64_t)1 << 29) / V}), LIN_TILE_ROWS);
@@ -285,8 +334,8 @@ Space space_of(const Shape& s, bool train, bool sum)
     w.factor = w.logit + up(s.piece * 4, 256);
     w.stats = w.factor + (train ? up(s.piece * 4, 256) : 0);
     w.x = w.stats + up(most * 8, 256);
-    w.e = w.x + (train ? up(s.piece * s.K * 2, 256) : 0);
-    w.sum = w.e + (train ? up(s.piece * s.V * 2, 256) : 0);
+    w.e = w.x + (train || aligns_x(s, s.piece) ? up(s.piece * s.ldx * 2, 256) : 0);
+    w.sum = w.e + (train ? up(s.P * s.piece * s.lde * 2, 256) : 0);
     w.bytes = w.sum + (sum ? s.K * s.V * 4 : 0);
     return w;
 }
@@ -339,18 +388,36 @@ const void* rows_of(const void* p, int64_t first, int64_t row_bytes)
 // The product with its statistics for `rows` rows from `first`, and the rows' arguments.
 int softmax_product(const Call& c, LinEpi epi, const float* weights, int64_t first, int64_t rows, RowsArgs* a, cudaStream_t stream)
 {
+    const void* x = rows_of(c.X, first, c.s.K * 2);
+    int64_t ldx = c.s.K;
+    if (aligns_x(c.s, rows)) {
+        void* to = c.ws + c.space.x;
+        ldx = c.s.ldx;
+        int sms = 0;
+        if (device_sms(&sms)) return fail(RTP_ECUDA, "%s: no CUDA device", c.fn);
+        const int64_t vectors = rows * (c.s.K / 8);
+        const unsigned blocks = (unsigned)std::min<int64_t>((vectors + THREADS - 1) / THREADS, (int64_t)8 * sms);
+        TRY(launch(c.fn, align_rows_kernel, dim3(blocks), THREADS, stream, static_cast<const uint4*>(x), static_cast<uint4*>(to), rows,
+                   (int)(c.s.K / 8), (int)(ldx / 8)));
+        x = to;
+    }
+    a->x = static_cast<const uint4*>(x);
+    a->x_vectors = (int)(c.s.K / 8);
+    a->x_stride = (int)(ldx / 8);
     LinGemm g;
     g.epi = epi;
+    g.lda = ldx;
     g.groups = c.s.P;
     g.a_shared = true;
     g.rows = rows;
     g.cols = c.s.Vp;
     g.kdim = c.s.K;
     for (int i = 0; i < c.s.P; ++i) {
-        g.A[i] = rows_of(c.X, first, c.s.K * 2);
+        g.A[i] = x;
         g.B[i] = c.W[i];
         if (epi == LIN_EXP) {
-            g.out[i] = c.ws + c.space.e + i * rows * c.s.Vp * 2;
+            g.out[i] = c.ws + c.space.e + i * rows * c.s.lde * 2;
+            g.ldo = c.s.lde;
             a->e[i] = static_cast<__nv_bfloat16*>(g.out[i]);
         }
     }
@@ -363,6 +430,7 @@ int softmax_product(const Call& c, LinEpi epi, const float* weights, int64_t fir
     g.softmax.weights = weights ? weights + first : nullptr;
     a->softmax = softmax_args(g.softmax, (int)parts(c.s, rows));
     a->P = c.s.P;
+    a->ld = c.s.lde;
     a->cols = (int)c.s.Vp;
     a->part_cols = part_cols(rows);
     a->parts_of_rank = a->softmax.parts / c.s.P;
@@ -415,24 +483,20 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
                 return fail(RTP_ECUDA, "%s: cudaMemsetAsync failed", fn);
         return RTP_OK;
     }
+    auto sum_up = [&](int piece, int alone) {  // behind the last piece's losses
+        if (piece < s.pieces - 1) return (int)RTP_OK;
+        return launch(fn, loss_total_kernel, dim3(1), 1024, stream, (const float*)loss, weights, s.M, mean, (const Shared*)sh, total, alone);
+    };
     for (int p = 0; p < s.pieces; ++p) {
         const int64_t first = p * s.piece, rows = std::min(s.piece, s.M - first);
         RowsArgs a = {};
         TRY(softmax_product(c, LIN_EXP, weights, first, rows, &a, stream));
         if (p == 0) TRY(set_scale());
-        a.x = static_cast<const uint4*>(rows_of(c.X, first, s.K * 2));
         a.scaled = reinterpret_cast<uint4*>(c.ws + c.space.x);
-        a.x_vectors = (int)(s.K / 8);
+        a.scaled_stride = (int)(s.ldx / 8);
         a.factor = reinterpret_cast<float*>(c.ws + c.space.factor);
         a.loss = loss + first;
         a.shared = sh;
-        a.mean = mean;
-        if (p == s.pieces - 1) {
-            a.total = total;
-            a.all_loss = loss;
-            a.all_weights = weights;
-            a.all_rows = s.M;
-        }
         TRY(launch(fn, loss_rows_kernel<true>, dim3((unsigned)rows), THREADS, stream, a));
         if (dX) {
             LinGemm g;
@@ -447,9 +511,11 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
                 g.A[i] = a.e[i];
                 g.B[i] = c.W[i];
             }
+            g.lda = s.lde;
             g.row_scale = a.factor;
             g.out[0] = static_cast<char*>(dX) + first * s.K * dx_size;
             TRY(launch_linear_gemm(fn, g, stream));
+            TRY(sum_up(p, 0));
         }
         if (dW) {
             LinGemm g;
@@ -458,6 +524,8 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
             g.a_shared = true;
             g.out_f32 = sums || dw_dtype == RTP_F32;
             g.accumulate = accumulate || p > 0;
+            g.lda = s.ldx;
+            g.ldb = s.lde;
             g.rows = s.K;
             g.cols = s.Vp;
             g.kdim = rows;
@@ -468,6 +536,7 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
             }
             TRY(launch_linear_gemm(fn, g, stream));
         }
+        if (!dX) TRY(sum_up(p, 1));
     }
     if (sums) {
         RoundArgs a = {};

@@ -48,6 +48,8 @@ struct LinGemm {
     LinEpi epi = LIN_OUT;
     int act = RTP_ACT_NONE;
     int64_t rows = 0, cols = 0, kdim = 0;
+    int64_t lda = 0, ldb = 0;  // row strides in elements of A and B as stored, 0: dense
+    int64_t ldo = 0;           // LIN_EXP: of out
     const void* A[LIN_MAX_GROUPS] = {};
     const void* B[LIN_MAX_GROUPS] = {};
     const void* B2[LIN_MAX_RANKS] = {};

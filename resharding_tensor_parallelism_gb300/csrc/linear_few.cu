@@ -51,6 +51,7 @@ struct Args {
     int32_t act, keep, weights_ready;
     unsigned long long wait_ns;  // limit of a wait for this kernel's own progress
     SoftmaxArgs softmax;
+    int64_t ldo;  // LIN_EXP: row stride of out
 };
 
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 2) linear_few_kernel(const __grid_con
             if (sum == 0.0f) ref = minus_infinity();
             if (lane == 0) a.softmax.stats[(int64_t)t * a.softmax.parts + tile] = make_float2(ref, sum);
             if (EPI == LIN_EXP && f < cols)
-                store_bf16x4(static_cast<__nv_bfloat16*>(a.out[g]) + (int64_t)t * a.cols + f0 + f,
+                store_bf16x4(static_cast<__nv_bfloat16*>(a.out[g]) + (int64_t)t * a.ldo + f0 + f,
                              takes_part(a.softmax, t) ? make_float4(e[0], e[1], e[2], e[3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f));
         }
     }
@@ -448,6 +449,7 @@ int launch_linear_few(const char* fn, const LinGemm& p, bool weights_ready, cuda
     a.cols = (int)p.cols;
     a.act = p.act;
     a.softmax = softmax_args(p.softmax, outs * a.tiles);
+    a.ldo = p.ldo ? p.ldo : p.cols;
     a.weights_ready = weights_ready;
     int64_t wait_ns = (int64_t)WAIT_LIMIT_NS;
     take_hook(RTP_HOOK_WAIT_LIMIT, &wait_ns);

@@ -14,13 +14,13 @@ int epi_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, bool f3
 
 // Encodes a map, or copies the previous group's when it is of the same buffer
 // (a shared operand is encoded once).
-int operand_map(CUtensorMap* maps, const void* const* ptrs, int i, int64_t rows, int64_t cols, int box_rows)
+int operand_map(CUtensorMap* maps, const void* const* ptrs, int i, int64_t rows, int64_t cols, int box_rows, int64_t ld)
 {
     if (i > 0 && ptrs[i] == ptrs[i - 1]) {
         maps[i] = maps[i - 1];
         return RTP_OK;
     }
-    return make_map(&maps[i], ptrs[i], rows, cols, box_rows);
+    return make_map(&maps[i], ptrs[i], rows, cols, box_rows, ld);
 }
 
 }  // namespace
@@ -32,18 +32,20 @@ int launch_linear_gemm(const char* fn, const LinGemm& p, cudaStream_t stream)
     const int tile_cols = p.epi == LIN_GLU ? BN / 2 : BN;
     int st;
     for (int g = 0; g < p.groups; ++g) {
-        if (p.a_t) st = operand_map(a.ta, p.A, g, p.kdim, p.rows, 64);
-        else st = operand_map(a.ta, p.A, g, p.rows, p.kdim, 128);
+        if (p.a_t) st = operand_map(a.ta, p.A, g, p.kdim, p.rows, 64, p.lda);
+        else st = operand_map(a.ta, p.A, g, p.rows, p.kdim, 128, p.lda);
         if (st) return st;
-        if (p.b_t) st = operand_map(a.tb, p.B, g, p.cols, p.kdim, 128);
-        else st = operand_map(a.tb, p.B, g, p.kdim, p.cols, BK);
+        if (p.b_t) st = operand_map(a.tb, p.B, g, p.cols, p.kdim, 128, p.ldb);
+        else st = operand_map(a.tb, p.B, g, p.kdim, p.cols, BK, p.ldb);
         if (st) return st;
         if (p.epi == LIN_GLU && (st = make_map(&a.tb[LIN_MAX_RANKS + g], p.B2[g], p.kdim, p.cols, BK))) return st;
     }
     const int outs = p.fused ? 1 : p.groups;
     a.keep = p.epi == LIN_DGLU || p.out2[0] != nullptr;
     for (int g = 0; g < outs; ++g) {
-        if (p.epi != LIN_LSE && (st = epi_map(&a.to[g], p.out[g], p.rows, p.cols, p.out_f32))) return st;
+        if (p.epi == LIN_EXP) st = encode_out_map(&a.to[g], p.out[g], p.rows, p.cols, p.ldo ? p.ldo : p.cols, false);
+        else if (p.epi != LIN_LSE) st = epi_map(&a.to[g], p.out[g], p.rows, p.cols, p.out_f32);
+        if (st) return st;
         if (a.keep && (st = epi_map(&a.to2[g], p.out2[g], p.rows, p.cols, false))) return st;
         if (a.keep && p.epi == LIN_GLU && (st = epi_map(&a.to3[g], p.out3[g], p.rows, p.cols, false))) return st;
         const void* in = p.epi == LIN_DGLU ? p.aux[g] : g < LIN_MAX_RANKS ? p.residual[g] : nullptr;

@@ -1,7 +1,7 @@
 // Python extension of the binding: checks lists of torch tensors against the type,
 // shape and device that a call will touch, and returns their addresses as one table
 // of 64-bit pointers; allocates lists of buffers; and makes the calls that take the
-// GPU least (a linear layer, a gated block, clipping) whole. The same checks as the
+// GPU least (a linear layer, a gated block, clipping, a loss, an AdamW step) whole. The same checks as the
 // binding's Python code, at about 20 ns a tensor instead of 500: a call on 8 ranks
 // passes 20 to 60 tensors, and a decoded token's product takes the GPU about as long
 // as that loop.
@@ -11,6 +11,8 @@
 
 #include <cstdint>
 #include <vector>
+
+#include "rtp.h"
 
 namespace {
 
@@ -148,20 +150,29 @@ using ClipFn = int (*)(int, const int32_t*, const int64_t*, const void* const*, 
 LinearFn linear_fn = nullptr;
 GluFn glu_fn = nullptr;
 ClipFn clip_fn = nullptr;
+decltype(&rtp_tp_cross_entropy) loss_fn = nullptr;
+decltype(&rtp_tp_cross_entropy_train) loss_train_fn = nullptr;
+decltype(&rtp_tp_cross_entropy_workspace) loss_workspace_fn = nullptr;
+decltype(&rtp_adamw_step) adamw_fn = nullptr;
 
-// bind(addresses of rtp_tp_linear, rtp_tp_glu, rtp_clip_grad_norm)
+// bind(addresses of rtp_tp_linear, rtp_tp_glu, rtp_clip_grad_norm, rtp_tp_cross_entropy,
+// rtp_tp_cross_entropy_train, rtp_tp_cross_entropy_workspace, rtp_adamw_step)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t nargs)
 {
-    if (nargs != 3) {
-        PyErr_SetString(PyExc_TypeError, "bind(linear, glu, clip)");
+    if (nargs != 7) {
+        PyErr_SetString(PyExc_TypeError, "bind(linear, glu, clip, loss, loss_train, loss_workspace, adamw)");
         return nullptr;
     }
-    const auto a = PyLong_AsUnsignedLongLong(args[0]), b = PyLong_AsUnsignedLongLong(args[1]),
-               c = PyLong_AsUnsignedLongLong(args[2]);
+    uintptr_t at[7];
+    for (int i = 0; i < 7; ++i) at[i] = (uintptr_t)PyLong_AsUnsignedLongLong(args[i]);
     if (PyErr_Occurred()) return nullptr;
-    clip_fn = reinterpret_cast<ClipFn>((uintptr_t)c);
-    linear_fn = reinterpret_cast<LinearFn>((uintptr_t)a);
-    glu_fn = reinterpret_cast<GluFn>((uintptr_t)b);
+    linear_fn = reinterpret_cast<LinearFn>(at[0]);
+    glu_fn = reinterpret_cast<GluFn>(at[1]);
+    clip_fn = reinterpret_cast<ClipFn>(at[2]);
+    loss_fn = reinterpret_cast<decltype(loss_fn)>(at[3]);
+    loss_train_fn = reinterpret_cast<decltype(loss_train_fn)>(at[4]);
+    loss_workspace_fn = reinterpret_cast<decltype(loss_workspace_fn)>(at[5]);
+    adamw_fn = reinterpret_cast<decltype(adamw_fn)>(at[6]);
     Py_RETURN_NONE;
 }
 
@@ -371,6 +382,188 @@ PyObject* clip(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     }
 }
 
+// ---- losses and the AdamW step -------------------------------------------------------
+
+at::TensorOptions on(at::ScalarType type, long device)
+{
+    return at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, (c10::DeviceIndex)device));
+}
+
+// What both loss calls take: X, W, targets.
+struct LossArguments {
+    int P;
+    int64_t M, K, Vp;
+    const void *x[1], *w[MAX_RANKS], *targets;
+    int wide;
+};
+bool loss_arguments(PyObject* const* args, long device, LossArguments* a)
+{
+    if (!PyList_Check(args[1]) || !THPVariable_Check(args[2])) return false;
+    const Py_ssize_t P = PyList_GET_SIZE(args[1]);
+    int64_t Kw;
+    if (P < 1 || P > MAX_RANKS || PyList_Check(args[0]) || !matrix(args[0], &a->M, &a->K, device) ||
+        !matrix(args[1], &Kw, &a->Vp, device))
+        return false;
+    const at::Tensor& t = THPVariable_Unpack(args[2]);
+    if ((t.scalar_type() != at::kLong && t.scalar_type() != at::kInt) || t.sizes() != at::IntArrayRef{a->M} || !placed(t, device) ||
+        !addresses(args[0], 1, {a->M, a->K}, device, a->x) || !addresses(args[1], P, {a->K, a->Vp}, device, a->w))
+        return false;
+    a->P = (int)P;
+    a->targets = t.data_ptr();
+    a->wide = t.scalar_type() == at::kLong;
+    return true;
+}
+
+// loss(X, W, targets, vocab, ignore, device, stream): rtp_tp_cross_entropy with new
+// outputs and workspace, vocab < 0: all columns. Returns (loss, lse), or as linear() does.
+PyObject* loss(PyObject*, PyObject* const* args, Py_ssize_t nargs)
+{
+    if (nargs != 7 || !loss_fn) {
+        PyErr_SetString(PyExc_TypeError, "loss(X, W, targets, vocab, ignore, device, stream)");
+        return nullptr;
+    }
+    const long long vocab = PyLong_AsLongLong(args[3]), ignore = PyLong_AsLongLong(args[4]);
+    const long device = PyLong_AsLong(args[5]);
+    const unsigned long long stream = PyLong_AsUnsignedLongLong(args[6]);
+    if (PyErr_Occurred()) return nullptr;
+    LossArguments a;
+    if (!loss_arguments(args, device, &a)) Py_RETURN_NONE;
+    const int64_t V = a.Vp * a.P;
+    int64_t bytes = 0;
+    int rc = loss_workspace_fn(a.P, a.M, a.K, V, 0, 0, RTP_F32, &bytes);
+    if (rc) return PyLong_FromLong(rc);
+    at::Tensor l, s, ws;
+    try {
+        l = at::empty({a.M}, on(at::kFloat, device));
+        s = at::empty({a.M}, on(at::kFloat, device));
+        ws = at::empty({bytes}, on(at::kByte, device));
+    } catch (const std::exception&) {  // out of memory: the Python code raises it
+        Py_RETURN_NONE;
+    }
+    rc = loss_fn(a.P, a.M, a.K, V, vocab < 0 ? V : vocab, a.x[0], a.w, a.wide, a.targets, ignore, ws.data_ptr(), bytes,
+                 l.data_ptr<float>(), s.data_ptr<float>(), reinterpret_cast<void*>((uintptr_t)stream));
+    if (rc) return PyLong_FromLong(rc);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(std::move(l)), THPVariable_Wrap(std::move(s)));
+}
+
+// loss_train(X, W, targets, weights, vocab, ignore, mean, scale, device, stream):
+// rtp_tp_cross_entropy_train with new bf16 gradients. Returns (total, loss, dX, dW).
+PyObject* loss_train(PyObject*, PyObject* const* args, Py_ssize_t nargs)
+{
+    if (nargs != 10 || !loss_train_fn) {
+        PyErr_SetString(PyExc_TypeError, "loss_train(X, W, targets, weights, vocab, ignore, mean, scale, device, stream)");
+        return nullptr;
+    }
+    const long long vocab = PyLong_AsLongLong(args[4]), ignore = PyLong_AsLongLong(args[5]);
+    const bool mean = args[6] == Py_True;
+    const double scale = PyFloat_AsDouble(args[7]);
+    const long device = PyLong_AsLong(args[8]);
+    const unsigned long long stream = PyLong_AsUnsignedLongLong(args[9]);
+    if (PyErr_Occurred()) return nullptr;
+    LossArguments a;
+    if (!loss_arguments(args, device, &a)) Py_RETURN_NONE;
+    const float* weights = nullptr;
+    if (args[3] != Py_None) {
+        if (!THPVariable_Check(args[3])) Py_RETURN_NONE;
+        const at::Tensor& t = THPVariable_Unpack(args[3]);
+        if (t.scalar_type() != at::kFloat || t.sizes() != at::IntArrayRef{a.M} || !placed(t, device)) Py_RETURN_NONE;
+        weights = static_cast<const float*>(t.data_ptr());
+    }
+    const int64_t V = a.Vp * a.P;
+    int64_t bytes = 0;
+    int rc = loss_workspace_fn(a.P, a.M, a.K, V, 0, 1, RTP_BF16, &bytes);
+    if (rc) return PyLong_FromLong(rc);
+    at::Tensor total, l, dx, ws, dw[MAX_RANKS];
+    void* dwp[MAX_RANKS];
+    try {
+        total = at::empty(at::IntArrayRef{}, on(at::kFloat, device));
+        l = at::empty({a.M}, on(at::kFloat, device));
+        dx = at::empty({a.M, a.K}, bf16_on(device));
+        for (int i = 0; i < a.P; ++i) {
+            dw[i] = at::empty({a.K, a.Vp}, bf16_on(device));
+            dwp[i] = dw[i].data_ptr();
+        }
+        ws = at::empty({bytes}, on(at::kByte, device));
+    } catch (const std::exception&) {
+        Py_RETURN_NONE;
+    }
+    rc = loss_train_fn(a.P, a.M, a.K, V, vocab < 0 ? V : vocab, a.x[0], a.w, a.wide, a.targets, ignore, weights, mean, (float)scale, 0,
+                       ws.data_ptr(), bytes, total.data_ptr<float>(), l.data_ptr<float>(), RTP_BF16, dx.data_ptr(), RTP_BF16, dwp,
+                       0, reinterpret_cast<void*>((uintptr_t)stream));
+    if (rc) return PyLong_FromLong(rc);
+    PyObject* list = PyList_New(a.P);
+    if (!list) return nullptr;
+    for (int i = 0; i < a.P; ++i) {
+        PyObject* e = THPVariable_Wrap(std::move(dw[i]));
+        if (!e) {
+            Py_DECREF(list);
+            return nullptr;
+        }
+        PyList_SET_ITEM(list, i, e);
+    }
+    return Py_BuildValue("(NNNN)", THPVariable_Wrap(std::move(total)), THPVariable_Wrap(std::move(l)),
+                         THPVariable_Wrap(std::move(dx)), list);
+}
+
+// A float32 scalar on the device: its address, or NULL.
+const float* scalar_on(PyObject* o, long device)
+{
+    if (!THPVariable_Check(o)) return nullptr;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.scalar_type() != at::kFloat || t.numel() != 1 || t.get_device() != device) return nullptr;
+    return static_cast<const float*>(t.data_ptr());
+}
+
+// adamw(table, n, params, masters, grads, bits, lr, eps, norm, max_norm, seed, clock,
+// device, stream): rtp_adamw_step on a group's table (an address), which is brought up to
+// the tensors as they are. lr: a number or a scalar tensor; norm: None or a scalar tensor.
+// Returns True; a status; or None when a tensor is not what the group was built over.
+PyObject* adamw(PyObject*, PyObject* const* args, Py_ssize_t nargs)
+{
+    if (nargs != 14 || !adamw_fn || !PyList_Check(args[2]) || !PyList_Check(args[3]) || !PyList_Check(args[4])) {
+        PyErr_SetString(PyExc_TypeError,
+                        "adamw(table, n, params, masters, grads, bits, lr, eps, norm, max_norm, seed, clock, device, stream)");
+        return nullptr;
+    }
+    auto* table = reinterpret_cast<rtp_adamw_tensor*>((uintptr_t)PyLong_AsUnsignedLongLong(args[0]));
+    const long n = PyLong_AsLong(args[1]), bits = PyLong_AsLong(args[5]), device = PyLong_AsLong(args[12]);
+    const double eps = PyFloat_AsDouble(args[7]), max_norm = PyFloat_AsDouble(args[9]);
+    const unsigned long long seed = PyLong_AsUnsignedLongLong(args[10]), clock = PyLong_AsUnsignedLongLong(args[11]),
+                             stream = PyLong_AsUnsignedLongLong(args[13]);
+    if (PyErr_Occurred()) return nullptr;
+    const float *lr_at = nullptr, *norm = nullptr;
+    double lr = 0.0;
+    if (PyFloat_Check(args[6])) lr = PyFloat_AS_DOUBLE(args[6]);
+    else if (!(lr_at = scalar_on(args[6], device))) Py_RETURN_NONE;
+    if (args[8] != Py_None && !(norm = scalar_on(args[8], device))) Py_RETURN_NONE;
+    for (int k = 2; k < 5; ++k)
+        if (PyList_GET_SIZE(args[k]) != n) Py_RETURN_NONE;
+    for (long i = 0; i < n; ++i) {
+        PyObject *po = PyList_GET_ITEM(args[2], i), *mo = PyList_GET_ITEM(args[3], i), *go = PyList_GET_ITEM(args[4], i);
+        if (!THPVariable_Check(po) || !THPVariable_Check(go) || (mo != Py_None && !THPVariable_Check(mo))) Py_RETURN_NONE;
+        const at::Tensor &p = THPVariable_Unpack(po), &g = THPVariable_Unpack(go);
+        rtp_adamw_tensor& t = table[i];
+        at::ScalarType want;
+        if (!scalar_type(t.param_dtype, &want) || p.scalar_type() != want || p.numel() != t.numel || !placed(p, device)) Py_RETURN_NONE;
+        if ((g.scalar_type() != at::kFloat && g.scalar_type() != at::kBFloat16) || g.sizes() != p.sizes() || !placed(g, device))
+            Py_RETURN_NONE;
+        void* master = nullptr;
+        if (mo != Py_None) {
+            const at::Tensor& m = THPVariable_Unpack(mo);
+            if (m.scalar_type() != at::kFloat || want != at::kBFloat16 || m.sizes() != p.sizes() || !placed(m, device)) Py_RETURN_NONE;
+            master = m.data_ptr();
+        }
+        t.param = p.data_ptr();
+        t.master = static_cast<float*>(master);
+        t.grad = g.data_ptr();
+        t.grad_dtype = g.scalar_type() == at::kFloat ? RTP_F32 : RTP_BF16;
+    }
+    const int rc = adamw_fn((int)n, table, (int)bits, (float)lr, lr_at, (float)eps, norm, (float)max_norm, (uint32_t)seed,
+                            reinterpret_cast<void*>((uintptr_t)clock), reinterpret_cast<void*>((uintptr_t)stream));
+    if (rc) return PyLong_FromLong(rc);
+    Py_RETURN_TRUE;
+}
+
 // A method of the module. No C++ exception leaves it: tensors that torch itself wraps,
 // or that have no storage, raise from the very calls that ask for their addresses.
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
@@ -399,7 +592,8 @@ PyMethodDef entry(const char* name)
 
 PyMethodDef methods[] = {entry<bind>("bind"),       entry<table>("table"),         entry<like>("like"),
                          entry<buffers>("buffers"), entry<linear>("linear"),       entry<glu>("glu"),
-                         entry<clip>("clip"),       entry<unchanged>("unchanged"), {nullptr, nullptr, 0, nullptr}};
+                         entry<clip>("clip"),       entry<unchanged>("unchanged"), entry<loss>("loss"),
+                         entry<loss_train>("loss_train"), entry<adamw>("adamw"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_table", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -287,14 +287,14 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
 }
 
-// 2D bf16 tensor map over a row-major [rows, cols] matrix, box [box_rows, 64],
-// 128-byte swizzle (64 bf16 per box row).
-inline int make_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int box_rows)
+// 2D bf16 tensor map over a row-major [rows, cols] matrix (rows ld elements apart, 0: cols),
+// box [box_rows, 64], 128-byte swizzle (64 bf16 per box row).
+inline int make_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int box_rows, int64_t ld = 0)
 {
     auto fn = encode_fn();
     if (!fn) return fail(RTP_ECUDA, "operand map: cuTensorMapEncodeTiled is unavailable");
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)(cols * 2)};
+    cuuint64_t strides[1] = {(cuuint64_t)((ld ? ld : cols) * 2)};
     cuuint32_t box[2] = {64u, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1u, 1u};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
