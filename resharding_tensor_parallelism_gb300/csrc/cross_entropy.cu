@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(THREADS) loss_rows_kernel(const __grid_constan
     if (me == 0) {
         const float lse = (ref + log2f(sum)) * LN2;
         if (a.lse) a.lse[row] = lse;
-        a.loss[row] = ignored ? 0.0f : known ? lse - logit : __int_as_float(0x7FC00000);
+        const float loss = lse - logit;  // rounding may leave it below 0; a NaN stays one
+        a.loss[row] = ignored ? 0.0f : !known ? __int_as_float(0x7FC00000) : loss < 0.0f ? 0.0f : loss;
     }
     if constexpr (TRAIN) {
         // a target outside the vocabulary shows
