@@ -25,7 +25,9 @@
 // (rounding to nearest would leave v as it is: a step changes it by 1 - b2, less than
 // half a spacing). A bf16 weight without a float32 copy is rounded the same way, or small
 // steps would be lost. The bits are a hash of seed, tensor, step and element: a step is
-// reproducible bit for bit. The update itself uses m and v before they are rounded.
+// reproducible bit for bit. The update itself uses m and v before they are rounded. They are
+// formed by single float32 operations (no fused ones), so that any float32 program gets
+// the same codes.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -252,8 +254,8 @@ __device__ __noinline__ void any_row(const Item& it, int64_t row, const Rates& s
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float d = dx[j] * s.clip;
-        m[j] = fmaf(s.beta1, m[j], s.rest1 * d);
-        v[j] = fmaf(s.beta2, v[j], s.rest2 * d * d);
+        m[j] = BITS8 ? __fadd_rn(__fmul_rn(s.beta1, m[j]), __fmul_rn(s.rest1, d)) : fmaf(s.beta1, m[j], s.rest1 * d);
+        v[j] = BITS8 ? __fadd_rn(__fmul_rn(s.beta2, v[j]), __fmul_rn(__fmul_rn(s.rest2, d), d)) : fmaf(s.beta2, v[j], s.rest2 * d * d);
         x[j] = fmaf(x[j], keep, -s.rate * __fdividef(m[j], sqrt_fast(v[j] * s.correct2) + s.eps));
         noise[j] = pcg((uint32_t)at + (uint32_t)j + key);
         b[j] = it.master ? round_bf16(x[j]) : round_bf16_at_random(x[j], pcg(noise[j]) & 0xFFFFu);
@@ -332,8 +334,8 @@ __device__ __forceinline__ bool row_of_8_bits(const Item& it, int64_t at, const 
         const float d = dx[j] * s.clip;
         const float mo = __int_as_float((int)(mw << (24 - 8 * j)) >> 4 & (int)0x87F00000);
         const float vo = __uint_as_float((j < 3 ? vw << (20 - 8 * j) : vw >> 4) & 0x0FF00000u);
-        m[j] = fmaf(mo, fm, s.rest1 * d);
-        v[j] = fmaf(vo, fv, s.rest2 * d * d);
+        m[j] = __fadd_rn(__fmul_rn(mo, fm), __fmul_rn(s.rest1, d));
+        v[j] = __fadd_rn(__fmul_rn(vo, fv), __fmul_rn(__fmul_rn(s.rest2, d), d));
         x[j] = fmaf(x[j], keep, rate * m[j] * rcp_ftz(sqrt_ftz(v[j] * root) + eps));
     }
     const float mt = max_nan(max_nan(fabsf(m[0]), fabsf(m[1])), max_nan(fabsf(m[2]), fabsf(m[3])));

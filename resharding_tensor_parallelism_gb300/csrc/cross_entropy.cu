@@ -145,12 +145,17 @@ __global__ void __launch_bounds__(THREADS) loss_rows_kernel(const __grid_constan
         a.loss[row] = ignored ? 0.0f : !known ? __int_as_float(0x7FC00000) : loss < 0.0f ? 0.0f : loss;
     }
     if constexpr (TRAIN) {
-        // a target outside the vocabulary shows
-        const float factor = !part ? 0.0f : known ? scale * w / sum : __int_as_float(0x7FC00000);
+        // A target outside the vocabulary shows. What rounding did to the target's element, the
+        // largest of the row, is put right in the factor.
+        const float rest = exp2_fast(fmaf(logit, LOG2E, -ref)) - sum;
+        const __nv_bfloat16 kept = __float2bfloat16_rn(rest);
+        const float turned = __bfloat162float(kept);
+        const float factor = !part    ? 0.0f
+                             : !known ? __int_as_float(0x7FC00000)
+                                      : scale * w / sum * (turned != 0.0f ? rest / turned : 1.0f);
         if (me == 0) {
             a.factor[row] = factor;
-            if (part && known)
-                a.e[t / a.cols][row * a.ld + t % a.cols] = __float2bfloat16_rn(exp2_fast(fmaf(logit, LOG2E, -ref)) - sum);
+            if (part && known) a.e[t / a.cols][row * a.ld + t % a.cols] = kept;
         }
         uint4* scaled = a.scaled + row * a.scaled_stride;
         auto put = [&](int v, const uint4& x) {  // a row without a part is 0 whatever it holds

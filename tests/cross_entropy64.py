@@ -42,11 +42,15 @@ def gradients(X, W, targets, vocab, ignore, weights=None, mean=True, scale=1.0):
     d = p.clone()
     rows = torch.nonzero(counted & (targets >= 0) & (targets < vocab))[:, 0]
     d[rows, targets.long()[rows]] -= g[rows]
-    # Both products read d's exponentials (at the target: less the row's sum) rounded to bf16, half a step of d itself; dW
-    # reads rows of X that were multiplied by a factor and rounded, half a step more of every term. The exponentials and
-    # the factor are off by the row's error (each once).
+    # Both products read d's exponentials (at the target: less the row's sum) rounded to bf16, half a step of d itself; the
+    # row's factor takes the target's error back, which gives its half step to the row's others. dW reads rows of X that
+    # were multiplied by the factor and rounded, half a step more of every term. The exponentials and the factor are off
+    # by the row's error (each once).
     row = p.abs() * lse_bound(X, W, vocab, lse, logits)[:, None] * 2
-    ex, ew = BF16 * d.abs() * 1.01 + row, 2 * BF16 * d.abs() * 1.01 + row
+    others = d.abs().clone()
+    others[rows, targets.long()[rows]] = 0
+    ex = 2 * BF16 * others * 1.02 + 8 * EPS * d.abs() + row
+    ew = ex + BF16 * d.abs() * 1.02
     pad = W.shape[1] - vocab
     d, ex, ew = (torch.nn.functional.pad(t, (0, pad)) for t in (d, ex, ew))
     Xd, Wd = X.double(), W.double()
