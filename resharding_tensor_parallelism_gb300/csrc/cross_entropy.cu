@@ -237,6 +237,33 @@ __global__ void __launch_bounds__(THREADS) align_rows_kernel(const uint4* x, uin
         to[i / vectors * stride + i % vectors] = __ldcg(x + i);
 }
 
+// dX from the float32 products of its slices (dx_slices), in their order, times the rows' factors.
+struct SliceArgs {
+    const float4* from;  // [slices][rows][quads]
+    const float* factor;
+    void* to;
+    int64_t quads;  // of all rows
+    int32_t row_quads, slices;
+};
+template <bool F32>
+__global__ void __launch_bounds__(THREADS) slices_kernel(const __grid_constant__ SliceArgs a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < a.quads; i += (int64_t)gridDim.x * THREADS) {
+        float4 s = __ldcg(a.from + i);
+#pragma unroll 8
+        for (int k = 1; k < a.slices; ++k) {
+            const float4 v = __ldcg(a.from + k * a.quads + i);
+            s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+        const float f = __ldcg(a.factor + i / a.row_quads);
+        s = make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
+        if constexpr (F32) static_cast<float4*>(a.to)[i] = s;
+        else static_cast<uint2*>(a.to)[i] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+    }
+}
+
 // float32 sums to bf16 gradients.
 struct RoundArgs {
     const float4* from[LIN_MAX_RANKS];
@@ -297,6 +324,30 @@ struct Shape {
 int part_cols(int64_t rows) { return rows <= LIN_FEW_ROWS ? LIN_FEW_COLS : LIN_TILE_COLS; }
 int64_t parts(const Shape& s, int64_t rows) { return s.P * ((s.Vp + part_cols(rows) - 1) / part_cols(rows)); }
 
+// Slices of each rank's columns whose products for dX are summed by a kernel of their own
+// (0: none, all ranks in one accumulator). dX of few rows and a narrow model has few tiles,
+// each the product of the whole vocabulary, which a cluster shares four ways at most:
+// 256 x 512 from 8192 columns took 20 us on 8 of 76 pairs. K blocks take 0.28 us of a
+// pair, the sum 5 us.
+int64_t slice_columns(const Shape& s, int n) { return up((s.Vp + n - 1) / n, 64); }
+int dx_slices(const Shape& s, int64_t rows)
+{
+    constexpr int PAIRS = 76;
+    if (rows <= 0) return 0;
+    const int64_t tiles = ((rows + LIN_TILE_ROWS - 1) / LIN_TILE_ROWS) * ((s.K + LIN_TILE_COLS - 1) / LIN_TILE_COLS);
+    const int64_t kbs = s.P * ((s.Vp + 63) / 64);
+    const double one = 0.28 * (double)kbs / (double)std::min<int64_t>(4, std::max<int64_t>(1, PAIRS / tiles));
+    int best = 1;
+    double least = one;
+    for (int n = 1; n <= LIN_MAX_GROUPS / s.P; ++n) {
+        const int64_t parts = tiles * s.P * n, split = std::min<int64_t>(4, PAIRS / parts), kdim = slice_columns(s, n);
+        if (s.P * n < 2 || split < 1 || kdim < 512 || (n - 1) * kdim >= s.Vp) continue;
+        const double t = 0.28 * (double)(kdim / 64) / (double)split + 5.0;
+        if (t < 0.9 * least) least = t, best = n;
+    }
+    return least < one ? best : 0;
+}
+
 // Whether the product reads a copy of X with aligned rows: where its gain, an eighth of the
 // product's time, is more than the copy's 3 us.
 bool aligns_x(const Shape& s, int64_t rows)
@@ -328,7 +379,7 @@ int check_shape(const char* fn, int P, int64_t M, int64_t K, int64_t V, int64_t 
 
 // Where things are in a workspace; sum: float32 sums of dW.
 struct Space {
-    int64_t logit, factor, stats, x, e, sum, bytes;
+    int64_t logit, factor, stats, x, e, slices, sum, bytes;
 };
 Space space_of(const Shape& s, bool train, bool sum)
 {
@@ -341,7 +392,10 @@ Space space_of(const Shape& s, bool train, bool sum)
     w.stats = w.factor + (train ? up(s.piece * 4, 256) : 0);
     w.x = w.stats + up(most * 8, 256);
     w.e = w.x + (train || aligns_x(s, s.piece) ? up(s.piece * s.ldx * 2, 256) : 0);
-    w.sum = w.e + (train ? up(s.P * s.piece * s.lde * 2, 256) : 0);
+    w.slices = w.e + (train ? up(s.P * s.piece * s.lde * 2, 256) : 0);
+    int64_t sliced = 0;
+    for (int64_t rows : {s.piece, last}) sliced = std::max(sliced, dx_slices(s, rows) * s.P * rows * s.K * 4);
+    w.sum = w.slices + (train ? up(sliced, 256) : 0);
     w.bytes = w.sum + (sum ? s.K * s.V * 4 : 0);
     return w;
 }
@@ -504,7 +558,32 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
         a.loss = loss + first;
         a.shared = sh;
         TRY(launch(fn, loss_rows_kernel<true>, dim3((unsigned)rows), THREADS, stream, a));
-        if (dX) {
+        const int slices = dx_slices(s, rows);
+        if (dX && slices) {
+            LinGemm g;
+            g.groups = s.P * slices;
+            g.b_t = true;
+            g.out_f32 = true;
+            g.rows = rows;
+            g.cols = s.K;
+            g.kdim = slice_columns(s, slices);
+            g.lda = s.lde;
+            g.ldb = s.Vp;
+            float* products = reinterpret_cast<float*>(c.ws + c.space.slices);
+            for (int i = 0; i < g.groups; ++i) {
+                const int64_t col = i % slices * g.kdim;
+                g.A[i] = a.e[i / slices] + col;
+                g.B[i] = static_cast<const __nv_bfloat16*>(c.W[i / slices]) + col;
+                g.kdims[i] = std::min(g.kdim, s.Vp - col);
+                g.out[i] = products + i * rows * s.K;
+            }
+            TRY(launch_linear_gemm(fn, g, stream));
+            TRY(sum_up(p, 0));
+            const SliceArgs b = {reinterpret_cast<const float4*>(products), a.factor, static_cast<char*>(dX) + first * s.K * dx_size,
+                                 rows * s.K / 4, (int)(s.K / 4), g.groups};
+            const unsigned blocks = (unsigned)std::min<int64_t>((b.quads + THREADS - 1) / THREADS, (int64_t)8 * sms);
+            TRY(launch(fn, dx_dtype == RTP_F32 ? slices_kernel<true> : slices_kernel<false>, dim3(blocks), THREADS, stream, b));
+        } else if (dX) {
             LinGemm g;
             g.groups = s.P;
             g.fused = true;

@@ -50,6 +50,7 @@ struct LinGemm {
     int64_t rows = 0, cols = 0, kdim = 0;
     int64_t lda = 0, ldb = 0;  // row strides in elements of A and B as stored, 0: dense
     int64_t ldo = 0;           // LIN_EXP: of out
+    int64_t kdims[LIN_MAX_GROUPS] = {};  // b_t, not a_t: K range of a group where it is shorter than kdim (0: kdim)
     const void* A[LIN_MAX_GROUPS] = {};
     const void* B[LIN_MAX_GROUPS] = {};
     const void* B2[LIN_MAX_RANKS] = {};

@@ -33,9 +33,9 @@ int launch_linear_gemm(const char* fn, const LinGemm& p, cudaStream_t stream)
     int st;
     for (int g = 0; g < p.groups; ++g) {
         if (p.a_t) st = operand_map(a.ta, p.A, g, p.kdim, p.rows, 64, p.lda);
-        else st = operand_map(a.ta, p.A, g, p.rows, p.kdim, 128, p.lda);
+        else st = operand_map(a.ta, p.A, g, p.rows, p.kdims[g] ? p.kdims[g] : p.kdim, 128, p.lda);
         if (st) return st;
-        if (p.b_t) st = operand_map(a.tb, p.B, g, p.cols, p.kdim, 128, p.ldb);
+        if (p.b_t) st = operand_map(a.tb, p.B, g, p.cols, p.kdims[g] ? p.kdims[g] : p.kdim, 128, p.ldb);
         else st = operand_map(a.tb, p.B, g, p.kdim, p.cols, BK, p.ldb);
         if (st) return st;
         if (p.epi == LIN_GLU && (st = make_map(&a.tb[LIN_MAX_RANKS + g], p.B2[g], p.kdim, p.cols, BK))) return st;

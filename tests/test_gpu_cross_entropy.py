@@ -88,6 +88,21 @@ def test_train(M, K, V, P, vocab, dtype):
     assert rtp.device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,K,V,P", [(256, 512, 8192, 2), (5, 64, 16384, 1), (300, 264, 24600, 3), (130, 520, 12352, 1),
+                                     (257, 72, 8 * 1032, 8), (600, 136, 16392, 1)])
+def test_narrow_models(M, K, V, P, dtype):
+    """Few tiles of dX, whose columns are summed in slices: even and ragged ones, on one to eight ranks."""
+    X, W, shards, t = _inputs(M, K, V, P, V - 3, seed=14)
+    out = Guarded()
+    dX, dW = out.empty((M, K), dtype, "dX"), out.many([(K, V // P)] * P, dtype, "dW")
+    got = rtp.tp_cross_entropy_train(X, shards, t, vocab=V - 3, ignore_index=IGNORE, dX=dX, dW=dW)
+    out.check("train")
+    _check_train(X, W, t, V - 3, got)
+    _check_train(X, W, t, V - 3, rtp.tp_cross_entropy_train(X, shards, t, vocab=V - 3, ignore_index=IGNORE, dx_dtype=dtype,
+                                                            dw_dtype=dtype, piece_rows=256))
+
+
 @pytest.mark.parametrize("reduction", ["mean", "sum"])
 @pytest.mark.parametrize("M,K,V,P,vocab", [(5, 64, 264, 3, 260), (333, 128, 1040, 2, 1040)])
 def test_weights_and_scale(M, K, V, P, vocab, reduction):
