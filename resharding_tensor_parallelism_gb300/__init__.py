@@ -1339,12 +1339,14 @@ class AdamWGroup:
 
     def _scalar(self, name, t):
         """A float32 scalar on the group's GPU, as its address."""
+        if not isinstance(t, _torch().Tensor):
+            raise RtpError(-1, "AdamWGroup: %s is no tensor" % name)
         if t.dtype is not _torch().float32 or t.numel() != 1 or t.device != self.device:
             raise RtpError(-1, "AdamWGroup: %s must be one float32 on %s" % (name, self.device))
         return t.data_ptr()
 
     def step(self, grads, lr=None, norm=None, max_norm: float = 1.0, stream=None):
-        """One step with the gradients of the weights (float32 or bf16, each like its weight). lr: instead of the group's;
+        """One step with the gradients of the weights (float32 or bf16, each like its weight, none missing). lr: instead of the group's;
         a float, or a float32 scalar on the GPU (which a replayed step reads anew). norm: the global norm on the GPU
         (GradGroup.norm): gradients count times min(1, max_norm / (norm + 1e-6)), and stay as they are."""
         fn = "AdamWGroup.step"
@@ -1397,7 +1399,8 @@ class AdamWGroup:
         return got if self.scales is None else {**got, "scales": self.scales}
 
     def load_state_dict(self, state: dict) -> None:
-        """Copies a state_dict of a group over tensors of the same sizes into this one's buffers, on the current stream."""
+        """Copies a state_dict of a group over tensors of the same sizes into this one's buffers, on the current stream
+        (steps on other streams must be ordered after it by the caller). betas are this group's own."""
         fn = "AdamWGroup.load_state_dict"
         names = ["exp_avg", "exp_avg_sq"] + (["scales"] if self.states == 8 else [])
         if set(state) != set(names + ["step"]):

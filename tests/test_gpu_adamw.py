@@ -361,3 +361,62 @@ def test_an_empty_group_counts_its_steps():
     group = rtp.AdamWGroup([torch.zeros((0, 4), device="cuda")], states=8)
     group.step([torch.zeros((0, 4), device="cuda")])
     assert int(group.steps) == 1 and group.moments()[0].numel() == 0
+
+
+@pytest.mark.parametrize("n", [1, 130, 5000])
+def test_8_bit_moments_anywhere_in_memory(n):
+    """Codes and scales at odd places, through the C ABI: as those at whole vectors."""
+    def run(shift):
+        (p,), (g,) = _tensors([n], F32, None, 20), _tensors([n], F32, None, 21, 1e-3)
+        out = Guarded()
+        m, v = (out.empty((n + shift,), torch.uint8)[shift:].zero_() for _ in range(2))
+        scales = out.empty((2 * ((n + 127) // 128) + 2 * shift,), torch.uint8)[2 * shift:].zero_()
+        clock = torch.zeros(16, dtype=torch.int64, device="cuda")
+        rtp._check(rtp.lib().rtp_adamw_clock(clock.data_ptr(), 0, 0.9, 0.95, None))
+        t = (rtp.AdamWTensor * 1)()
+        t[0].numel, t[0].param, t[0].grad, t[0].exp_avg, t[0].exp_avg_sq = n, p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr()
+        t[0].scales, t[0].weight_decay = scales.data_ptr(), DECAY
+        for _ in range(3):
+            rtp._check(rtp.lib().rtp_adamw_step(1, t, 8, LR, None, EPS, None, 1.0, SEED, clock.data_ptr(), None))
+        out.check("step")
+        return p, m, v, scales
+    torch.cuda.synchronize()
+    a, b = run(0), run(1)
+    assert all(torch.equal(x, y) for x, y in zip(a[1:], b[1:]))
+    # the two forms of the quotient: each within 2^-20 of itself, of an update of lr at most 3 times over
+    assert ((a[0] - b[0]).abs() <= 3 * LR * 2.0 ** -18 + 4 * plain.EPS * a[0].abs()).all()
+
+
+@pytest.mark.parametrize("top", [1e-12, 1.0, 1e10, 1e30])
+def test_8_bit_moments_of_any_size(top):
+    """Blocks whose exponents fit the fast form and not, and both in one tensor."""
+    n = 4096
+    for spread in (1.0, 1e-4):  # squares stay normal float32 numbers
+        p, g = _tensors([n], F32, None, 22), _tensors([n], F32, None, 23)
+        g[0] *= top ** 0.5 if top > 1 else top
+        g[0][::2048] *= spread
+        group = rtp.AdamWGroup(p, lr=LR, betas=BETAS, eps=EPS, weight_decay=DECAY, states=8, seed=SEED)
+        for t in range(1, 4):
+            before = _before(group)
+            group.step(g)
+            _check_step(group, before, g, t)
+
+
+def test_two_groups_at_once():
+    """Steps of two groups on two streams beside each other."""
+    def make(i):
+        return rtp.AdamWGroup(_tensors([300_000, 77], BF16, None, 24 + i), lr=LR, states=8 if i else 32, masters=True, seed=SEED)
+    grads = [_tensors([300_000, 77], F32, None, 26 + i, 1e-3) for i in range(2)]
+    want = [make(i) for i in range(2)]
+    for i, group in enumerate(want):
+        for _ in range(6):
+            group.step(grads[i])
+    got, streams = [make(i) for i in range(2)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for i, group in enumerate(got):
+            group.step(grads[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert int(b.steps) == 6
+        assert all(torch.equal(x, y) for x, y in zip([*a.params, *a.masters, *a.moments()], [*b.params, *b.masters, *b.moments()]))

@@ -281,3 +281,78 @@ def test_more_exponentials_than_31_bits_count():
     _check_train(X[-4:], W, t[-4:], V, (total, loss[-4:], dX[-4:], dW), w[-4:])
     first = plain.forward(X[:4], W, t[:4], V, IGNORE)
     _near(loss[:4], first[0], plain.lse_bound(X[:4], W, V, first[1], first[2]) * 2, "first rows")
+
+
+def _c_train(X, shards, t, V, dX, dW, dw_dtype=rtp.BF16, piece=0):
+    """rtp_tp_cross_entropy_train through the C ABI, dX or dW may be None. Returns (total, loss)."""
+    M, K = X.shape
+    P = len(shards)
+    ws, n = rtp._loss_workspace(P, M, K, V, piece, 1, dw_dtype, 0, None)
+    total, loss = torch.full((), 7.0, device="cuda"), torch.full((M,), 7.0, device="cuda")
+    rtp._check(rtp.lib().rtp_tp_cross_entropy_train(
+        P, M, K, V, V, X.data_ptr(), rtp._ptrs([w.data_ptr() for w in shards]), 1, t.data_ptr(), IGNORE, None, 1, 1.0, piece,
+        ws.data_ptr(), n, total.data_ptr(), loss.data_ptr(), rtp.BF16, None if dX is None else dX.data_ptr(), dw_dtype,
+        None if dW is None else rtp._ptrs([d.data_ptr() for d in dW]), 0, rtp._stream_ptr(None)))
+    return total, loss
+
+
+@pytest.mark.parametrize("M,piece", [(5, 0), (300, 0), (600, 256)])
+def test_gradients_that_are_not_wanted(M, piece):
+    X, W, shards, t = _inputs(M, 136, 1040, 2, 1040, seed=15)
+    want = rtp.tp_cross_entropy_train(X, shards, t, ignore_index=IGNORE, piece_rows=piece)
+    dX, dW = torch.empty_like(X), [torch.empty_like(w) for w in shards]
+    for x, w in ((dX, None), (None, dW), (None, None)):
+        total, loss = _c_train(X, shards, t, 1040, x, w, piece=piece)
+        assert torch.equal(total, want[0]) and torch.equal(loss, want[1])
+    assert torch.equal(dX, want[2]) and all(torch.equal(a, b) for a, b in zip(dW, want[3]))
+    alone = torch.empty((M,), device="cuda")
+    ws, n = rtp._loss_workspace(2, M, 136, 1040, 0, 0, rtp.F32, 0, None)
+    rtp._check(rtp.lib().rtp_tp_cross_entropy(2, M, 136, 1040, 1040, X.data_ptr(), rtp._ptrs([w.data_ptr() for w in shards]), 1,
+                                              t.data_ptr(), IGNORE, ws.data_ptr(), n, alone.data_ptr(), None,
+                                              rtp._stream_ptr(None)))
+    assert torch.equal(alone, rtp.tp_cross_entropy(X, shards, t, ignore_index=IGNORE)[0])
+
+
+def test_two_calls_at_once():
+    """Calls on two streams beside each other, each with its own workspace, again and again."""
+    sizes = [(300, 136, 4112, 2), (60, 520, 8208, 1)]
+    sets = [_inputs(M, K, V, P, V, seed=16 + i) for i, (M, K, V, P) in enumerate(sizes)]
+    want = [rtp.tp_cross_entropy_train(X, s, t, ignore_index=IGNORE) for X, _, s, t in sets]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(8):
+        for s, (X, _, shards, t) in zip(streams, sets):
+            with torch.cuda.stream(s):
+                got.append(rtp.tp_cross_entropy_train(X, shards, t, ignore_index=IGNORE))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        w = want[i % 2]
+        assert all(torch.equal(a, b) for a, b in zip([*g[:3], *g[3]], [*w[:3], *w[3]]))
+
+
+def test_an_ignored_index_inside_the_vocabulary():
+    X, W, shards, t = _inputs(300, 64, 512, 2, 512, ignored=0.0, seed=18)
+    u = torch.where(t < 100, IGNORE, t)
+    t[t < 100] = 7
+    want = rtp.tp_cross_entropy_train(X, shards, u, ignore_index=IGNORE)
+    got = rtp.tp_cross_entropy_train(X, shards, t, ignore_index=7)
+    assert all(torch.equal(a, b) for a, b in zip([*got[:3], *got[3]], [*want[:3], *want[3]]))
+
+
+def test_refusals_of_the_binding():
+    X, W, shards, t = _inputs(6, 64, 512, 2, 512)
+    call, train = rtp.tp_cross_entropy, rtp.tp_cross_entropy_train
+    wide = torch.zeros((6, 128), dtype=BF16, device="cuda")
+    for bad in (lambda: call(wide[:, ::2], shards, t), lambda: call(X, shards, t[:5]), lambda: call(X, shards, t.float()),
+                lambda: call(X, shards, t.cpu()), lambda: call(X, shards, t[:, None]), lambda: call(X.float(), shards, t),
+                lambda: call(X, [shards[0], shards[1][:, :8]], t), lambda: call(X, shards, t, vocab=0),
+                lambda: call(X, shards, t, vocab=513), lambda: call(X, [w[:, :252].contiguous() for w in shards], t),
+                lambda: train(X, shards, t, weights=torch.ones(6, dtype=torch.float64, device="cuda")),
+                lambda: train(X, shards, t, weights=torch.ones(5, device="cuda")), lambda: train(X, shards, t, reduction="none"),
+                lambda: train(X, shards, t, accumulate=True, dW=[torch.zeros_like(w) for w in shards]),
+                lambda: train(X, shards, t, piece_rows=-1), lambda: train(X, shards, t, dX=wide),
+                lambda: train(X, shards, t, loss=torch.zeros(6, dtype=BF16, device="cuda"))):
+        with pytest.raises(rtp.RtpError):
+            bad()
+    with pytest.raises(TypeError):
+        train(X, shards, t, dw_dtype=torch.float16)
