@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS32) adamw_kernel(const __grid_c
 // its rows (50 M elements: 188 us, issue slots 53 % busy). A lane copies and reads its own
 // elements only, so nothing is synchronised.
 
-constexpr int STRIP8 = 4, THREADS8 = 128, WARPS8 = THREADS8 / 32, BLOCKS8 = 5;
+constexpr int STRIP8 = 4, THREADS8 = 64, WARPS8 = THREADS8 / 32, BLOCKS8 = 10;
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* shared, const void* global)
@@ -612,13 +612,14 @@ __global__ void adamw_clock_kernel(Clock* k, long long step, double beta1, doubl
 }
 
 // Values of 8-bit moments: 8 elements a thread, 16 threads a block of the format (16 a
-// thread left half of every sector to another store: 61 us for 50 M elements).
+// thread left half of every sector to another store: 61 us for 50 M elements, 49 so). Its
+// dependents are not launched early: a step's blocks, which share the work evenly, would
+// find some SMs taken (19 M elements, step and values in turn: 105 us, 92 so).
 template <bool F32>
 __global__ void __launch_bounds__(THREADS) adamw_values_kernel(const uint2* m8, const uint2* v8, const uchar2* scales, void* m,
                                                                void* v, int64_t units)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t stride = (int64_t)gridDim.x * THREADS;
 #pragma unroll 4
     for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < units; i += stride) {
