@@ -635,8 +635,9 @@ int64_t rtp_grad_workspace_bytes(int n);
  *   workspace rtp_tp_cross_entropy_workspace() bytes of device memory, 256-byte aligned;
  *             needs no preparation; not shared by calls that may overlap
  *   loss      float32 [M];  lse: float32 [M] (of every row), or NULL
- * float32 accumulation and statistics; exponentials are within 2^-21 of themselves. Up to
- * 128 rows run in the few-row kernel of rtp_tp_linear, more in its pair kernel.
+ * float32 accumulation and statistics; the exponential of a logit l is within 2^-21 +
+ * |l| 2^-23 of itself. A loss that rounding would leave below 0 is 0. Up to 128 rows run
+ * in the few-row kernel of rtp_tp_linear, more in its pair kernel.
  * Requirements (RTP_ESHAPE): V % P == 0; K and V/P multiples of 8. Alignment (X, weights
  * 16 bytes), errors, launches and M == 0 as in rtp_tp_linear; results do not change from
  * run to run.

@@ -20,6 +20,10 @@
 // The exponentials take 2 V bytes a row. Rows are taken in pieces, so that they take no
 // more than the float32 sums of dW that several pieces need (4 K V: 2 K rows), or 1 GiB.
 // With several pieces dW is summed in float32, by adds in the output's TMA stores.
+//
+// The tensor pipe bounds many rows, the weights' bytes few. Measured at 4096 x 131072 on 8
+// ranks: 8192 rows forward 5.1 ms (1730 TFLOP/s), training 15.8 to 16.5 (the power cap);
+// one row 156 us (6.9 TB/s of the weights).
 #include <algorithm>
 #include <cstring>
 
