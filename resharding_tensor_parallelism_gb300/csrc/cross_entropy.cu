@@ -368,6 +368,9 @@ int check_shape(const char* fn, int P, int64_t M, int64_t K, int64_t V, int64_t 
     if (V % P || K % 8 || (V / P) % 8)
         return fail(RTP_ESHAPE, "%s: K=%lld and a rank's columns (V=%lld over P=%d) must be multiples of 8 (16-byte rows)", fn,
                     (long long)K, (long long)V, P);
+    const double limit = 0x1p50;  // of rows or K times columns: no byte count below overflows
+    if ((double)M * (double)V > limit || (double)K * (double)V > limit)
+        return fail(RTP_ESHAPE, "%s: M=%lld, K=%lld, V=%lld are too large", fn, (long long)M, (long long)K, (long long)V);
     if (vocab < 1 || vocab > V) return fail(RTP_ESHAPE, "%s: vocab=%lld outside [1, V=%lld]", fn, (long long)vocab, (long long)V);
     if (piece_rows < 0) return fail(RTP_EINVAL, "%s: piece_rows=%lld", fn, (long long)piece_rows);
     s->P = P, s->M = M, s->K = K, s->V = V, s->vocab = vocab, s->Vp = V / P;

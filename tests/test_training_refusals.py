@@ -23,7 +23,8 @@ def _p(n, base=0x100000):
 COMMON = [
     (dict(P=0), EUNSUPPORTED), (dict(P=9), EUNSUPPORTED), (dict(M=-1), ESHAPE), (dict(M=1 << 31), ESHAPE), (dict(K=0), ESHAPE),
     (dict(K=12), ESHAPE), (dict(V=33), ESHAPE), (dict(V=24), ESHAPE), (dict(V=0), ESHAPE), (dict(vocab=0), ESHAPE),
-    (dict(vocab=33), ESHAPE), (dict(X=None), EINVAL), (dict(X=4104), EINVAL), (dict(W=None), EINVAL),
+    (dict(vocab=33), ESHAPE), (dict(M=1 << 24, V=1 << 30), ESHAPE),
+    (dict(K=1 << 24, V=1 << 30), ESHAPE), (dict(X=None), EINVAL), (dict(X=4104), EINVAL), (dict(W=None), EINVAL),
     (dict(W=rtp._ptrs([4096, 0])), EINVAL), (dict(W=rtp._ptrs([4096, 8200])), EINVAL), (dict(wide=2), EINVAL),
     (dict(targets=None), EINVAL), (dict(targets=4100), EINVAL), (dict(targets=4098, wide=0), EINVAL), (dict(ws=None), EINVAL),
     (dict(ws=0x10010), EINVAL), (dict(bytes=16), EINVAL), (dict(loss=None), EINVAL), (dict(loss=4097), EINVAL)]
