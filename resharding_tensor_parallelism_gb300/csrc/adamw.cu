@@ -19,9 +19,9 @@
 // 8-bit moments (128 elements share a power of two; an exponent byte E of the block's
 // largest absolute value, at least 27, as in a float32; 255: everything is NaN):
 //   m  sign, 4 bits of exponent, 3 of mantissa: value (1 + M/8) 2^(e-7), e = 0: M/8 2^-6,
-//      times 2^(E-134): the largest has the exponent 7, 2^-17.8 of it is the least
+//      times 2^(E-134): the largest has the exponent 7, the least is 2^-16 to 2^-17 of it
 //   v  5 bits of exponent, 3 of mantissa: (1 + M/8) 2^(e-15), e = 0: M/8 2^-14, times
-//      2^(E-142): down to 2^-33 of the largest; what is not zero never becomes zero, or
+//      2^(E-142): the least is 2^-32 to 2^-33 of the largest; what is not zero never becomes zero, or
 //      the next step would divide by eps
 // Values are rounded up or down at random, with the probabilities that keep the mean
 // (rounding to nearest would leave v as it is: a step changes it by 1 - b2, less than
