@@ -145,7 +145,7 @@ def prepare(case, seed):
     s["p"] = wide if case["param"] == "f32" else wide.to(BF16)
     s["master"] = wide if case["param"] == "master" else None
     kinds = _kinds(case)
-    grads = {kind: normal((total,), 1e-3, kind) for kind in dict.fromkeys(kinds)}
+    grads = {kind: normal((total,), 1e-3, kind) for kind in set(kinds)}
     s["g"] = [views(grads[kind])[i] for i, kind in enumerate(kinds)]
     for kind, g in grads.items():
         g.mul_(used & torch.tensor([k is kind for k in kinds], device="cuda")[s["owner"]])
