@@ -211,15 +211,16 @@ __global__ void __launch_bounds__(1024) loss_scale_kernel(const void* targets, i
     if (!alone) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(1024) loss_total_kernel(const float* loss, const float* weights, int64_t rows, int mean,
+__global__ void __launch_bounds__(1024) loss_total_kernel(const float* loss, const void* targets, int targets64,
+                                                          const float* weights, int64_t rows, int64_t ignore, int mean,
                                                           const Shared* sh, float* total, int alone)
 {
     if (alone) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     double s = 0.0;
     for (int64_t r = threadIdx.x; r < rows; r += 1024) {
-        const float w = weights ? __ldcg(weights + r) : 1.0f;
-        if (w != 0.0f) s += (double)w * (double)__ldcg(loss + r);  // ignored rows: 0
+        const float w = weights ? __ldcg(weights + r) : 1.0f;  // an ignored row's may be anything
+        if (w != 0.0f && target_at(targets, targets64, r) != ignore) s += (double)w * (double)__ldcg(loss + r);
     }
     s = block_sum_1024(s);
     if (threadIdx.x == 0) {
@@ -552,7 +553,8 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
     }
     auto sum_up = [&](int piece, int alone) {  // behind the last piece's losses
         if (piece < s.pieces - 1) return (int)RTP_OK;
-        return launch(fn, loss_total_kernel, dim3(1), 1024, stream, (const float*)loss, weights, s.M, mean, (const Shared*)sh, total, alone);
+        return launch(fn, loss_total_kernel, dim3(1), 1024, stream, (const float*)loss, c.targets, c.targets64, weights, s.M, c.ignore,
+                      mean, (const Shared*)sh, total, alone);
     };
     for (int p = 0; p < s.pieces; ++p) {
         const int64_t first = p * s.piece, rows = std::min(s.piece, s.M - first);

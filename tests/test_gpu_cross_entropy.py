@@ -356,3 +356,21 @@ def test_refusals_of_the_binding():
             bad()
     with pytest.raises(TypeError):
         train(X, shards, t, dw_dtype=torch.float16)
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum"])
+@pytest.mark.parametrize("M,piece", [(4, 0), (300, 0), (600, 256)])
+def test_weights_of_ignored_rows_hold_anything(M, piece, reduction):
+    """NaN, infinite and huge weights in ignored rows (a quotient over padded rows is 0 / 0) change nothing."""
+    X, W, shards, t = _inputs(M, 64, 512, 2, 512, ignored=0.0, seed=19)
+    w = torch.rand((M,), device="cuda") + 0.5
+    bad = [0, 2, M - 2][:M - 1]
+    t[bad] = IGNORE
+    w[bad] = 1.0
+    call = lambda: rtp.tp_cross_entropy_train(X, shards, t, weights=w, ignore_index=IGNORE, reduction=reduction, piece_rows=piece)
+    want = call()
+    assert torch.isfinite(want[0])
+    for value in (float("nan"), float("inf"), -float("inf"), 3e38):
+        w[bad] = value
+        got = call()
+        assert all(torch.equal(a, b) for a, b in zip([*got[:3], *got[3]], [*want[:3], *want[3]])), value
