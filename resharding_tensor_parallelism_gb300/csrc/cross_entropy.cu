@@ -329,6 +329,10 @@ struct Shape {
 int part_cols(int64_t rows) { return rows <= LIN_FEW_ROWS ? LIN_FEW_COLS : LIN_TILE_COLS; }
 int64_t parts(const Shape& s, int64_t rows) { return s.P * ((s.Vp + part_cols(rows) - 1) / part_cols(rows)); }
 
+// Columns of rank i that are in the vocabulary. The products for dX go no further: the exponentials behind are 0, but
+// the weights there may be anything, and 0 times an infinity or a NaN is a NaN.
+int64_t rank_columns(const Shape& s, int i) { return std::max<int64_t>(0, std::min(s.Vp, s.vocab - i * s.Vp)); }
+
 // Slices of each rank's columns whose products for dX are summed by a kernel of their own
 // (0: none, all ranks in one accumulator). dX of few rows and a narrow model has few tiles,
 // each the product of the whole vocabulary, which a cluster shares four ways at most:
@@ -570,7 +574,7 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
         const int slices = dx_slices(s, rows);
         if (dX && slices) {
             LinGemm g;
-            g.groups = s.P * slices;
+            g.groups = 0;
             g.b_t = true;
             g.out_f32 = true;
             g.rows = rows;
@@ -579,13 +583,14 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
             g.lda = s.lde;
             g.ldb = s.Vp;
             float* products = reinterpret_cast<float*>(c.ws + c.space.slices);
-            for (int i = 0; i < g.groups; ++i) {
-                const int64_t col = i % slices * g.kdim;
-                g.A[i] = a.e[i / slices] + col;
-                g.B[i] = static_cast<const __nv_bfloat16*>(c.W[i / slices]) + col;
-                g.kdims[i] = std::min(g.kdim, s.Vp - col);
-                g.out[i] = products + i * rows * s.K;
-            }
+            for (int i = 0; i < s.P; ++i)
+                for (int64_t col = 0; col < rank_columns(s, i); col += g.kdim) {
+                    const int at = g.groups++;
+                    g.A[at] = a.e[i] + col;
+                    g.B[at] = static_cast<const __nv_bfloat16*>(c.W[i]) + col;
+                    g.kdims[at] = std::min(g.kdim, rank_columns(s, i) - col);
+                    g.out[at] = products + at * rows * s.K;
+                }
             TRY(launch_linear_gemm(fn, g, stream));
             TRY(sum_up(p, 0));
             const SliceArgs b = {reinterpret_cast<const float4*>(products), a.factor, static_cast<char*>(dX) + first * s.K * dx_size,
@@ -594,7 +599,7 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
             TRY(launch(fn, dx_dtype == RTP_F32 ? slices_kernel<true> : slices_kernel<false>, dim3(blocks), THREADS, stream, b));
         } else if (dX) {
             LinGemm g;
-            g.groups = s.P;
+            g.groups = 0;
             g.fused = true;
             g.b_t = true;
             g.out_f32 = dx_dtype == RTP_F32;
@@ -602,10 +607,13 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
             g.cols = s.K;
             g.kdim = s.Vp;
             for (int i = 0; i < s.P; ++i) {
-                g.A[i] = a.e[i];
-                g.B[i] = c.W[i];
+                if (!rank_columns(s, i)) continue;
+                g.A[g.groups] = a.e[i];
+                g.B[g.groups] = c.W[i];
+                g.kdims[g.groups++] = rank_columns(s, i);
             }
             g.lda = s.lde;
+            g.ldb = s.Vp;
             g.row_scale = a.factor;
             g.out[0] = static_cast<char*>(dX) + first * s.K * dx_size;
             TRY(launch_linear_gemm(fn, g, stream));

@@ -374,3 +374,25 @@ def test_weights_of_ignored_rows_hold_anything(M, piece, reduction):
         w[bad] = value
         got = call()
         assert all(torch.equal(a, b) for a, b in zip([*got[:3], *got[3]], [*want[:3], *want[3]])), value
+
+
+# padding inside a tile, from the middle of a rank on, over whole ranks, with dX in slices of the vocabulary, in pieces
+@pytest.mark.parametrize("M,K,V,P,vocab,piece", [
+    (3, 64, 512, 2, 509, 0), (100, 64, 768, 3, 300, 0), (300, 64, 512, 2, 500, 0), (300, 136, 2064, 2, 1000, 0),
+    (257, 200, 2048, 8, 257, 0), (129, 72, 1048, 1, 1, 0), (256, 512, 8192, 2, 8131, 0), (256, 512, 8192, 2, 4000, 0),
+    (300, 264, 24600, 3, 9001, 0), (600, 136, 1056, 2, 1001, 256)])
+def test_padding_columns_hold_anything(M, K, V, P, vocab, piece):
+    """Columns of the weights from `vocab` on take no part: not NaN, not infinities, nor the largest values."""
+    X, W, _, t = _inputs(M, K, V, P, vocab, seed=20)
+    call = lambda: rtp.tp_cross_entropy_train(X, [w.contiguous() for w in W.chunk(P, 1)], t, vocab=vocab, ignore_index=IGNORE,
+                                              piece_rows=piece)
+    W[:, vocab:] = 0.0
+    want = call()
+    _check_train(X, W, t, vocab, want)
+    for value in (float("nan"), float("inf"), -3.38e38):
+        W[:, vocab:] = value
+        got = call()
+        assert all(torch.equal(a, b) for a, b in zip([*got[:3], *got[3]], [*want[:3], *want[3]])), value
+        loss, lse = rtp.tp_cross_entropy(X, [w.contiguous() for w in W.chunk(P, 1)], t, vocab=vocab, ignore_index=IGNORE)
+        assert torch.isfinite(loss).all() and torch.isfinite(lse).all()
+    assert rtp.device_error() == 0
