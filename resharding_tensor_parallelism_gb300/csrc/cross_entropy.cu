@@ -382,7 +382,8 @@ int check_shape(const char* fn, int P, int64_t M, int64_t K, int64_t V, int64_t 
     s->lde = up(s->Vp, 64), s->ldx = up(K, 64);
     // As many rows as the head of this file allows, in pieces of about the same size;
     // whole row tiles, so that only the last piece ends inside one.
-    const int64_t most = up(piece_rows ? piece_rows : std::max({2 * K, (int64_t)2048, ((int64_t)1 << 29) / V}), LIN_TILE_ROWS);
+    const int64_t wanted = piece_rows ? piece_rows : std::max({2 * K, (int64_t)2048, ((int64_t)1 << 29) / V});
+    const int64_t most = up(std::min(wanted, std::max<int64_t>(M, 1)), LIN_TILE_ROWS);
     s->pieces = train && M > most ? (int)((M + most - 1) / most) : 1;
     s->piece = s->pieces > 1 ? up((M + s->pieces - 1) / s->pieces, LIN_TILE_ROWS) : M;
     if (s->pieces > 1) s->pieces = (int)((M + s->piece - 1) / s->piece);

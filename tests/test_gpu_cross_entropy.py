@@ -396,3 +396,12 @@ def test_padding_columns_hold_anything(M, K, V, P, vocab, piece):
         loss, lse = rtp.tp_cross_entropy(X, [w.contiguous() for w in W.chunk(P, 1)], t, vocab=vocab, ignore_index=IGNORE)
         assert torch.isfinite(loss).all() and torch.isfinite(lse).all()
     assert rtp.device_error() == 0
+
+
+@pytest.mark.parametrize("M", [5, 600])
+def test_a_piece_of_more_rows_than_there_are(M):
+    X, W, shards, t = _inputs(M, 64, 512, 2, 512, seed=23)
+    want = rtp.tp_cross_entropy_train(X, shards, t, ignore_index=IGNORE, piece_rows=M)
+    for piece in (1 << 31, (1 << 63) - 1):
+        got = rtp.tp_cross_entropy_train(X, shards, t, ignore_index=IGNORE, piece_rows=piece)
+        assert all(torch.equal(a, b) for a, b in zip([*got[:3], *got[3]], [*want[:3], *want[3]]))

@@ -131,3 +131,14 @@ def test_binding_checks_before_any_launch():
                  lambda: rtp.AdamWGroup([torch.zeros(4)])):
         with pytest.raises(rtp.RtpError):
             call()
+
+
+@pytest.mark.parametrize("M", [1, 600, 70000])
+def test_workspace_of_a_piece_of_more_rows_than_there_are(M):
+    n = ctypes.c_int64()
+    size = lambda piece, dw: (rtp.lib().rtp_tp_cross_entropy_workspace(2, M, 64, 1024, piece, 1, dw, ctypes.byref(n)), n.value)
+    for dw in (0, 1):
+        want = size(M, dw)
+        assert want[0] == 0
+        for piece in (M + 1, 1 << 31, (1 << 63) - 300, (1 << 63) - 1):
+            assert size(piece, dw) == want, piece
