@@ -405,3 +405,21 @@ def test_a_piece_of_more_rows_than_there_are(M):
     for piece in (1 << 31, (1 << 63) - 1):
         got = rtp.tp_cross_entropy_train(X, shards, t, ignore_index=IGNORE, piece_rows=piece)
         assert all(torch.equal(a, b) for a, b in zip([*got[:3], *got[3]], [*want[:3], *want[3]]))
+
+
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("M,K,V,P,piece", [(7, 200, 1040, 2, 0), (300, 200, 1040, 2, 0), (256, 512, 8192, 2, 0),
+                                           (600, 136, 1056, 2, 256)])
+def test_rows_do_not_meet(M, K, V, P, piece, far):
+    """Other rows, of ordinary logits or of some hundreds, leave a row's loss and gradient as they are, bit for bit."""
+    X, W, shards, t = _inputs(M, K, V, P, V, seed=21)
+    Y, _, _, u = _inputs(M, K, V, P, V, seed=22, spread=100.0 if far else 1.0)
+    keep = torch.rand((M,), device="cuda") < 0.5
+    keep[0], keep[M // 2] = True, False
+    Y[keep], u[keep] = X[keep], t[keep]
+    assert not torch.equal(X, Y)
+    train = lambda x, y: rtp.tp_cross_entropy_train(x, shards, y, ignore_index=IGNORE, reduction="sum", piece_rows=piece)
+    for a, b in zip(train(X, t)[1:3], train(Y, u)[1:3]):
+        assert torch.equal(a[keep], b[keep]) and not torch.equal(a, b)
+    for a, b in zip(*(rtp.tp_cross_entropy(x, shards, y, ignore_index=IGNORE) for x, y in ((X, t), (Y, u)))):
+        assert torch.equal(a[keep], b[keep]) and not torch.equal(a, b)
