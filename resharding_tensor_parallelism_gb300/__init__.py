@@ -1228,8 +1228,8 @@ class AdamWGroup:
     """AdamW over a program's weights (rank pieces, float32 and bf16 mixed), all of them in one pass.
 
     weight_decay: one for all, or one per tensor. masters: float32 copies that bf16 weights are updated through, one per
-    tensor (None for a tensor without), or True for copies that the group makes; a bf16 weight without one is rounded at
-    random, so that small steps are not lost. states: bits of the moments, 32 or 8 (blocks of 128 elements share a power of
+    tensor (None for a tensor without), or True for copies that the group makes and holds in its state; a bf16 weight without
+    one is rounded at random, so that small steps are not lost. states: bits of the moments, 32 or 8 (blocks of 128 elements share a power of
     two, values are rounded at random; see rtp_adamw_step in rtp.h). seed: of the random bits.
 
     The group keeps the tensors and, in one flat buffer each, the moments (exp_avg, exp_avg_sq: float32, or codes with
@@ -1260,19 +1260,15 @@ class AdamWGroup:
             self._check(fn, "params", i, p)
         with _allocating_on(stream):
             self.masters = self._masters(fn, masters)
-            self.offsets = [0]
-            for p in self.params:
-                self.offsets.append(self.offsets[-1] + (p.numel() + ADAMW_BLOCK - 1) // ADAMW_BLOCK * ADAMW_BLOCK)
-            total = self.offsets.pop()
+            self.offsets, total = self._places(self.params)
             flat = dict(dtype=torch.float32 if states == 32 else torch.uint8, device=self.device)
             self.exp_avg, self.exp_avg_sq = torch.zeros(total, **flat), torch.zeros(total, **flat)
             self.scales = torch.zeros((total // ADAMW_BLOCK, 2), **flat) if states == 8 else None
             self._clock = torch.zeros(_ADAMW_CLOCK_BYTES // 8, dtype=torch.int64, device=self.device)
             self.steps = self._clock[0]
             self._set_clock(0, None)
-            self._own = [t for t in (self.exp_avg, self.exp_avg_sq, self.scales, self._clock) if t is not None]
             # copies that the group made belong to it, as its state does
-            self._own += [m for m in self.masters if m is not None and masters is True]
+            self._own = [t for t in (self.exp_avg, self.exp_avg_sq, self.scales, self._clock, self._copies) if t is not None]
             self._joined = {torch._C._cuda_getCurrentRawStream(self._index) or None}
             self._ready = None
             if not torch.cuda.is_current_stream_capturing():
@@ -1289,13 +1285,37 @@ class AdamWGroup:
         if t.numel() and (t.device != self.device or not t.is_contiguous()):
             raise RtpError(-1, "%s: %s[%d] must be contiguous and on %s" % (fn, name, i, self.device))
 
+    @staticmethod
+    def _places(tensors):
+        """(where each tensor begins in a flat buffer of whole blocks, the buffer's elements)"""
+        at = [0]
+        for t in tensors:
+            at.append(at[-1] + (t.numel() + ADAMW_BLOCK - 1) // ADAMW_BLOCK * ADAMW_BLOCK)
+        return at[:-1], at[-1]
+
+    def _copies_in(self, flat):
+        """For each tensor its float32 copy in a flat buffer of the copies of all bf16 weights, None for float32 ones."""
+        narrow = [p for p in self.params if p.dtype is _torch().bfloat16]
+        places = iter(self._places(narrow)[0])
+        return [flat[at:at + p.numel()].view(p.shape) if at is not None else None for p, at in (
+            (p, next(places) if p.dtype is _torch().bfloat16 else None) for p in self.params)]
+
     def _masters(self, fn, masters):
         torch = _torch()
         n = len(self.params)
+        self._copies = None  # the flat buffer of the copies that the group makes
         if masters is None or masters is False:
             return [None] * n
         if masters is True:
-            return [p.detach().float() if p.dtype is torch.bfloat16 else None for p in self.params]
+            narrow = [p for p in self.params if p.dtype is torch.bfloat16]
+            if not narrow:
+                return [None] * n
+            self._copies = torch.zeros(self._places(narrow)[1], dtype=torch.float32, device=self.device)
+            masters = self._copies_in(self._copies)
+            for m, p in zip(masters, self.params):
+                if m is not None:
+                    m.copy_(p.detach())
+            return masters
         masters = list(masters)
         if len(masters) != n:
             raise RtpError(-1, "%s: %d masters for %d tensors" % (fn, len(masters), n))
@@ -1393,29 +1413,49 @@ class AdamWGroup:
         return m, v
 
     def state_dict(self) -> dict:
-        """The state, for load_state_dict: "step" (an int: waits for the GPU), "exp_avg", "exp_avg_sq" and, of 8-bit states,
-        "scales": the group's own buffers, not copies."""
+        """The state, for load_state_dict: "step" (an int: waits for the GPU), "exp_avg", "exp_avg_sq", of 8-bit states
+        "scales", and "masters", flat, if the group made its float32 copies: the group's own buffers, not copies. The weights,
+        and float32 copies that the caller gave, are the caller's to keep."""
         got = {"step": int(self.steps), "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq}
-        return got if self.scales is None else {**got, "scales": self.scales}
+        if self.scales is not None:
+            got["scales"] = self.scales
+        if self._copies is not None:
+            got["masters"] = self._copies
+        return got
 
     def load_state_dict(self, state: dict) -> None:
         """Copies a state_dict of a group over tensors of the same sizes into this one's buffers, on the current stream
-        (steps on other streams must be ordered after it by the caller). betas are this group's own."""
+        (steps on other streams must be ordered with it by the caller). A group that made its float32 copies needs a state
+        that holds them; one that was given copies of all its bf16 weights takes them where the state has them. betas and
+        seed are this group's own, and so are the weights, which the next step sets from their copies."""
         fn = "AdamWGroup.load_state_dict"
+        torch = _torch()
         names = ["exp_avg", "exp_avg_sq"] + (["scales"] if self.states == 8 else [])
-        if set(state) != set(names + ["step"]):
-            raise RtpError(-1, "%s: keys %s, expected %s" % (fn, sorted(state), sorted(names + ["step"])))
-        for name in names:
-            own, t = getattr(self, name), state[name]
-            if t.shape != own.shape or t.dtype is not own.dtype:
-                raise RtpError(-2, "%s: %s is %s %s, expected %s %s" % (fn, name, t.dtype, tuple(t.shape), own.dtype,
-                                                                      tuple(own.shape)))
+        narrow = [p for p in self.params if p.dtype is torch.bfloat16]
+        complete = narrow and all(m is not None for m, p in zip(self.masters, self.params) if p.dtype is torch.bfloat16)
+        copies = self._copies is not None or ("masters" in state and complete)
+        wanted = names + ["step"] + (["masters"] if copies else [])
+        if set(state) != set(wanted):
+            raise RtpError(-1, "%s: keys %s, expected %s" % (fn, sorted(state), sorted(wanted)))
+        expected = {name: (getattr(self, name).dtype, tuple(getattr(self, name).shape)) for name in names}
+        if copies:
+            expected["masters"] = torch.float32, (self._places(narrow)[1],)
+        for name, (dtype, shape) in expected.items():
+            t = state[name]
+            if tuple(t.shape) != shape or t.dtype is not dtype:
+                raise RtpError(-2, "%s: %s is %s %s, expected %s %s" % (fn, name, t.dtype, tuple(t.shape), dtype, shape))
         step = int(state["step"])
         if step < 0:
             raise RtpError(-1, "%s: step %d" % (fn, step))
         handle = self._begin(None)
         for name in names:
             getattr(self, name).copy_(state[name])
+        if self._copies is not None:
+            self._copies.copy_(state["masters"])
+        elif copies:
+            for m, t in zip(self.masters, self._copies_in(state["masters"])):
+                if t is not None:
+                    m.detach().copy_(t)
         self._set_clock(step, handle)
 
 

@@ -420,3 +420,64 @@ def test_two_groups_at_once():
     for a, b in zip(want, got):
         assert int(b.steps) == 6
         assert all(torch.equal(x, y) for x, y in zip([*a.params, *a.masters, *a.moments()], [*b.params, *b.masters, *b.moments()]))
+
+
+def _trained(states, mixed, seed=50):
+    sizes = [700, 33, 1]
+    params = _tensors(sizes, BF16, None, seed)
+    if mixed:
+        params[1] = params[1].float()
+    group = rtp.AdamWGroup(params, lr=1e-5, states=states, seed=3, masters=True)  # steps far below a bf16 spacing
+    for t in range(2):
+        group.step(_tensors(sizes, F32, None, seed + 1 + t))
+    return group, sizes
+
+
+def _alike(a, b):
+    for x, y in zip([*a.params, *(m for m in a.masters if m is not None), *a.moments()],
+                    [*b.params, *(m for m in b.masters if m is not None), *b.moments()]):
+        assert torch.equal(x, y)
+    assert int(a.steps) == int(b.steps)
+
+
+@pytest.mark.parametrize("mixed", [False, True])
+@pytest.mark.parametrize("states", [32, 8])
+def test_a_state_holds_the_copies_that_the_group_made(states, mixed):
+    """Weights and state_dict are all that goes from one group to another, or back into the same one."""
+    a, sizes = _trained(states, mixed)
+    weights = [p.clone() for p in a.params]
+    state = {k: v if isinstance(v, int) else v.clone() for k, v in a.state_dict().items()}
+    b = rtp.AdamWGroup([p.clone() for p in weights], lr=1e-5, states=states, seed=3, masters=True)
+    b.load_state_dict({k: v if isinstance(v, int) else v.cpu() for k, v in state.items()})
+    _alike(a, b)
+    grads = _tensors(sizes, F32, None, 60)
+    for group in (a, b):
+        group.step(grads)
+    _alike(a, b)
+    for p, w in zip(a.params, weights):  # back to the saved point
+        p.copy_(w)
+    a.load_state_dict(state)
+    a.step(grads)
+    _alike(a, b)
+
+
+def test_states_whose_copies_do_not_fit_are_refused():
+    a, sizes = _trained(32, False)
+    state = a.state_dict()
+    without = {k: v for k, v in state.items() if k != "masters"}
+    plain_group = rtp.AdamWGroup([p.clone() for p in a.params])
+    for group, bad in ((a, without), (a, {**state, "masters": state["masters"][:5]}),
+                       (a, {**state, "masters": state["masters"].to(BF16)}), (plain_group, state)):
+        kept = [t.clone() for t in (group.exp_avg, *group.params)]
+        with pytest.raises(rtp.RtpError):
+            group.load_state_dict(bad)
+        assert all(torch.equal(x, y) for x, y in zip(kept, (group.exp_avg, *group.params)))
+    # copies that the caller gave are the caller's own: in no state, and brought up to one that has them
+    own = [m.clone() for m in a.masters]
+    given = rtp.AdamWGroup([p.clone() for p in a.params], masters=own)
+    assert set(given.state_dict()) == {"step", "exp_avg", "exp_avg_sq"}
+    given.load_state_dict(without)
+    for m in own:
+        m.zero_()
+    given.load_state_dict(state)
+    assert all(torch.equal(x, y) for x, y in zip(own, a.masters))
