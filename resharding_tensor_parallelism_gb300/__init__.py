@@ -1413,9 +1413,10 @@ class AdamWGroup:
         return m, v
 
     def state_dict(self) -> dict:
-        """The state, for load_state_dict: "step" (an int: waits for the GPU), "exp_avg", "exp_avg_sq", of 8-bit states
-        "scales", and "masters", flat, if the group made its float32 copies: the group's own buffers, not copies. The weights,
-        and float32 copies that the caller gave, are the caller's to keep."""
+        """The state, for load_state_dict: "step" (an int: waits for the GPU, for steps on every stream), "exp_avg",
+        "exp_avg_sq", of 8-bit states "scales", and "masters", flat, if the group made its float32 copies: the group's own
+        buffers, not copies. The weights, and float32 copies that the caller gave, are the caller's to keep."""
+        _torch().cuda.synchronize(self.device)
         got = {"step": int(self.steps), "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq}
         if self.scales is not None:
             got["scales"] = self.scales

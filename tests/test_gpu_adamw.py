@@ -481,3 +481,14 @@ def test_states_whose_copies_do_not_fit_are_refused():
         m.zero_()
     given.load_state_dict(state)
     assert all(torch.equal(x, y) for x, y in zip(own, a.masters))
+
+
+def test_a_state_waits_for_steps_on_every_stream():
+    params = [torch.zeros(50_000_000, device="cuda")]
+    group = rtp.AdamWGroup(params, states=8)
+    grads = [torch.ones_like(params[0])]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        group.step(grads, stream=s)
+    assert group.state_dict()["step"] == 20
