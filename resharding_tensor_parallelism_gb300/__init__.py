@@ -1375,12 +1375,16 @@ class AdamWGroup:
         lr = self.lr if lr is None else lr
         if type(lr) is int:
             lr = float(lr)
-        if _called((_ext or _tables()).adamw(self._table_at, len(self.params), self.params, self.masters, grads, self.states,
+        if _called((_ext or _tables()).adamw(self._table_at, len(self._numels), self.params, self.masters, grads, self.states,
                                              lr, self.eps, norm, float(max_norm), self.seed, self._clock_at, self._index,
                                              handle or 0)):
             return
-        if len(grads) != len(self.params):
-            raise RtpError(-1, "%s: %d gradients for %d tensors" % (fn, len(grads), len(self.params)))
+        n = len(self._numels)
+        if len(self.params) != n or len(self.masters) != n:
+            raise RtpError(-1, "%s: %d params and %d masters, the group was built over %d tensors" % (
+                fn, len(self.params), len(self.masters), n))
+        if len(grads) != n:
+            raise RtpError(-1, "%s: %d gradients for %d tensors" % (fn, len(grads), n))
         for i, (t, p, m, g) in enumerate(zip(self._table, self.params, self.masters, grads)):
             self._check(fn, "params", i, p)
             if p.numel() != self._numels[i]:
@@ -1390,7 +1394,9 @@ class AdamWGroup:
             t.param, t.param_dtype = p.data_ptr() or None, _dtype_code(p)
             if m is not None:
                 self._check(fn, "masters", i, m, p)
-                t.master = m.data_ptr() or None
+                if m.dtype is not _torch().float32:
+                    raise RtpError(-1, "%s: masters[%d] must be float32" % (fn, i))
+            t.master = None if m is None else m.data_ptr() or None
             t.grad, t.grad_dtype = g.data_ptr() or None, _dtype_code(g)
         at = None
         if isinstance(lr, _torch().Tensor):

@@ -492,3 +492,28 @@ def test_a_state_waits_for_steps_on_every_stream():
     for _ in range(20):
         group.step(grads, stream=s)
     assert group.state_dict()["step"] == 20
+
+
+def test_tensors_that_are_not_what_the_group_was_built_over():
+    """More or fewer tensors than the group's table holds, and copies of another type, are refused; a copy that is gone is
+    not written."""
+    make = lambda: rtp.AdamWGroup(_tensors([64, 9], BF16, None, 70), masters=True, lr=LR)
+    grads = _tensors([64, 9, 5], F32, None, 71)
+    for change, n in ((lambda g: (g.params.append(grads[2].clone()), g.masters.append(None)), 3),
+                      (lambda g: g.params.append(grads[2].clone()), 3),
+                      (lambda g: (g.params.pop(), g.masters.pop()), 1), (lambda g: g.masters.pop(), 2),
+                      (lambda g: g.masters.__setitem__(0, g.masters[0].to(BF16)), 2),
+                      (lambda g: g.masters.__setitem__(0, None), 1)):
+        group = make()
+        change(group)
+        kept = [p.clone() for p in group.params]
+        with pytest.raises(rtp.RtpError):
+            group.step(grads[:n])
+        assert int(group.steps) == 0 and all(torch.equal(a, b) for a, b in zip(kept, group.params))
+    for lr in (LR, torch.tensor(LR, device="cuda")):
+        group = make()
+        copy = group.masters[0]
+        kept = copy.clone()
+        group.masters[0] = None
+        group.step(grads[:2], lr=lr)
+        assert torch.equal(copy, kept) and int(group.steps) == 1
