@@ -218,12 +218,38 @@ __device__ __forceinline__ float sqrt_fast(float x)
     asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float sqrt_ftz(float x)
+{
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 
 // What a step has read from the device, and its launch's arguments.
 struct Rates {
     float beta1, beta2, rest1, rest2, correct2, lr, rate, clip, eps;
     uint32_t seed, step;
 };
+
+// A weight behind its moments. The second form goes with the blocks of 8-bit moments whose exponents are
+// no larger than these: it takes fewer instructions, and the denominator is formed times 2^32, so that no v but 0
+// counts as zero. Which of them a weight takes depends on its values alone, not on its place in memory: replicas
+// that are given the same stay the same.
+constexpr int MOST_M = 140, MOST_V = 156;
+__device__ __forceinline__ float updated(float x, float keep, float m, float v, const Rates& s)
+{
+    return fmaf(x, keep, -s.rate * __fdividef(m, sqrt_fast(v * s.correct2) + s.eps));
+}
+__device__ __forceinline__ float updated_scaled(float x, float keep, float m, float v, const Rates& s)
+{
+    return fmaf(x, keep, s.rate * -0x1p32f * m * rcp_ftz(sqrt_ftz(v * (s.correct2 * 0x1p64f)) + s.eps * 0x1p32f));
+}
 
 // One row of any types, alignment and length.
 template <bool BITS8>
@@ -236,12 +262,14 @@ __device__ __noinline__ void any_row(const Item& it, int64_t row, const Rates& s
     const uint32_t key = pcg(pcg(pcg(s.seed) + it.id) + s.step);
     const float keep = 1.0f - s.lr * it.decay;
     float x[4], dx[4], m[4], v[4];
+    bool scaled = BITS8;
     floats(it.master ? load4(it.master, false, at, n, vec) : load4(it.param, pb, at, n, vec), pb && !it.master, x);
     floats(load4(it.grad, gb, at, n, vec), gb, dx);
     if constexpr (BITS8) {
         const uint32_t mw = load_codes(it.m, at, n, vec), vw = load_codes(it.v, at, n, vec);
         const uchar2 scales = __ldcs(it.scales + row / ROW);
         const float ms = block_scale(scales.x, 134), vs = block_scale(scales.y, 142);
+        scaled = scales.x <= MOST_M && scales.y <= MOST_V;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             m[j] = decode_m(mw >> 8 * j & 255u, ms);
@@ -252,19 +280,13 @@ __device__ __noinline__ void any_row(const Item& it, int64_t row, const Rates& s
         floats(load4(it.m, false, at, n, vec), false, m);
         floats(load4(it.v, false, at, n, vec), false, v);
     }
-    uint32_t noise[4], b[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float d = dx[j] * s.clip;
         m[j] = BITS8 ? __fadd_rn(__fmul_rn(s.beta1, m[j]), __fmul_rn(s.rest1, d)) : fmaf(s.beta1, m[j], s.rest1 * d);
         v[j] = BITS8 ? __fadd_rn(__fmul_rn(s.beta2, v[j]), __fmul_rn(__fmul_rn(s.rest2, d), d)) : fmaf(s.beta2, v[j], s.rest2 * d * d);
-        x[j] = fmaf(x[j], keep, -s.rate * __fdividef(m[j], sqrt_fast(v[j] * s.correct2) + s.eps));
-        noise[j] = pcg((uint32_t)at + (uint32_t)j + key);
-        b[j] = it.master ? round_bf16(x[j]) : round_bf16_at_random(x[j], pcg(noise[j]) & 0xFFFFu);
     }
-    if (it.master) store_f32(it.master, at, n, vec, x);
-    if (pb) store_16(it.param, at, n, vec, b);
-    else store_f32(it.param, at, n, vec, x);
+    int me = 0, ve = 0;  // exponents of the block's largest
     if constexpr (BITS8) {
         uint32_t mt = 0u, vt = 0u;
 #pragma unroll
@@ -272,8 +294,21 @@ __device__ __noinline__ void any_row(const Item& it, int64_t row, const Rates& s
             mt = max(mt, j < n ? __float_as_uint(fabsf(m[j])) : 0u);
             vt = max(vt, j < n ? __float_as_uint(fabsf(v[j])) : 0u);
         }
-        const int me = max((int)(__reduce_max_sync(0xffffffffu, mt) >> 23), LEAST_EXPONENT);
-        const int ve = max((int)(__reduce_max_sync(0xffffffffu, vt) >> 23), LEAST_EXPONENT);
+        me = max((int)(__reduce_max_sync(0xffffffffu, mt) >> 23), LEAST_EXPONENT);
+        ve = max((int)(__reduce_max_sync(0xffffffffu, vt) >> 23), LEAST_EXPONENT);
+        scaled = scaled && me <= MOST_M && ve <= MOST_V;
+    }
+    uint32_t noise[4], b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[j] = scaled ? updated_scaled(x[j], keep, m[j], v[j], s) : updated(x[j], keep, m[j], v[j], s);
+        noise[j] = pcg((uint32_t)at + (uint32_t)j + key);
+        b[j] = it.master ? round_bf16(x[j]) : round_bf16_at_random(x[j], pcg(noise[j]) & 0xFFFFu);
+    }
+    if (it.master) store_f32(it.master, at, n, vec, x);
+    if (pb) store_16(it.param, at, n, vec, b);
+    else store_f32(it.param, at, n, vec, x);
+    if constexpr (BITS8) {
         const float ms = power_of_two(261 - me), vs = power_of_two(269 - ve);  // 2^(134 - E), 2^(142 - E)
         uint32_t mc = 0u, vc = 0u;
 #pragma unroll
@@ -298,18 +333,6 @@ __device__ __forceinline__ float max_nan(float a, float b)
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-__device__ __forceinline__ float sqrt_ftz(float x)
-{
-    float r;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float rcp_ftz(float x)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 // Whole, aligned rows of 8-bit moments: the row's update in as few instructions as the
 // format allows (in the form of any_row, 200 an element, the arithmetic took 2.3 times as
@@ -317,9 +340,7 @@ __device__ __forceinline__ float rcp_ftz(float x)
 // end in, subnormal ones too, is the value it stands for times a power of two, which goes
 // into beta's factor; a value times a power of two has its code in those bits, with the
 // lost part below. Both hold for block exponents that such powers of two fit; other
-// rows (and NaN) return false with nothing written. The denominator is formed times 2^32,
-// so that no v but 0 counts as zero.
-constexpr int MOST_M = 140, MOST_V = 156;
+// rows (and NaN) return false with nothing written.
 template <bool PB, bool MASTER, bool GB>
 __device__ __forceinline__ bool row_of_8_bits(const Item& it, int64_t at, const Raw& p, const Raw& g, uint32_t mw, uint32_t vw,
                                               uchar2 scales, const Rates& s, float keep, uint32_t key)
@@ -327,7 +348,6 @@ __device__ __forceinline__ bool row_of_8_bits(const Item& it, int64_t at, const 
     const int em = max((int)scales.x, LEAST_EXPONENT), ev = max((int)scales.y, LEAST_EXPONENT);
     if (em > MOST_M || ev > MOST_V) return false;
     const float fm = s.beta1 * power_of_two(em - 14 + 127), fv = s.beta2 * power_of_two(ev - 30 + 127);
-    const float root = s.correct2 * 0x1p64f, eps = s.eps * 0x1p32f, rate = s.rate * -0x1p32f;
     float x[4], dx[4], m[4], v[4];
     floats(p, PB && !MASTER, x);
     floats(g, GB, dx);
@@ -338,7 +358,7 @@ __device__ __forceinline__ bool row_of_8_bits(const Item& it, int64_t at, const 
         const float vo = __uint_as_float((j < 3 ? vw << (20 - 8 * j) : vw >> 4) & 0x0FF00000u);
         m[j] = __fadd_rn(__fmul_rn(mo, fm), __fmul_rn(s.rest1, d));
         v[j] = __fadd_rn(__fmul_rn(vo, fv), __fmul_rn(__fmul_rn(s.rest2, d), d));
-        x[j] = fmaf(x[j], keep, rate * m[j] * rcp_ftz(sqrt_ftz(v[j] * root) + eps));
+        x[j] = updated_scaled(x[j], keep, m[j], v[j], s);
     }
     const float mt = max_nan(max_nan(fabsf(m[0]), fabsf(m[1])), max_nan(fabsf(m[2]), fabsf(m[3])));
     const float vt = max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3]));
@@ -388,7 +408,7 @@ __device__ __forceinline__ void row_of_32_bits(const Item& it, int64_t at, const
         const float d = dx[j] * s.clip;
         m[j] = fmaf(s.beta1, m[j], s.rest1 * d);
         v[j] = fmaf(s.beta2, v[j], s.rest2 * d * d);
-        x[j] = fmaf(x[j], keep, -s.rate * __fdividef(m[j], sqrt_fast(v[j] * s.correct2) + s.eps));
+        x[j] = updated(x[j], keep, m[j], v[j], s);
         if (PB) b[j] = MASTER ? round_bf16(x[j]) : round_bf16_at_random(x[j], pcg(pcg((uint32_t)at + (uint32_t)j + key)) & 0xFFFFu);
     }
     if (MASTER) store_f32(it.master, at, 4, true, x);

@@ -517,3 +517,21 @@ def test_tensors_that_are_not_what_the_group_was_built_over():
         group.masters[0] = None
         group.step(grads[:2], lr=lr)
         assert torch.equal(copy, kept) and int(group.steps) == 1
+
+
+@pytest.mark.parametrize("size", [1.0, 1e-12, 1e10])
+@pytest.mark.parametrize("param", ["f32", "bf16", "master"])
+@pytest.mark.parametrize("states", [32, 8])
+def test_a_step_does_not_depend_on_the_place_in_memory(states, param, size):
+    """Tensors that can be read in vectors and not, bit for bit, whichever form of the quotient their blocks take."""
+    def run(shift):
+        dtype = F32 if param == "f32" else BF16
+        group = rtp.AdamWGroup(_tensors([1, 130, 5000], dtype, None, 80, shift=shift), lr=LR, betas=BETAS, weight_decay=DECAY,
+                               states=states, seed=SEED, masters=True if param == "master" else None)
+        for t in range(3):
+            grads = _tensors([1, 130, 5000], F32, None, 81 + t, 1e-3, shift)
+            for g in grads[1:]:
+                g[100:200] *= size
+            group.step(grads)
+        return [*group.params, *(m for m in group.masters if m is not None), *group.moments()]
+    assert all(torch.equal(a, b) for a, b in zip(run(0), run(1)))
