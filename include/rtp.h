@@ -707,7 +707,7 @@ typedef struct {
     uint8_t* scales;
     int32_t param_dtype, grad_dtype;
     float weight_decay;
-    int32_t reserved;
+    int32_t noise; /* 0: the random bits go by the tensor's place among the n; k > 0: as at place k - 1 */
 } rtp_adamw_tensor;
 
 enum { RTP_ADAMW_BLOCK = 128, RTP_ADAMW_CLOCK_BYTES = 128 };
@@ -720,14 +720,15 @@ enum { RTP_ADAMW_BLOCK = 128, RTP_ADAMW_CLOCK_BYTES = 128 };
  *             held to 2^-100 at least; a block with an infinity or a NaN becomes NaN
  *   lr        the learning rate; lr_at: NULL, or a device pointer that it is read from
  *   norm      NULL (no clipping), or the device pointer of a norm (rtp_grad_norm)
- *   seed      of the random bits, a hash of seed, the tensor's place among the n, the step
- *             and the element: a step is reproducible bit for bit
+ *   seed      of the random bits, a hash of seed, the tensor's place among the n (or its
+ *             noise), the step and the element: a step is reproducible bit for bit. Replicas
+ *             of one piece need the same noise: rounded apart, they would drift apart
  *   clock     RTP_ADAMW_CLOCK_BYTES of device memory, 16-byte aligned, set by
  *             rtp_adamw_clock; its first 8 bytes are the steps done (int64). Every call
  *             counts on by one, so that a captured step does so with each replay. Not shared
  *             by calls that may overlap
  * The quotient is within 2^-20 of itself. tensors[] is read before the call returns. lr,
- * eps, max_norm and weight decays must be numbers >= 0 (RTP_EINVAL).
+ * eps, max_norm, weight decays and noise must be numbers >= 0 (RTP_EINVAL).
  */
 int rtp_adamw_step(int n, const rtp_adamw_tensor* tensors, int bits, float lr, const float* lr_at, float eps, const float* norm,
                    float max_norm, uint32_t seed, void* clock, rtp_stream stream);

@@ -84,7 +84,7 @@ class AdamWTensor(ctypes.Structure):
         ("param_dtype", ctypes.c_int32),
         ("grad_dtype", ctypes.c_int32),
         ("weight_decay", ctypes.c_float),
-        ("reserved", ctypes.c_int32),
+        ("noise", ctypes.c_int32),
     ]
 
 
@@ -1230,7 +1230,9 @@ class AdamWGroup:
     weight_decay: one for all, or one per tensor. masters: float32 copies that bf16 weights are updated through, one per
     tensor (None for a tensor without), or True for copies that the group makes and holds in its state; a bf16 weight without
     one is rounded at random, so that small steps are not lost. states: bits of the moments, 32 or 8 (blocks of 128 elements share a power of
-    two, values are rounded at random; see rtp_adamw_step in rtp.h). seed: of the random bits.
+    two, values are rounded at random; see rtp_adamw_step in rtp.h). seed: of the random bits. noise: a whole number >= 0 per
+    tensor, by which its random bits go instead of its place; replicas (the rank pieces of a Broadcast weight) need the same
+    one, and then stay alike, or rounding at random lets them drift apart.
 
     The group keeps the tensors and, in one flat buffer each, the moments (exp_avg, exp_avg_sq: float32, or codes with
     `scales`), tensor i in [offsets[i], offsets[i] + numel), a multiple of 128 from the start. The steps done are counted
@@ -1239,7 +1241,7 @@ class AdamWGroup:
     stream)."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=1e-2, masters=None,
-                 states: int = 32, seed: int = 0, stream=None):
+                 states: int = 32, seed: int = 0, stream=None, noise=None):
         torch = _torch()
         fn = "AdamWGroup"
         self.params = list(params)
@@ -1256,6 +1258,9 @@ class AdamWGroup:
         if len(decay) != n:
             raise RtpError(-1, "%s: %d weight decays for %d tensors" % (fn, len(decay), n))
         self._decay = [float(d) for d in decay]
+        self._noise = list(range(n)) if noise is None else [int(k) for k in noise]
+        if len(self._noise) != n or any(not 0 <= k < 2 ** 31 - 1 for k in self._noise):
+            raise RtpError(-1, "%s: noise must be a whole number >= 0 (below 2^31 - 1) for each of %d tensors" % (fn, n))
         for i, p in enumerate(self.params):
             self._check(fn, "params", i, p)
         with _allocating_on(stream):
@@ -1341,6 +1346,7 @@ class AdamWGroup:
             at = self.offsets[i]
             t.numel, t.param, t.param_dtype, t.weight_decay = p.numel(), p.data_ptr() or None, _dtype_code(p), self._decay[i]
             t.master = None if m is None else m.data_ptr() or None
+            t.noise = self._noise[i] + 1
             t.exp_avg, t.exp_avg_sq = self.exp_avg.data_ptr() + at * size, self.exp_avg_sq.data_ptr() + at * size
             if self.states == 8:
                 t.scales = self.scales.data_ptr() + at // ADAMW_BLOCK * 2

@@ -27,7 +27,8 @@
 // (rounding to nearest would leave v as it is: a step changes it by 1 - b2, less than
 // half a spacing). A bf16 weight without a float32 copy is rounded the same way, or small
 // steps would be lost. The bits are a hash of seed, tensor, step and element: a step is
-// reproducible bit for bit. The update itself uses m and v before they are rounded. They are
+// reproducible bit for bit (replicas of a tensor are given the same number instead of their
+// places, and stay alike). The update itself uses m and v before they are rounded. They are
 // formed by single float32 operations (no fused ones), so that any float32 program gets
 // the same codes.
 #include <cuda_bf16.h>
@@ -57,7 +58,7 @@ struct Item {
     int64_t numel;
     uint32_t chunk0;  // first chunk
     float decay;
-    uint32_t id;
+    uint32_t id;  // of its random bits
     uint8_t param_bf16, grad_bf16, vectors, unused;
 };
 template <int N>
@@ -756,6 +757,7 @@ int step_impl(const char* fn, int n, const rtp_adamw_tensor* tensors, int bits, 
             return fail(RTP_EINVAL, "%s: tensor %d is of an unknown type", fn, i);
         if (w.numel < 0 || w.numel >= (int64_t)1 << 39) return fail(RTP_ESHAPE, "%s: tensor %d has %lld elements", fn, i, (long long)w.numel);
         if (!(w.weight_decay >= 0.0f)) return fail(RTP_EINVAL, "%s: weight decay %g of tensor %d is not a number >= 0", fn, (double)w.weight_decay, i);
+        if (w.noise < 0) return fail(RTP_EINVAL, "%s: noise %d of tensor %d is below 0", fn, w.noise, i);
         if (w.numel == 0) continue;
         const bool pb = w.param_dtype == RTP_BF16, gb = w.grad_dtype == RTP_BF16;
         if (!w.param || !w.grad || !w.exp_avg || !w.exp_avg_sq || (bits == 8 && !w.scales))
@@ -768,7 +770,7 @@ int step_impl(const char* fn, int n, const rtp_adamw_tensor* tensors, int bits, 
         if ((f32s & 3u) || (b16s & 1u) || (bits == 8 && ((uintptr_t)w.scales & 1u)))
             return fail(RTP_EINVAL, "%s: a buffer of tensor %d is not aligned to its elements", fn, i);
         Item it = {w.param, w.grad, w.master, w.exp_avg, w.exp_avg_sq, reinterpret_cast<uchar2*>(w.scales), w.numel, 0u,
-                   w.weight_decay, (uint32_t)i, pb, gb, (uint8_t)(!(f32s & 15u) && !(b16s & 7u) && !(b8s & 3u)), 0};
+                   w.weight_decay, (uint32_t)(w.noise ? w.noise - 1 : i), pb, gb, (uint8_t)(!(f32s & 15u) && !(b16s & 7u) && !(b8s & 3u)), 0};
         items.push_back(it);
         elements += (uint64_t)w.numel;
         const uintptr_t p = (uintptr_t)w.param;

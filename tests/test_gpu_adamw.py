@@ -535,3 +535,40 @@ def test_a_step_does_not_depend_on_the_place_in_memory(states, param, size):
             group.step(grads)
         return [*group.params, *(m for m in group.masters if m is not None), *group.moments()]
     assert all(torch.equal(a, b) for a, b in zip(run(0), run(1)))
+
+
+@pytest.mark.parametrize("param", ["f32", "bf16", "master"])
+@pytest.mark.parametrize("states", [32, 8])
+@pytest.mark.parametrize("numel", [100, 5000])
+def test_replicas_stay_alike(states, param, numel):
+    """Pieces that hold the same (one of them elsewhere in its vectors) and are given the same noise do so after any number of
+    steps; with another number they are rounded another way."""
+    dtype = F32 if param == "f32" else BF16
+    make = lambda kind, seed, std: [_tensors([numel], kind, None, seed, std, shift)[0] for shift in (0, 1, 0)]
+    group = rtp.AdamWGroup(make(dtype, 30, 1.0), lr=LR, betas=BETAS, weight_decay=DECAY, states=states, seed=SEED,
+                           masters=True if param == "master" else None, noise=[4, 4, 1])
+    for t in range(4):
+        group.step(make(F32, 31 + t, 1e-2))
+    first, same, other = (torch.cat([x.double().reshape(-1) for x in (p, *_moments(group, i))] +
+                                    ([] if group.masters[i] is None else [group.masters[i].double()]))
+                          for i, p in enumerate(group.params))
+    assert torch.equal(first, same)
+    assert torch.equal(first, other) == (states == 32 and param != "bf16")
+
+
+@pytest.mark.parametrize("states", [32, 8])
+def test_noise_is_the_tensors_place_by_default(states):
+    def run(noise):
+        group = rtp.AdamWGroup(_tensors([300, 40], BF16, None, 40), lr=LR, states=states, seed=SEED, noise=noise)
+        group.step(_tensors([300, 40], F32, None, 41))
+        return [*group.params, *group.moments()]
+    a, b, c = run(None), run([0, 1]), run([1, 0])
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and not torch.equal(a[0], c[0])
+
+
+def test_noise_that_is_refused():
+    p = [torch.zeros(8, device="cuda"), torch.zeros(8, device="cuda")]
+    for noise in ([0], [0, 1, 2], [0, -1], [0, 2 ** 31 - 1]):
+        with pytest.raises(rtp.RtpError):
+            rtp.AdamWGroup(p, noise=noise)
+    rtp.AdamWGroup(p, noise=[0, 2 ** 31 - 2]).step([torch.zeros_like(t) for t in p])

@@ -142,3 +142,11 @@ def test_workspace_of_a_piece_of_more_rows_than_there_are(M):
         assert want[0] == 0
         for piece in (M + 1, 1 << 31, (1 << 63) - 300, (1 << 63) - 1):
             assert size(piece, dw) == want, piece
+
+
+def test_noise_below_zero():
+    t = (rtp.AdamWTensor * 1)()
+    t[0].numel, t[0].param, t[0].grad, t[0].exp_avg, t[0].exp_avg_sq = 4, 0x1000, 0x2000, 0x3000, 0x4000
+    t[0].noise = -1
+    assert rtp.lib().rtp_adamw_step(1, t, 32, 0.1, None, 1e-8, None, 1.0, 0, 0x10000, None) == EINVAL
+    assert "noise" in rtp.last_error()
