@@ -75,24 +75,32 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             cmd.insert(1, "-Xptxas=-v")
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         objs.append(obj)
-    table_tmp = TABLE + ".tmp%d" % os.getpid()
-    cmd = _table_command(table_tmp)
-    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    failed = []
-    for cmd, p in procs:
-        out, _ = p.communicate()
-        text = out.decode(errors="replace")
-        if p.returncode != 0:
-            failed.append((cmd, text))
-        elif verbose and text.strip():
-            sys.stderr.write(text)
-    if failed:
-        msg = "\n".join(" ".join(c) + "\n" + t for c, t in failed)
-        raise RuntimeError("librtp build failed:\n" + msg)
-    tmp = LIB + ".tmp%d" % os.getpid()
-    subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
-    os.replace(tmp, LIB)
-    os.replace(table_tmp, TABLE)
+    table_tmp, tmp = (f + ".tmp%d" % os.getpid() for f in (TABLE, LIB))
+    try:
+        cmd = _table_command(table_tmp)
+        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+        failed = []
+        for cmd, p in procs:
+            out, _ = p.communicate()
+            text = out.decode(errors="replace")
+            if p.returncode != 0:
+                failed.append((cmd, text))
+            elif verbose and text.strip():
+                sys.stderr.write(text)
+        if failed:
+            msg = "\n".join(" ".join(c) + "\n" + t for c, t in failed)
+            raise RuntimeError("librtp build failed:\n" + msg)
+        subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
+        os.replace(tmp, LIB)
+        os.replace(table_tmp, TABLE)
+    finally:  # a build that failed or was interrupted leaves neither compilers nor files behind
+        for _, p in procs:
+            if p.poll() is None:
+                p.kill()
+            p.wait()
+        for f in (table_tmp, tmp):
+            if os.path.exists(f):
+                os.remove(f)
     return LIB
 
 
