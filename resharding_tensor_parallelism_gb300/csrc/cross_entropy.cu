@@ -337,19 +337,20 @@ int64_t rank_columns(const Shape& s, int i) { return std::max<int64_t>(0, std::m
 // (0: none, all ranks in one accumulator). dX of few rows and a narrow model has few tiles,
 // each the product of the whole vocabulary, which a cluster shares four ways at most:
 // 256 x 512 from 8192 columns took 20 us on 8 of 76 pairs. K blocks take 0.28 us of a
-// pair, the sum 5 us.
+// pair, the sum 5 us. Workspaces are sized without a device, so the rule is one for these
+// SLICE_PAIRS; a device with fewer SMs, where its slices would not run side by side, takes none.
+constexpr int SLICE_PAIRS = 76;
 int64_t slice_columns(const Shape& s, int n) { return up((s.Vp + n - 1) / n, 64); }
 int dx_slices(const Shape& s, int64_t rows)
 {
-    constexpr int PAIRS = 76;
     if (rows <= 0) return 0;
     const int64_t tiles = ((rows + LIN_TILE_ROWS - 1) / LIN_TILE_ROWS) * ((s.K + LIN_TILE_COLS - 1) / LIN_TILE_COLS);
     const int64_t kbs = s.P * ((s.Vp + 63) / 64);
-    const double one = 0.28 * (double)kbs / (double)std::min<int64_t>(4, std::max<int64_t>(1, PAIRS / tiles));
+    const double one = 0.28 * (double)kbs / (double)std::min<int64_t>(4, std::max<int64_t>(1, SLICE_PAIRS / tiles));
     int best = 1;
     double least = one;
     for (int n = 1; n <= LIN_MAX_GROUPS / s.P; ++n) {
-        const int64_t parts = tiles * s.P * n, split = std::min<int64_t>(4, PAIRS / parts), kdim = slice_columns(s, n);
+        const int64_t parts = tiles * s.P * n, split = std::min<int64_t>(4, SLICE_PAIRS / parts), kdim = slice_columns(s, n);
         if (s.P * n < 2 || split < 1 || kdim < 512 || (n - 1) * kdim >= s.Vp) continue;
         const double t = 0.28 * (double)(kdim / 64) / (double)split + 5.0;
         if (t < 0.9 * least) least = t, best = n;
@@ -572,7 +573,7 @@ int train_impl(Call& c, int targets64, int64_t workspace_bytes, const float* wei
         a.loss = loss + first;
         a.shared = sh;
         TRY(launch(fn, loss_rows_kernel<true>, dim3((unsigned)rows), THREADS, stream, a));
-        const int slices = dx_slices(s, rows);
+        const int slices = sms >= 2 * SLICE_PAIRS ? dx_slices(s, rows) : 0;
         if (dX && slices) {
             LinGemm g;
             g.groups = 0;
