@@ -37,6 +37,7 @@
 #include <algorithm>
 #include <vector>
 
+#include "launch.cuh"
 #include "rtp_internal.h"
 
 namespace rtp {
@@ -675,22 +676,6 @@ __global__ void __launch_bounds__(THREADS) adamw_values_kernel(const uint2* m8, 
 }
 
 // ---- host side --------------------------------------------------------------------
-
-template <class... A, class... B>
-int launch(const char* fn, void (*kernel)(A...), unsigned grid, int threads, cudaStream_t stream, B... args)
-{
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    return e == cudaSuccess ? RTP_OK : fail(RTP_ECUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
-}
 
 // Table by table, in chunks of `chunk` elements. The step's clock moves on with the last
 // one, which runs (on one block) even when there is nothing to update.

@@ -27,6 +27,7 @@
 #include <algorithm>
 #include <cstring>
 
+#include "launch.cuh"
 #include "linear.h"
 #include "softmax.cuh"
 #include "tcgen05.cuh"
@@ -290,30 +291,6 @@ __global__ void __launch_bounds__(THREADS) round_kernel(const __grid_constant__ 
 }
 
 // ---- host side --------------------------------------------------------------------
-
-#define TRY(call)          \
-    do {                   \
-        int st_ = (call);  \
-        if (st_) return st_; \
-    } while (0)
-
-// A launch that may be set up while the stream's previous kernel still runs (every
-// kernel here waits for it before it touches memory).
-template <class... A, class... B>
-int launch(const char* fn, void (*kernel)(A...), dim3 grid, int threads, cudaStream_t stream, B... args)
-{
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    return e == cudaSuccess ? RTP_OK : fail(RTP_ECUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
-}
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 

@@ -178,12 +178,6 @@ int forward(const char* fn, const LinGemm& p, bool weights_ready, cudaStream_t s
     return st ? st : launch_linear_few(fn, rows_from(p, top.rows), true, stream);
 }
 
-#define TRY(call)          \
-    do {                   \
-        int st_ = (call);  \
-        if (st_) return st_; \
-    } while (0)
-
 int check_common(const char* fn, int P, int64_t M, int64_t a, int64_t b, int act)
 {
     if (P < 1 || P > LIN_MAX_RANKS) return fail(RTP_EUNSUPPORTED, "%s: P = %d outside [1, %d]", fn, P, LIN_MAX_RANKS);

@@ -16,6 +16,13 @@ namespace rtp {
 int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 void clear_error();
 
+// Returns from the function with a status that is not RTP_OK.
+#define TRY(call)          \
+    do {                   \
+        int st_ = (call);  \
+        if (st_) return st_; \
+    } while (0)
+
 // Runs the body of an entry point that allocates host memory: a failed
 // allocation (std::bad_alloc) becomes RTP_ENOMEM, and no exception crosses the
 // C ABI.
