@@ -378,7 +378,7 @@ __device__ __forceinline__ bool row_of_8_bits(const Item& it, int64_t at, const 
         const uint32_t w = ((h >> ((h >> 28) + 4u)) ^ h) * 277803737u, noise = (w >> 22) ^ w;
         // the random 16 bits, and half of the next one, 4 bits up as the codes
         const uint32_t rm = __byte_perm(noise, 0x80u, 0x5104), rv = __byte_perm(noise, 0x80u, 0x5324);
-        // (A funnel shift: CUDA 13.0's assembler takes a plain shift of these bits, or 16 times them, for 0.)
+        // (A funnel shift: with a plain shift of these bits, or 16 times them, this kernel's codes came out as 0.)
         mc[j] = (__funnelshift_l(0u, __float_as_uint(fabsf(m[j]) * sm), 4) + rm) | (__float_as_uint(m[j]) & 0x80000000u);
         vc[j] = __funnelshift_l(0u, __float_as_uint(v[j] * sv), 4) + rv;
         if (v[j] > 0.0f) vc[j] = max(vc[j], 1u << 24);

@@ -32,12 +32,12 @@ struct SoftmaxArgs {
 // Whether exponentials relative to 0 with this sum are kept (not a NaN sum).
 __device__ __forceinline__ bool in_range(float sum) { return sum >= 0x1p-64f && sum <= 0x1p64f; }
 
-// The target of a row, counted from column `first` of the vocabulary; -1: not in the
-// `cols` columns from there.
+// The target of a row, counted over the whole vocabulary.
 __device__ __forceinline__ int64_t target_at(const void* targets, int wide, int64_t row)
 {
     return wide ? __ldcg(static_cast<const long long*>(targets) + row) : (int64_t)__ldcg(static_cast<const int*>(targets) + row);
 }
+// The same, counted from column `first`; -1: not in the `cols` columns from there.
 __device__ __forceinline__ int target_in(const SoftmaxArgs& a, int64_t row, int64_t first, int cols)
 {
     const int64_t t = target_at(a.targets, a.targets64, row) - first;

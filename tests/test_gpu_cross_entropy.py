@@ -423,3 +423,16 @@ def test_rows_do_not_meet(M, K, V, P, piece, far):
         assert torch.equal(a[keep], b[keep]) and not torch.equal(a, b)
     for a, b in zip(*(rtp.tp_cross_entropy(x, shards, y, ignore_index=IGNORE) for x, y in ((X, t), (Y, u)))):
         assert torch.equal(a[keep], b[keep]) and not torch.equal(a, b)
+
+
+@pytest.mark.parametrize("P", [1, 3])
+def test_far_rows_in_many_tiles(P):
+    """Several tiles for every pair of SMs, some of whose rows are gone through once more relative to their largest logit."""
+    M, V = 1300, 24 * 1016
+    X, W, _, t = _inputs(M, 64, V, P, V - 5, seed=24)
+    X[5::7] *= 200
+    W[:, 3000:9000] *= 4
+    shards = [w.contiguous() for w in W.chunk(P, 1)]
+    loss, lse = rtp.tp_cross_entropy(X, shards, t, vocab=V - 5, ignore_index=IGNORE)
+    _check_forward(X, W, t, V - 5, loss, lse)
+    _check_train(X, W, t, V - 5, rtp.tp_cross_entropy_train(X, shards, t, vocab=V - 5, ignore_index=IGNORE))
