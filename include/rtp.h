@@ -628,7 +628,7 @@ int64_t rtp_grad_workspace_bytes(int n);
  *   loss_r = lse_r - l_{r,t_r}
  *   X         bf16 [M, K];  W_shards: P bf16 [K, V/P]
  *   vocab     columns from here on (counted over the ranks) are padding that takes no
- *             part; in [1, V]
+ *             part, whatever the weights hold there; in [1, V]
  *   targets   [M] int64 (targets64 = 1) or int32 (0) on the device, counted over the ranks
  *   ignore_index  rows with this target have a loss of 0. A target outside [0, vocab) that
  *             is not ignore_index gives a NaN loss (the host does not see targets)
@@ -659,7 +659,7 @@ int rtp_tp_cross_entropy(int P, int64_t M, int64_t K, int64_t V, int64_t vocab, 
  *   dX        [M, K] by dx_dtype, or NULL;  dW: P [K, V/P] by dw_dtype, or NULL
  *   accumulate 1: the products are added to the float32 dW that is there (several
  *             micro-batches); subnormal values count as zero in such a sum
- *   piece_rows rows that are taken at once (rounded up to 256): the workspace holds 2 V
+ *   piece_rows rows that are taken at once (rounded up to 256; at most M): the workspace holds 2 V
  *             bytes for each; 0: as many as keep that within the float32 sums of dW that
  *             several pieces need (2 K rows, at least 2048), or within 1 GiB
  * The products read bf16: the exponentials, of a row relative to the same number (at the
